@@ -5,7 +5,9 @@ of ``include/bt.h``). This module only marshals torch tensors (device memory) an
 current HIP stream into those calls; every step of the path runs in the library's
 kernels. Names follow the C ABI: ``pack_weights``, ``quant_act``, ``ternary_gemv``,
 ``ternary_gemm`` (+ ``unpack_weights``, ``linear``, and ``pack_weights_rows`` for
-row-group weight scales, which the product calls then take in place of one scale).
+row-group weight scales, which the product calls then take in place of one scale), and the
+attention block around the products: ``lora_apply`` (also through ``linear``) and
+``qk_norm_rope``.
 """
 from __future__ import annotations
 
@@ -24,7 +26,9 @@ from .api import (
     GEMV_MAX_M,
     GEMV_MFMA,
     GEMV_STAGED,
+    LORA_MAX_RANK,
     STATIC_SCRATCH_BYTES,
+    LoraAdapters,
     PackedWeight,
     act_row_bytes,
     binarize_act,
@@ -36,12 +40,17 @@ from .api import (
     linear,
     linear_static,
     linear_workspace_bytes,
+    lora_apply,
+    lora_workspace,
+    lora_workspace_bytes,
     pack_weights,
     pack_weights_binary,
     pack_weights_rows,
     pack_workspace_bytes,
     packed_weight_bytes,
+    qk_norm_rope,
     quant_act,
+    rope_frequencies,
     ternary_gemm,
     ternary_gemv,
     ternary_gemv_a1,
@@ -53,4 +62,6 @@ __all__ = [
     "BTError", "lib", "GEMV_AUTO", "GEMV_DOT4", "GEMV_LUT", "GEMV_MFMA", "GEMV_STAGED", "GEMV_MAX_M", "PackedWeight", "act_row_bytes",
     "gemm_split_plan", "gemm_workspace", "gemm_workspace_bytes", "linear", "linear_workspace_bytes", "pack_weights", "pack_weights_rows", "pack_workspace_bytes", "packed_weight_bytes", "quant_act", "ternary_gemm",
     "ternary_gemv", "unpack_weights", "kernel_plan", "CALL_LINEAR", "CALL_GEMV", "CALL_GEMM", "CALL_GEMM_WS", "CALL_QUANT", "linear_static", "STATIC_SCRATCH_BYTES",
+    "LORA_MAX_RANK", "LoraAdapters", "lora_apply", "lora_workspace", "lora_workspace_bytes", "qk_norm_rope",
+    "rope_frequencies",
 ]

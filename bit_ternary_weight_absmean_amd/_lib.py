@@ -37,6 +37,11 @@ SIGNATURES = {
     "bt_binary_gemv": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "bt_ternary_gemv_a1": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "bt_kernel_plan": (_i32, [_i32, _i64, _i64, _i64, _i32, _i32, ctypes.c_char_p, _sz]),
+    "bt_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "bt_lora_apply": (_i32, [_vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
+                             _vp]),
+    "bt_qk_norm_rope": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _i64, _i32,
+                               _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp]),
     "bt_status_str": (ctypes.c_char_p, [_i32]),
     "bt_last_error": (ctypes.c_char_p, []),
 }

@@ -249,13 +249,23 @@ def linear_workspace_bytes(M: int, N: int, K: int) -> int:
 
 
 def linear(X: torch.Tensor, pw: PackedWeight, want_y=True, want_acc=False, out_y=None, out_acc=None,
-           workspace: torch.Tensor | None = None):
+           workspace: torch.Tensor | None = None, adapters: LoraAdapters | None = None,
+           adapter_index: torch.Tensor | None = None):
     """bt_ternary_linear: fp32 X [M,K] in, (Y [M,N] fp32, acc [M,N] int32) out.
 
-    One fused launch for decode-sized M; quantize + GEMV/GEMM otherwise.
+    One fused launch for decode-sized M; quantize + GEMV/GEMM otherwise. With ``adapters`` and
+    ``adapter_index`` [M] int32, Y also receives each token's low-rank product (lora_apply, of
+    the unquantized X); acc stays the shared product's.
     """
     pw.check()
     dev = pw.data.device
+    if (adapters is None) != (adapter_index is None):
+        raise ValueError("adapters and adapter_index come together")
+    if adapters is not None:
+        if (adapters.N, adapters.K) != (pw.N, pw.K):
+            raise ValueError(f"the adapters are for {adapters.N} x {adapters.K}, the weights are {pw.N} x {pw.K}")
+        if out_y is None and not want_y:
+            raise ValueError("adapters are added to Y: want_y or out_y is needed")
     if X.dim() != 2:
         raise ValueError(f"X must be [M, K], got shape {tuple(X.shape)}")
     _need(X, "X", torch.float32, device=dev)
@@ -268,9 +278,14 @@ def linear(X: torch.Tensor, pw: PackedWeight, want_y=True, want_acc=False, out_y
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     elif ws_bytes:
         _need_bytes(workspace, "workspace", ws_bytes, dev)
+    if adapters is not None:
+        _need(adapters.B, "adapters", adapters.B.dtype, None, dev)
+        _need(adapter_index, "adapter_index", torch.int32, (M,), dev)
     fn = lib().bt_ternary_linear_rs if pw.row_scales else lib().bt_ternary_linear
     check(fn(_ptr(pw.data), _ptr(pw.scale), _ptr(X), M, pw.N, K, _ptr(Y), _ptr(acc),
              _ptr(workspace) if ws_bytes else 0, _stream(dev)))
+    if adapters is not None:
+        lora_apply(X, adapters, adapter_index, base=Y, out=Y)
     return Y, acc
 
 
@@ -367,3 +382,198 @@ def binary_gemv(pw: PackedWeight, b, want_y=True, want_acc=False, out_y=None, ou
 def ternary_gemv_a1(pw: PackedWeight, b, want_y=True, want_acc=False, out_y=None, out_acc=None):
     """bt_ternary_gemv_a1 (W1.58A1): ``pw`` from pack_weights, ``b`` from binarize_act(X, BITS_CODES)."""
     return _bits_product("bt_ternary_gemv_a1", pw, b, BITS_CODES, want_y, want_acc, out_y, out_acc)
+
+
+# ------------------------------------------------- the attention block around the products
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # BT_F32, BT_BF16, BT_F16
+
+
+def _type_of(t, name: str, allowed) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in allowed:
+        raise TypeError(f"{name} must be one of {[str(a) for a in allowed]}, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _need_strided(t, name: str, dtype, shape, device, output: bool = False):
+    """A device tensor of the given shape whose last dimension is contiguous; as an output, one whose
+    elements do not share memory."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not _on_device(t):
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.is_contiguous():
+        return
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if output and t.numel():
+        span = 1
+        for step, n in sorted((t.stride(d), t.shape[d]) for d in range(t.dim()) if t.shape[d] > 1):
+            if step < span:
+                raise ValueError(f"{name} is an output and must not overlap itself")
+            span = step * (n - 1) + span
+
+
+def _call(dev, fn, *args):
+    """A library call on ``dev``'s current stream; ``dev`` need not be the current device."""
+    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        check(fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, _stream(dev)))
+
+
+LORA_MAX_RANK = 256  # BT_LORA_MAX_RANK
+
+
+@dataclass(frozen=True)
+class LoraAdapters:
+    """Low-rank adapters of one projection: ``A`` [L, groups * R, K] and ``B`` [L, N, R] (bf16, fp16 or
+    fp32), ``scale`` [L] fp32, optionally the ``ranks`` [L] int32 in use and, for a fused projection, the
+    ``group_rows`` (rows of each group, summing to N; every group has its own R rows of A)."""
+
+    A: torch.Tensor
+    B: torch.Tensor
+    scale: torch.Tensor
+    ranks: torch.Tensor | None = None
+    group_rows: tuple | None = None
+
+    def __post_init__(self):
+        for t, name in ((self.A, "A"), (self.B, "B")):
+            _type_of(t, name, _TYPES)
+            if t.dim() != 3:
+                raise ValueError(f"{name} must have three dimensions, got shape {tuple(t.shape)}")
+        L, N, R = self.B.shape
+        groups = 1
+        if self.group_rows is not None:
+            object.__setattr__(self, "group_rows", tuple(int(r) for r in self.group_rows))
+            groups = len(self.group_rows)
+            if not 1 <= groups <= 8 or min(self.group_rows) < 1 or sum(self.group_rows) != N:
+                raise ValueError(f"group_rows {self.group_rows} must be 1 to 8 positive counts that sum to N = {N}")
+        if not 1 <= R <= LORA_MAX_RANK:
+            raise ValueError(f"the rank must be 1 to {LORA_MAX_RANK}, got {R}")
+        dev = self.B.device
+        _need(self.B, "B", self.B.dtype)
+        _need(self.A, "A", self.B.dtype, (L, groups * R, self.A.shape[2]), dev)
+        _need(self.scale, "scale", torch.float32, (L,), dev)
+        if self.ranks is not None:
+            _need(self.ranks, "ranks", torch.int32, (L,), dev)
+        arr = None if self.group_rows is None else (ctypes.c_int64 * groups)(*self.group_rows)
+        object.__setattr__(self, "_groups", (arr, groups))
+
+    @property
+    def K(self) -> int:
+        return self.A.shape[2]
+
+    @property
+    def N(self) -> int:
+        return self.B.shape[1]
+
+    @property
+    def rank(self) -> int:
+        return self.B.shape[2]
+
+
+def lora_workspace_bytes(M: int, adapters: LoraAdapters) -> int:
+    """bt_lora_workspace_bytes for M tokens."""
+    return int(lib().bt_lora_workspace_bytes(M, adapters.K, adapters.rank, adapters._groups[1]))
+
+
+def lora_workspace(M: int, adapters: LoraAdapters) -> torch.Tensor:
+    """A workspace for lora_apply with M tokens (its contents do not matter)."""
+    return torch.empty(max(lora_workspace_bytes(M, adapters), 256), dtype=torch.uint8, device=adapters.B.device)
+
+
+def lora_apply(X: torch.Tensor, adapters: LoraAdapters, index: torch.Tensor, base: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bt_lora_apply: ``base`` (None: zeros) plus each token's low-rank product. ``index`` [M] int32 names
+    the token's adapter (outside [0, L): none). ``out`` may be ``base``. Returns out [M, N] fp32."""
+    B = adapters.B
+    dev = B.device
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a tensor [M, K]")
+    M, (L, N, R), K = X.shape[0], B.shape, adapters.A.shape[2]
+    _need(X, "X", torch.float32, (M, K), dev)
+    _need(index, "index", torch.int32, (M,), dev)
+    if base is not None:
+        _need(base, "base", torch.float32, (M, N), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", torch.float32, (M, N), dev)
+    arr, groups = adapters._groups
+    need = int(lib().bt_lora_workspace_bytes(M, K, R, groups))
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    else:
+        _need_bytes(workspace, "workspace", need, dev)
+    _call(dev, lib().bt_lora_apply, _ptr(adapters.A), _ptr(B), _TYPES[B.dtype], _ptr(adapters.scale),
+          _ptr(adapters.ranks), L, R, None if arr is None else ctypes.addressof(arr), groups, _ptr(index), _ptr(X),
+          _ptr(base), M, N, K, _ptr(out), _ptr(workspace))
+    return out
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The usual fp64 angles per position of qk_norm_rope: base ** (-2 p / rot_dim), p < rot_dim / 2."""
+    p = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+    return float(base) ** (-2.0 * p / rot_dim)
+
+
+def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, inv_freq: torch.Tensor | None, heads: int,
+                 kv_heads: int, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                 eps: float = 1e-6, interleaved: bool = False, rows: torch.Tensor | None = None, out=None,
+                 dtype: torch.dtype = torch.bfloat16):
+    """bt_qk_norm_rope: per-head norms and position rotation of the Q and K heads of fused QKV rows
+    ``qkv`` [M, (heads + 2 kv_heads) * D], and the conversion of Q, K and V to the attention's type.
+
+    ``inv_freq`` [rot_dim / 2] fp64 (None: no rotation) gives the rotated part of the heads. ``out`` =
+    (q [M, heads, D], k, v) of one type, rows and heads at any stride; k and v are [M, kv_heads, D], or
+    caches [any, kv_heads, D] with ``rows`` [M] int32 naming each token's row (outside: not written).
+    Without ``out``, new tensors of ``dtype``. Returns (q, k, v)."""
+    in_type = _type_of(qkv, "qkv", _TYPES)
+    if qkv.dim() != 2:
+        raise ValueError(f"qkv must be [M, values], got shape {tuple(qkv.shape)}")
+    if heads < 1 or kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"heads = {heads} must be a positive multiple of kv_heads = {kv_heads}")
+    M, total = qkv.shape[0], heads + 2 * kv_heads
+    if qkv.shape[1] == 0 or qkv.shape[1] % total:
+        raise ValueError(f"qkv rows of {qkv.shape[1]} values are not {total} heads")
+    D, dev = qkv.shape[1] // total, qkv.device
+    _need_strided(qkv, "qkv", qkv.dtype, qkv.shape, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.float32, (D,), dev)
+    rot = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a 1-D tensor of rot_dim / 2 angles")
+        rot = 2 * inv_freq.shape[0]
+        _need(inv_freq, "inv_freq", torch.float64, None, dev)
+        _need(positions, "positions", torch.int32, (M,), dev)
+    if rows is not None:
+        _need(rows, "rows", torch.int32, (M,), dev)
+        if out is None:
+            raise ValueError("rows names rows of the k and v given in out")
+    if out is None:
+        q = torch.empty((M, heads, D), dtype=dtype, device=dev)
+        k = torch.empty((M, kv_heads, D), dtype=dtype, device=dev)
+        v = torch.empty((M, kv_heads, D), dtype=dtype, device=dev)
+    else:
+        q, k, v = out
+    out_type = _type_of(q, "q", _TYPES)
+    room = k.shape[0] if rows is not None and isinstance(k, torch.Tensor) and k.dim() == 3 else M
+    _need_strided(q, "q", q.dtype, (M, heads, D), dev, output=True)
+    _need_strided(k, "k", q.dtype, (room, kv_heads, D), dev, output=True)
+    _need_strided(v, "v", q.dtype, (room, kv_heads, D), dev, output=True)
+    strides = (ctypes.c_int64 * 6)(q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    _call(dev, lib().bt_qk_norm_rope, _ptr(qkv), in_type, qkv.stride(0), M, heads, kv_heads, D, _ptr(q_weight),
+          _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot, int(interleaved), _ptr(rows), room,
+          _ptr(q), _ptr(k), _ptr(v), out_type, ctypes.addressof(strides))
+    return q, k, v

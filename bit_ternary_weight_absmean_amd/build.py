@@ -26,7 +26,8 @@ CEILINGS_SRC = "ceilings.hip"
 CEILINGS_LIB = os.path.join(PKG, "libbt_ceilings.so")
 ARCH = "gfx950"
 
-SOURCES = ["abi.hip", "pack.hip", "quant.hip", "gemv.hip", "lut.hip", "bits.hip", "decode.hip", "gemm.hip"]
+SOURCES = ["abi.hip", "pack.hip", "quant.hip", "gemv.hip", "lut.hip", "bits.hip", "decode.hip", "gemm.hip",
+           "heads.hip", "lora.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -89,6 +89,30 @@ bt_status check_product(const void *Wp, const float *w_scale, const int8_t *Xq, 
     return BT_OK;
 }
 
+// The row groups of a matrix of N rows, as the end row of each.
+bt_status read_groups(const int64_t *group_rows, int64_t ngroups, int64_t N, bt::RowGroups &groups)
+{
+    if (ngroups < 1 || ngroups > BT_MAX_ROW_GROUPS)
+        return fail(BT_ERR_SHAPE, "ngroups = %lld outside [1, %d]", (long long)ngroups, BT_MAX_ROW_GROUPS);
+    int64_t end = 0;
+    for (int64_t g = 0; g < ngroups; ++g) {
+        if (group_rows[g] < 1)
+            return fail(BT_ERR_SHAPE, "group %lld has %lld rows", (long long)g, (long long)group_rows[g]);
+        // each count is bounded before the sum, which then cannot overflow
+        end = group_rows[g] > N ? N + 1 : end + group_rows[g];
+        if (end > N)
+            break;
+        groups.end[g] = end;
+    }
+    if (end != N)
+        return fail(BT_ERR_SHAPE, "the row groups cover %lld rows, not N = %lld", (long long)end, (long long)N);
+    groups.n = (int)ngroups;
+    return BT_OK;
+}
+
+bool known_type(int32_t t) { return t == BT_F32 || t == BT_BF16 || t == BT_F16; }
+int type_size(int32_t t) { return t == BT_F32 ? 4 : 2; }
+
 }  // namespace
 
 extern "C" {
@@ -138,22 +162,9 @@ bt_status bt_pack_weights_rows(const float *W, int64_t N, int64_t K, const int64
     if (bt_status s = check_nk(N, K))
         return s;
     bt::RowGroups groups{};
-    if (group_rows) {
-        if (ngroups < 1 || ngroups > BT_MAX_ROW_GROUPS)
-            return fail(BT_ERR_SHAPE, "ngroups = %lld outside [1, %d]", (long long)ngroups, BT_MAX_ROW_GROUPS);
-        int64_t end = 0;
-        for (int64_t g = 0; g < ngroups; ++g) {
-            if (group_rows[g] < 1)
-                return fail(BT_ERR_SHAPE, "group %lld has %lld rows", (long long)g, (long long)group_rows[g]);
-            end += group_rows[g];
-            if (end > N)
-                break;
-            groups.end[g] = end;
-        }
-        if (end != N)
-            return fail(BT_ERR_SHAPE, "the row groups cover %lld rows, not N = %lld", (long long)end, (long long)N);
-        groups.n = (int)ngroups;
-    }
+    if (group_rows)
+        if (bt_status s = read_groups(group_rows, ngroups, N, groups))
+            return s;
     if (N == 0)
         return ok();
     if (!W && K > 0)
@@ -621,6 +632,95 @@ bt_status bt_kernel_plan(int32_t call, int64_t M, int64_t N, int64_t K, int32_t 
         return gemv_plan(BT_GEMV_AUTO);
     add(bt::plan_gemm(M, N, K, rows, true, buf + used, room()));
     return ok();
+}
+
+size_t bt_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t ngroups)
+{
+    if (M <= 0 || M > BT_MAX_DIM || K < 0 || K > BT_MAX_K || R < 1 || R > BT_LORA_MAX_RANK || ngroups < 1 ||
+        ngroups > BT_MAX_ROW_GROUPS)
+        return 0;
+    return bt::lora_workspace_bytes(M, K, R, ngroups);
+}
+
+bt_status bt_lora_apply(const void *A, const void *B, int32_t w_type, const float *scale, const int32_t *ranks,
+                        int64_t L, int64_t R, const int64_t *group_rows, int64_t ngroups, const int32_t *adapter,
+                        const float *X, const float *Y0, int64_t M, int64_t N, int64_t K, float *Y, void *workspace,
+                        void *stream)
+{
+    if (M < 0 || M > BT_MAX_DIM || N < 0 || N > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "M = %lld or N = %lld outside [0, 2^23]", (long long)M, (long long)N);
+    if (bt_status s = check_k(K))
+        return s;
+    if (M * N > BT_MAX_MN)
+        return fail(BT_ERR_SHAPE, "M * N = %lld above 2^36", (long long)(M * N));
+    if (L < 0 || L > INT32_MAX)
+        return fail(BT_ERR_SHAPE, "L = %lld outside [0, 2^31)", (long long)L);
+    if (R < 1 || R > BT_LORA_MAX_RANK)
+        return fail(BT_ERR_SHAPE, "R = %lld outside [1, %d]", (long long)R, BT_LORA_MAX_RANK);
+    if (!known_type(w_type))
+        return fail(BT_ERR_UNSUPPORTED, "unknown element type %d", w_type);
+    if (M == 0 || N == 0)
+        return ok();
+    bt::RowGroups groups{};
+    if (group_rows) {
+        if (bt_status s = read_groups(group_rows, ngroups, N, groups))
+            return s;
+    } else {
+        groups.n = 1;
+        groups.end[0] = N;
+    }
+    if (!Y || !adapter || !workspace || (K > 0 && !X) || (L > 0 && (!B || !scale || (K > 0 && !A))))
+        return fail(BT_ERR_NULL, "NULL A, B, scale, adapter, X, Y or workspace");
+    const int wb = type_size(w_type);
+    if (!aligned(A, wb) || !aligned(B, wb) || !aligned(scale, 4) || !aligned(ranks, 4) || !aligned(adapter, 4) ||
+        !aligned(X, 4) || !aligned(Y0, 4) || !aligned(Y, 4))
+        return fail(BT_ERR_ALIGN, "arrays must be aligned to their elements");
+    if (!aligned(workspace, 256))
+        return fail(BT_ERR_ALIGN, "workspace must be 256-byte aligned");
+    return hip_status(bt::launch_lora(A, B, w_type, scale, ranks, L, R, groups, adapter, X, Y0, M, N, K, Y, workspace,
+                                      static_cast<hipStream_t>(stream)),
+                      "bt_lora_apply launch");
+}
+
+bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int64_t M, int64_t heads,
+                          int64_t kv_heads, int64_t head_dim, const float *q_weight, const float *k_weight, float eps,
+                          const int32_t *positions, const double *inv_freq, int64_t rot_dim, int32_t interleaved,
+                          const int32_t *rows, int64_t kv_rows, void *q, void *k, void *v, int32_t out_type,
+                          const int64_t *strides, void *stream)
+{
+    if (M < 0 || M > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "M = %lld outside [0, 2^23]", (long long)M);
+    if (heads < 1 || kv_heads < 1 || heads > 65536 || heads % kv_heads)
+        return fail(BT_ERR_SHAPE, "heads = %lld, kv_heads = %lld: heads must be a multiple of kv_heads, at most 65536",
+                    (long long)heads, (long long)kv_heads);
+    if (head_dim < 8 || head_dim > BT_ROPE_MAX_HEAD_DIM || head_dim % 8)
+        return fail(BT_ERR_SHAPE, "head_dim = %lld is not a multiple of 8 in [8, %d]", (long long)head_dim,
+                    BT_ROPE_MAX_HEAD_DIM);
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8)
+        return fail(BT_ERR_SHAPE, "rot_dim = %lld is not a multiple of 8 in [0, head_dim]", (long long)rot_dim);
+    if (!(eps >= 0.0f) || eps > 3.0e38f)
+        return fail(BT_ERR_SHAPE, "eps must be finite and not negative");
+    if (!known_type(in_type) || !known_type(out_type))
+        return fail(BT_ERR_UNSUPPORTED, "unknown element type %d or %d", in_type, out_type);
+    if (kv_rows < 0 || kv_rows > INT32_MAX || (!rows && kv_rows < M))
+        return fail(BT_ERR_SHAPE, "kv_rows = %lld for M = %lld tokens", (long long)kv_rows, (long long)M);
+    if (M == 0)
+        return ok();
+    if (!qkv || !q || !k || !v || !strides || (rot_dim > 0 && (!positions || !inv_freq)))
+        return fail(BT_ERR_NULL, "NULL qkv, q, k, v, strides, positions or inv_freq");
+    const uintptr_t ib = 4 * type_size(in_type), ob = 4 * type_size(out_type);
+    bool quads = qkv_row % 4 == 0 && qkv_row >= 0;
+    for (int i = 0; i < 6; ++i)
+        quads = quads && strides[i] % 4 == 0 && strides[i] >= 0;
+    if (!quads || !aligned(qkv, ib) || !aligned(q, ob) || !aligned(k, ob) || !aligned(v, ob) ||
+        !aligned(q_weight, 16) || !aligned(k_weight, 16))
+        return fail(BT_ERR_ALIGN, "arrays and strides must be aligned to four elements");
+    if (!aligned(positions, 4) || !aligned(rows, 4) || !aligned(inv_freq, 8))
+        return fail(BT_ERR_ALIGN, "positions, rows and inv_freq must be aligned to their elements");
+    return hip_status(bt::launch_qk_norm_rope(qkv, in_type, qkv_row, M, heads, kv_heads, head_dim, q_weight, k_weight,
+                                              eps, positions, inv_freq, rot_dim, interleaved != 0, rows, kv_rows, q, k,
+                                              v, out_type, strides, static_cast<hipStream_t>(stream)),
+                      "bt_qk_norm_rope launch");
 }
 
 const char *bt_status_str(bt_status s)

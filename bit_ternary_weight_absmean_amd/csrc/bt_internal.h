@@ -105,6 +105,19 @@ hipError_t launch_gemm(const uint4 *Wp, const float *w_scale, bool row_scales, c
                        const float *sx, const int32_t *xsum, int64_t M, int64_t N, int64_t K, float *Y, int32_t *acc,
                        void *workspace, size_t workspace_bytes, hipStream_t s);
 
+// The attention block around the products. Element types: BT_F32, BT_BF16, BT_F16; strides are
+// q_row, q_head, k_row, k_head, v_row, v_head in elements.
+hipError_t launch_qk_norm_rope(const void *qkv, int in_type, int64_t ld, int64_t M, int64_t heads, int64_t kv_heads,
+                               int64_t D, const float *qw, const float *kw, float eps, const int32_t *pos,
+                               const double *inv_freq, int64_t rot, int interleaved, const int32_t *rows,
+                               int64_t kv_rows, void *q, void *k, void *v, int out_type, const int64_t *strides,
+                               hipStream_t s);
+// Low-rank adapters. The workspace holds the adapters' inner products and needs no clearing.
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t groups);
+hipError_t launch_lora(const void *A, const void *B, int w_type, const float *scale, const int32_t *ranks, int64_t L,
+                       int64_t R, const RowGroups &groups, const int32_t *adapter, const float *X, const float *Y0,
+                       int64_t M, int64_t N, int64_t K, float *Y, void *workspace, hipStream_t s);
+
 // Names of the kernel instances the launchers pick for a call (host-only, snprintf
 // semantics; 16-byte aligned activation rows assumed), for bt_kernel_plan.
 int plan_quant_act(int64_t M, int64_t K, char *buf, size_t len);

@@ -391,6 +391,72 @@ bt_status bt_ternary_gemv_a1(const void *Wp, const float *w_scale, const uint32_
 bt_status bt_kernel_plan(int32_t call, int64_t M, int64_t N, int64_t K, int32_t algo, int32_t row_scales,
                          char *buf, size_t len);
 
+/*
+ * The attention block around the products: low-rank adapters beside a projection, the norms
+ * and the position rotation of Q and K, and attention. Element types of their arrays:
+ */
+#define BT_F32 0
+#define BT_BF16 1
+#define BT_F16 2
+
+/*
+ * bt_lora_apply -- low-rank adapters of many requests at once beside one shared projection:
+ *   Y[m,n] = Y0[m,n] + scale[a] * sum_{r < rank[a]} (sum_k X[m,k] A[a, g R + r, k]) B[a,n,r]
+ * with a = adapter[m] and g the row group of output n. A fused projection (Q, K and V; gate
+ * and up) keeps one A per group, stacked, as bt_pack_weights_rows keeps one scale.
+ *   A         [L, ngroups * R, K], B [L, N, R], both of type w_type, aligned to their element
+ *             (16-byte aligned with K and R multiples of 8 is faster).
+ *   scale     [L] fp32. ranks: [L] int32 or NULL (all R); ranks are clamped to [0, R], and
+ *             what A and B hold past an adapter's rank is not read.
+ *   group_rows  HOST array of ngroups row counts as for bt_pack_weights_rows, or NULL for one
+ *             group (ngroups ignored).
+ *   adapter   [M] int32 on the device. A token whose entry is outside [0, L) has no adapter:
+ *             its row of Y is Y0's.
+ *   X         [M,K] fp32. Y0 [M,N] fp32, or NULL for zeros. Y [M,N] fp32; Y may be Y0 itself,
+ *             and must not overlap the inputs otherwise.
+ *   workspace bt_lora_workspace_bytes(M, K, R, ngroups) bytes of device scratch, 256-byte
+ *             aligned; contents on entry are ignored. Calls sharing one must not overlap.
+ * Operands are multiplied without rounding them and summed in fp32 in an order that depends on
+ * the shape alone (no atomics). 1 <= R <= BT_LORA_MAX_RANK, 0 <= L < 2^31. An adapter's weights
+ * never reach the tokens of another one, whatever they hold.
+ */
+#define BT_LORA_MAX_RANK 256
+size_t bt_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t ngroups);
+bt_status bt_lora_apply(const void *A, const void *B, int32_t w_type, const float *scale, const int32_t *ranks,
+                        int64_t L, int64_t R, const int64_t *group_rows, int64_t ngroups, const int32_t *adapter,
+                        const float *X, const float *Y0, int64_t M, int64_t N, int64_t K, float *Y,
+                        void *workspace, void *stream);
+
+/*
+ * bt_qk_norm_rope -- from the fused QKV rows of a projection, in one pass: the norm of every
+ * query and key head, the rotation by the token's position, and the conversion of Q, K and V
+ * to the attention's type, K and V optionally straight into cache rows.
+ *   qkv       [M] rows of (heads + 2 * kv_heads) * head_dim values of in_type (Q heads, K
+ *             heads, V heads), qkv_row elements apart.
+ *   q_weight, k_weight  [head_dim] fp32, or NULL for no norm:
+ *             x * weight / sqrt(mean(x^2) + eps) per head.
+ *   rotation  of each head's first rot_dim values by t = positions[m] * inv_freq[p]:
+ *             (a, b) -> (a cos t - b sin t, b cos t + a sin t) for the pairs
+ *             (p, p + rot_dim/2), or (2p, 2p + 1) with interleaved != 0. inv_freq [rot_dim/2]
+ *             fp64; the angle is formed and reduced in fp64. positions [M] int32. Both may be
+ *             NULL when rot_dim == 0.
+ *   rows      NULL: token m's K and V go to row m of k and v (kv_rows >= M). Else [M] int32:
+ *             they go to row rows[m]; tokens with a row outside [0, kv_rows) write no K and V.
+ *             Rows that no token names stay as they are. Two tokens of one call must not name
+ *             the same row (which of them it then holds is unspecified).
+ *   q, k, v   outputs of out_type, value d of head h of row r at r * strides[2i] +
+ *             h * strides[2i+1] + d, i = 0, 1, 2 (strides: HOST array of 6, in elements). They
+ *             must not overlap each other or the inputs.
+ * head_dim and rot_dim are multiples of 8, rot_dim <= head_dim <= BT_ROPE_MAX_HEAD_DIM,
+ * heads a multiple of kv_heads. Arrays and strides are aligned to four elements.
+ */
+#define BT_ROPE_MAX_HEAD_DIM 512
+bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int64_t M, int64_t heads,
+                          int64_t kv_heads, int64_t head_dim, const float *q_weight, const float *k_weight,
+                          float eps, const int32_t *positions, const double *inv_freq, int64_t rot_dim,
+                          int32_t interleaved, const int32_t *rows, int64_t kv_rows, void *q, void *k, void *v,
+                          int32_t out_type, const int64_t *strides, void *stream);
+
 /* Static text for a status code. */
 const char *bt_status_str(bt_status s);
 
