@@ -6,8 +6,8 @@ current HIP stream into those calls; every step of the path runs in the library'
 kernels. Names follow the C ABI: ``pack_weights``, ``quant_act``, ``ternary_gemv``,
 ``ternary_gemm`` (+ ``unpack_weights``, ``linear``, and ``pack_weights_rows`` for
 row-group weight scales, which the product calls then take in place of one scale), and the
-attention block around the products: ``lora_apply`` (also through ``linear``) and
-``qk_norm_rope``.
+attention block around the products: ``lora_apply`` (also through ``linear``),
+``qk_norm_rope`` and ``attention``.
 """
 from __future__ import annotations
 
@@ -31,6 +31,9 @@ from .api import (
     LoraAdapters,
     PackedWeight,
     act_row_bytes,
+    attention,
+    attention_workspace,
+    attention_workspace_bytes,
     binarize_act,
     binary_gemv,
     gemm_split_plan,
@@ -63,5 +66,5 @@ __all__ = [
     "gemm_split_plan", "gemm_workspace", "gemm_workspace_bytes", "linear", "linear_workspace_bytes", "pack_weights", "pack_weights_rows", "pack_workspace_bytes", "packed_weight_bytes", "quant_act", "ternary_gemm",
     "ternary_gemv", "unpack_weights", "kernel_plan", "CALL_LINEAR", "CALL_GEMV", "CALL_GEMM", "CALL_GEMM_WS", "CALL_QUANT", "linear_static", "STATIC_SCRATCH_BYTES",
     "LORA_MAX_RANK", "LoraAdapters", "lora_apply", "lora_workspace", "lora_workspace_bytes", "qk_norm_rope",
-    "rope_frequencies",
+    "rope_frequencies", "attention", "attention_workspace", "attention_workspace_bytes",
 ]

@@ -8,6 +8,16 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libbt.so")
 
+class AttentionShape(ctypes.Structure):
+    """bt_attention_shape."""
+
+    _fields_ = ([(n, ctypes.c_int64) for n in ("tokens", "keys", "seqs", "prefix", "heads", "kv_heads", "head_dim")]
+                + [(n, ctypes.c_int32) for n in ("type", "out_type", "causal")] + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head",
+                                                 "prefix_k_row", "prefix_k_head", "prefix_v_row", "prefix_v_head",
+                                                 "out_row", "out_head")])
+
+
 # Every function declared in include/bt.h, with (restype, argtypes).
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 SIGNATURES = {
@@ -42,6 +52,8 @@ SIGNATURES = {
                              _vp]),
     "bt_qk_norm_rope": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _i64, _i32,
                                _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "bt_attention_workspace_bytes": (_sz, [_i64] * 6),
+    "bt_attention": (_i32, [_vp] * 13),
     "bt_status_str": (ctypes.c_char_p, [_i32]),
     "bt_last_error": (ctypes.c_char_p, []),
 }

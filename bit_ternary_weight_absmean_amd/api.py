@@ -11,7 +11,7 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import check, lib
+from ._lib import AttentionShape, check, lib
 
 GEMV_AUTO, GEMV_DOT4, GEMV_MFMA, GEMV_LUT, GEMV_STAGED = 0, 1, 2, 3, 4
 GEMV_MAX_M = 16
@@ -577,3 +577,82 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, inv_freq: to
           _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot, int(interleaved), _ptr(rows), room,
           _ptr(q), _ptr(k), _ptr(v), out_type, ctypes.addressof(strides))
     return q, k, v
+
+
+_HALF = {torch.bfloat16: 1, torch.float16: 2}
+
+
+def attention_workspace_bytes(tokens: int, seqs: int, heads: int, kv_heads: int, head_dim: int, prefix: int = 0) -> int:
+    """bt_attention_workspace_bytes: the scratch of an attention call (0: none)."""
+    return int(lib().bt_attention_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim, prefix))
+
+
+def attention_workspace(q: torch.Tensor, k: torch.Tensor, seqs: int,
+                        prefix_k: torch.Tensor | None = None) -> torch.Tensor | None:
+    """A workspace for attention of these arrays in ``seqs`` sequences (its contents do not matter), or
+    None where none is needed."""
+    n = attention_workspace_bytes(q.shape[0], seqs, q.shape[1], k.shape[1], q.shape[2],
+                                  0 if prefix_k is None else prefix_k.shape[0])
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, k_start: torch.Tensor,
+              k_len: torch.Tensor, causal: bool = True, scale: float | None = None,
+              prefix_k: torch.Tensor | None = None, prefix_v: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+              lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """bt_attention: softmax attention of packed sequences with grouped heads.
+
+    ``q`` [T, heads, D], ``k`` and ``v`` [rows, kv_heads, D] (bf16 or fp16, any row and head strides).
+    Sequence b has queries q_start[b] .. q_start[b + 1] and keys k_start[b] .. + k_len[b] (int32, on the
+    device); ``causal``: its last query sees all of them. With ``prefix_k`` / ``prefix_v`` [P, kv_heads,
+    D] every query also sees the whole prefix. ``scale`` defaults to D ** -0.5. ``out`` [T, heads, D] in
+    q's type or fp32 (``out_dtype``); ``lse`` [T, heads] fp32 receives the log of the softmax's sum.
+    Rows of no sequence are not written. Returns (out, lse)."""
+    kind = _type_of(q, "q", _HALF)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, heads, D], got shape {tuple(q.shape)}")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [rows, kv_heads, D]")
+    if not isinstance(k_len, torch.Tensor) or k_len.dim() != 1:
+        raise ValueError("k_len must be a 1-D tensor, one entry per sequence")
+    (T, heads, D), (S, kv_heads), B, dev, dt = q.shape, k.shape[:2], k_len.shape[0], q.device, q.dtype
+    if kv_heads < 1 or heads < 1 or heads % kv_heads:
+        raise ValueError(f"{heads} heads are not a positive multiple of {kv_heads} key heads")
+    _need_strided(q, "q", dt, q.shape, dev)
+    _need_strided(k, "k", dt, (S, kv_heads, D), dev)
+    _need_strided(v, "v", dt, (S, kv_heads, D), dev)
+    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
+    _need(k_start, "k_start", torch.int32, (B,), dev)
+    _need(k_len, "k_len", torch.int32, (B,), dev)
+    P, pk, pv = 0, (0, 0), (0, 0)
+    if (prefix_k is None) != (prefix_v is None):
+        raise ValueError("prefix_k and prefix_v come together")
+    if prefix_k is not None:
+        if not isinstance(prefix_k, torch.Tensor) or prefix_k.dim() != 3:
+            raise ValueError("prefix_k must be a tensor [P, kv_heads, D]")
+        P = prefix_k.shape[0]
+        _need_strided(prefix_k, "prefix_k", dt, (P, kv_heads, D), dev)
+        _need_strided(prefix_v, "prefix_v", dt, (P, kv_heads, D), dev)
+        pk, pv = prefix_k.stride(), prefix_v.stride()
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=out_dtype or dt, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    if out.dtype not in (dt, torch.float32):
+        raise TypeError(f"out must be {dt} or torch.float32, got {out.dtype}")
+    _need_strided(out, "out", out.dtype, (T, heads, D), dev, output=True)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, heads), dev)
+    need = attention_workspace_bytes(T, B, heads, kv_heads, D, P)
+    if workspace is not None:
+        _need_bytes(workspace, "workspace", need, dev)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+    shape = AttentionShape(T, S, B, P, heads, kv_heads, D, kind, _TYPES[out.dtype], int(causal),
+                           D ** -0.5 if scale is None else scale, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], pk[0],
+                           pk[1], pv[0], pv[1], os[0], os[1])
+    _call(dev, lib().bt_attention, ctypes.addressof(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(q_start), _ptr(k_start),
+          _ptr(k_len), _ptr(prefix_k), _ptr(prefix_v), _ptr(out), _ptr(lse), _ptr(workspace))
+    return out, lse

@@ -4,8 +4,11 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <math.h>
+
 #include <mutex>
 
+#include "attention.h"
 #include "bt.h"
 #include "bt_internal.h"
 
@@ -107,6 +110,31 @@ bt_status read_groups(const int64_t *group_rows, int64_t ngroups, int64_t N, bt:
     if (end != N)
         return fail(BT_ERR_SHAPE, "the row groups cover %lld rows, not N = %lld", (long long)end, (long long)N);
     groups.n = (int)ngroups;
+    return BT_OK;
+}
+
+// Shape checks of bt_attention that its workspace size shares.
+bt_status check_attention(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                          int64_t prefix, bt::AttnPlan &plan)
+{
+    if (tokens < 0 || tokens > BT_MAX_DIM || seqs < 0 || seqs > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "tokens = %lld or seqs = %lld outside [0, 2^23]", (long long)tokens, (long long)seqs);
+    if (prefix < 0 || prefix > INT32_MAX - 64)
+        return fail(BT_ERR_SHAPE, "prefix = %lld outside [0, 2^31 - 65]", (long long)prefix);
+    if (heads < 1 || kv_heads < 1 || heads > 65536 || heads % kv_heads)
+        return fail(BT_ERR_SHAPE, "heads = %lld, kv_heads = %lld: heads must be a multiple of kv_heads, at most 65536",
+                    (long long)heads, (long long)kv_heads);
+    if (head_dim < 8 || head_dim > BT_ATTENTION_MAX_HEAD_DIM || head_dim % 8)
+        return fail(BT_ERR_SHAPE, "head_dim = %lld is not a multiple of 8 in [8, %d]", (long long)head_dim,
+                    BT_ATTENTION_MAX_HEAD_DIM);
+    if (tokens * heads > INT32_MAX)
+        return fail(BT_ERR_SHAPE, "tokens * heads = %lld not below 2^31", (long long)(tokens * heads));
+    plan = bt::AttnPlan{};
+    if (tokens == 0 || seqs == 0)
+        return BT_OK;
+    plan = bt::attn_plan(tokens, seqs, heads, kv_heads, head_dim, prefix);
+    if (plan.main.items * kv_heads >= 1 << 24 || plan.pre.items * kv_heads >= 1 << 24)
+        return fail(BT_ERR_SHAPE, "%lld work items for one launch", (long long)(plan.main.items * kv_heads));
     return BT_OK;
 }
 
@@ -721,6 +749,96 @@ bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int
                                               eps, positions, inv_freq, rot_dim, interleaved != 0, rows, kv_rows, q, k,
                                               v, out_type, strides, static_cast<hipStream_t>(stream)),
                       "bt_qk_norm_rope launch");
+}
+
+size_t bt_attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                    int64_t prefix)
+{
+    bt::AttnPlan plan;
+    if (check_attention(tokens, seqs, heads, kv_heads, head_dim, prefix, plan))
+        return 0;
+    return plan.bytes;
+}
+
+bt_status bt_attention(const bt_attention_shape *shape, const void *q, const void *k, const void *v,
+                       const int32_t *q_start, const int32_t *k_start, const int32_t *k_len, const void *prefix_k,
+                       const void *prefix_v, void *out, float *lse, void *workspace, void *stream)
+{
+    if (!shape)
+        return fail(BT_ERR_NULL, "shape is NULL");
+    const bt_attention_shape &s = *shape;
+    bt::AttnPlan plan;
+    if (bt_status e = check_attention(s.tokens, s.seqs, s.heads, s.kv_heads, s.head_dim, s.prefix, plan))
+        return e;
+    if (s.keys < 0 || s.keys > INT32_MAX - 64)
+        return fail(BT_ERR_SHAPE, "keys = %lld outside [0, 2^31 - 65]", (long long)s.keys);
+    if (!(s.scale > 0.0f) || !(s.scale < 1.0e30f))
+        return fail(BT_ERR_SHAPE, "scale must be finite and positive");
+    if ((s.type != BT_BF16 && s.type != BT_F16) || (s.out_type != s.type && s.out_type != BT_F32))
+        return fail(BT_ERR_UNSUPPORTED, "type %d with out_type %d", s.type, s.out_type);
+    if (s.tokens == 0 || s.seqs == 0)
+        return ok();
+    if (!q || !out || !q_start || !k_start || !k_len || (s.keys > 0 && (!k || !v)) ||
+        (s.prefix > 0 && (!prefix_k || !prefix_v)) || (plan.bytes > 0 && !workspace))
+        return fail(BT_ERR_NULL, "NULL q, k, v, q_start, k_start, k_len, prefix_k, prefix_v, out or workspace");
+    const int64_t in[] = {s.q_row, s.q_head, s.k_row, s.k_head, s.v_row, s.v_head, s.prefix_k_row, s.prefix_k_head,
+                          s.prefix_v_row, s.prefix_v_head};
+    for (int i = 0; i < (s.prefix > 0 ? 10 : 6); ++i) {
+        if (in[i] < 0 || in[i] % 8)
+            return fail(BT_ERR_ALIGN, "strides of q, k, v and the prefix must be multiples of 8");
+        if (i >= 2 && i % 2 == 0 && in[i] > BT_MAX_DIM)
+            return fail(BT_ERR_SHAPE, "a row stride of %lld elements is above 2^23", (long long)in[i]);
+    }
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || (s.prefix > 0 && (!aligned(prefix_k, 16) || !aligned(prefix_v, 16))))
+        return fail(BT_ERR_ALIGN, "q, k, v and the prefix must be 16-byte aligned");
+    if (s.out_row < 0 || s.out_head < 0 || s.out_row % 4 || s.out_head % 4 || !aligned(out, 4 * type_size(s.out_type)))
+        return fail(BT_ERR_ALIGN, "out and its strides must be aligned to four elements");
+    if (!aligned(q_start, 4) || !aligned(k_start, 4) || !aligned(k_len, 4) || !aligned(lse, 4))
+        return fail(BT_ERR_ALIGN, "q_start, k_start, k_len and lse must be 4-byte aligned");
+    if (plan.bytes > 0 && !aligned(workspace, 256))
+        return fail(BT_ERR_ALIGN, "workspace must be 256-byte aligned");
+    bt::AttnArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_start = q_start;
+    a.k_start = k_start;
+    a.k_len = k_len;
+    a.out = out;
+    a.lse = lse;
+    a.ws_o = static_cast<float *>(workspace);
+    a.q_row = s.q_row;
+    a.q_head = s.q_head;
+    a.k_row = s.k_row;
+    a.k_head = s.k_head;
+    a.v_row = s.v_row;
+    a.v_head = s.v_head;
+    a.o_row = s.out_row;
+    a.o_head = s.out_head;
+    a.T = (int)s.tokens;
+    a.S = (int)s.keys;
+    a.B = (int)s.seqs;
+    a.Hq = (int)s.heads;
+    a.Hkv = (int)s.kv_heads;
+    a.G = (int)(s.heads / s.kv_heads);
+    a.D = (int)s.head_dim;
+    a.scale_log2 = (float)(s.scale * M_LOG2E);
+    a.causal = s.causal != 0;
+    bt::AttnArgs pre{};
+    if (s.prefix > 0) {
+        pre = a;
+        pre.k = prefix_k;
+        pre.v = prefix_v;
+        pre.k_row = s.prefix_k_row;
+        pre.k_head = s.prefix_k_head;
+        pre.v_row = s.prefix_v_row;
+        pre.v_head = s.prefix_v_head;
+        pre.P = (int)s.prefix;
+        pre.causal = 0;
+        pre.shared = 1;
+    }
+    return hip_status(bt::launch_attention(a, pre, plan, s.type, s.out_type, static_cast<hipStream_t>(stream)),
+                      "bt_attention launch");
 }
 
 const char *bt_status_str(bt_status s)

@@ -1,0 +1,1036 @@
+// Attention over packed sequences with grouped heads (bt_attention): whole causal prompts, prompts
+// continued behind cached keys, single tokens over a cache, and batches that share a prefix.
+//
+//   s[r, j] = scale * q_r . k_j over the keys j that row r sees;  out_r = sum_j softmax(s)_j v_j;
+//   lse_r = ln sum_j exp(s[r, j])      (no key seen: out 0, lse -inf)
+//
+// One pass over the keys with a running maximum m and sum l per row (both fp32; scores are kept in
+// powers of two, so exp is one v_exp_f32 of an FMA). A row's accumulator is rescaled only when its
+// maximum rose by more than 2^8: probabilities are relative to the reference m, whatever it is.
+//
+// Rows. The G = heads / kv_heads query heads of a key head read the same keys, so a tile's rows are
+// (token, head of the group) pairs: row r of a sequence is token r / G, head r % G of the group. A
+// decode step of one token thus already fills G rows of an MFMA with one read of the keys.
+//
+// Layout. Both products are computed transposed, S^T = K Q^T and O^T = V^T P^T, so that a query row
+// is a column of the MFMA result: its running maximum and sum live in the lanes of that column
+// (one exchange between lane halves or quarters per step), and the probabilities come out in the
+// registers in which the second product takes them, with no exchange at all, as long as both of its
+// operands number the keys alike. V^T operands come from row-major V in LDS through the transposing
+// LDS read (ds_read_b64_tr_b16: lane i of 16 receives column i of a 4 x 16 block).
+//
+// Rounding: scores, statistics and accumulators are fp32. Probabilities are rounded to the type of V
+// for the matrix cores, which is of the order of the output's own rounding where the output has that
+// type; for fp32 outputs they are carried as two such values (the rounded one and the rest).
+//
+// Masked places. Scores of unseen keys are replaced, never added to, so what K holds there does not
+// matter; keys past a sequence's end are not read at all. An unseen value meets a probability of
+// exactly 0, and 0 * inf would still be NaN: in a block whose mask is not full, infinities and NaNs
+// of V are set to 0 before the product, and (only if there were any) added afterwards to the rows
+// that see them.
+//
+// Work split. A work item is (row tile, slice of its keys, key head). Sequence lengths are device
+// data, so every workgroup derives the items from them itself (one wave scan over the sequences).
+// With `target` set, keys are cut into slices of equal length such that all items together are
+// about `target`: then the slices' outputs, normalized, go to the workspace with their lse, and
+// k_attn_combine joins them in slice order. No atomics, so results do not depend on timing.
+#include <math.h>
+
+#include "attention.h"
+#include "bt_internal.h"
+#include "convert.h"
+#include "wave.h"
+
+namespace bt {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int kUnit = 64;             // keys: granularity of the key slices
+constexpr float kRescale = 8.0f;      // exponent by which a maximum may rise without rescaling
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kBufferWord3 = 0x00020000;
+constexpr uint32_t kOutside = 0x7FFFFFF0u;  // a buffer offset past every record
+
+template <typename E>
+struct Elem;
+template <>
+struct Elem<bf16_t> {
+    typedef bf16_t v8 __attribute__((ext_vector_type(8)));
+    typedef bf16_t v2 __attribute__((ext_vector_type(2)));
+    static constexpr uint32_t kExp = 0x7F80u;
+    static __device__ f32x16 mma32(v8 a, v8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ f32x4 mma16(v8 a, v8 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Elem<f16_t> {
+    typedef f16_t v8 __attribute__((ext_vector_type(8)));
+    typedef f16_t v2 __attribute__((ext_vector_type(2)));
+    static constexpr uint32_t kExp = 0x7C00u;
+    static __device__ f32x16 mma32(v8 a, v8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ f32x4 mma16(v8 a, v8 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Two values rounded to E, packed.
+template <typename E>
+__device__ inline uint32_t pack2(float a, float b)
+{
+    const f32x2 f = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, typename Elem<E>::v2));
+}
+template <typename E>
+__device__ inline f32x2 unpack2(uint32_t p)
+{
+    return __builtin_convertvector(__builtin_bit_cast(typename Elem<E>::v2, p), f32x2);
+}
+
+// Does a pair of E values hold an infinity or NaN?
+template <typename E>
+__device__ inline bool not_finite(uint32_t p)
+{
+    constexpr uint32_t e = Elem<E>::kExp;
+    return (p & e) == e || (p >> 16 & e) == e;
+}
+
+// A pair of E values with infinities and NaNs set to 0.
+template <typename E>
+__device__ inline uint32_t finite_part(uint32_t p)
+{
+    constexpr uint32_t e = Elem<E>::kExp;
+    return ((p & e) == e ? 0u : p & 0xFFFFu) | ((p >> 16 & e) == e ? 0u : p & 0xFFFF0000u);
+}
+
+__device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ inline float other_half(float v)  // the value of lane ^ 32
+{
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float((threadIdx.x & 32) ? p[0] : p[1]);
+}
+
+// ---------------------------------------------------------------------------- work items
+
+struct Seq {
+    int q0, nq, k0, nk;
+};
+
+// Sequence b, its rows and keys kept inside the arrays whatever the offsets say.
+__device__ inline Seq load_seq(const AttnArgs &a, int b)
+{
+    Seq s = {0, 0, 0, 0};
+    if (a.shared) {  // the shared prefix: every token's rows over the prefix keys
+        s.nq = a.T;
+        s.nk = a.P;
+        return s;
+    }
+    s.q0 = min(max(a.q_start[b], 0), a.T);
+    s.nq = min(max(a.q_start[b + 1], s.q0), a.T) - s.q0;
+    s.k0 = min(max(a.k_start[b], 0), a.S);
+    s.nk = min(max(a.k_len[b], 0), a.S - s.k0);
+    return s;
+}
+
+struct Item {
+    Seq s;
+    int tile;           // row tile of the sequence
+    int piece, pieces;  // key slice and their number
+    int unit;           // units (of kUnit keys) of a slice
+    int b;
+    int base;  // first item of the sequence
+};
+
+__device__ inline int wave_scan(int v)  // inclusive
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(v, d);
+        v += lane >= d ? o : 0;
+    }
+    return v;
+}
+
+__device__ inline int row_tiles(const AttnArgs &a, const Seq &s, int bm)
+{
+    return (int)(((int64_t)s.nq * a.G + bm - 1) / bm);
+}
+
+__device__ inline int key_units(const Seq &s) { return (s.nk + kUnit - 1) / kUnit; }
+
+// Units per slice so that the items of all sequences are about `target` per key head.
+__device__ inline int slice_units(const AttnArgs &a, int bm, const Seq &mine, int nseq)
+{
+    if (a.target == 0)
+        return 1 << 30;
+    const int lane = threadIdx.x & 63;
+    float work = lane < nseq ? (float)row_tiles(a, mine, bm) * (float)key_units(mine) : 0.f;
+    for (int c = 64; c < nseq; c += 64)
+        if (c + lane < nseq) {
+            const Seq s = load_seq(a, c + lane);
+            work += (float)row_tiles(a, s, bm) * (float)key_units(s);
+        }
+#pragma unroll
+    for (int d = 32; d; d /= 2)
+        work += __shfl_xor(work, d);
+    const float per = ceilf(work / (float)a.target);
+    return max(a.min_units, (int)fminf(per, 1e9f));
+}
+
+__device__ inline int pieces_of(const Seq &s, int unit) { return max(1, (key_units(s) + unit - 1) / unit); }
+
+// Item `id` (of one key head), or tile `id` when `by_tile`; false: there are fewer.
+__device__ inline bool find_item(const AttnArgs &a, int bm, int id, bool by_tile, Item &it)
+{
+    const int lane = threadIdx.x & 63;
+    const int nseq = a.shared ? 1 : a.B;
+    Seq mine = {0, 0, 0, 0};
+    if (lane < nseq)
+        mine = load_seq(a, lane);
+    it.unit = uniform(slice_units(a, bm, mine, nseq));
+    int tiles_before = 0, items_before = 0;
+    for (int c = 0; c < nseq; c += 64) {
+        if (c)
+            mine = c + lane < nseq ? load_seq(a, c + lane) : Seq{0, 0, 0, 0};
+        const int tiles = row_tiles(a, mine, bm), items = tiles * pieces_of(mine, it.unit);
+        const int ti = wave_scan(tiles), ii = wave_scan(items);
+        const int key = by_tile ? tiles_before + ti : items_before + ii;
+        const uint64_t past = __ballot(key > id);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            it.s.q0 = __builtin_amdgcn_readlane(mine.q0, l);
+            it.s.nq = __builtin_amdgcn_readlane(mine.nq, l);
+            it.s.k0 = __builtin_amdgcn_readlane(mine.k0, l);
+            it.s.nk = __builtin_amdgcn_readlane(mine.nk, l);
+            it.b = c + l;
+            it.base = items_before + __builtin_amdgcn_readlane(ii - items, l);
+            const int tbase = tiles_before + __builtin_amdgcn_readlane(ti - tiles, l);
+            it.pieces = uniform(pieces_of(it.s, it.unit));
+            const int n = row_tiles(a, it.s, bm);
+            if (by_tile) {
+                it.tile = id - tbase;
+                it.piece = 0;
+            } else {
+                // later tiles of a prompt see more keys: they come first
+                it.tile = n - 1 - (id - it.base) / it.pieces;
+                it.piece = (id - it.base) % it.pieces;
+            }
+            return true;
+        }
+        tiles_before += __builtin_amdgcn_readlane(ti, 63);
+        items_before += __builtin_amdgcn_readlane(ii, 63);
+    }
+    return false;
+}
+
+// The item index of slice 0 of a tile (see find_item).
+__device__ inline int first_item(const AttnArgs &a, const Item &it, int bm)
+{
+    return it.base + (row_tiles(a, it.s, bm) - 1 - it.tile) * it.pieces;
+}
+
+// Keys that row r of a sequence sees: [0, limit).
+__device__ inline int row_limit(const AttnArgs &a, const Seq &s, int token)
+{
+    return a.causal ? max(0, s.nk - s.nq + token + 1) : s.nk;
+}
+
+// 16-byte chunk of a row's chunk c in LDS. Rows of 16 chunks or more: sixteen successive rows put
+// their chunk c in sixteen places (the S^T operand reads a column of 32 rows), and four successive
+// rows put theirs in different groups of four (the V^T operand reads 64 bytes of four rows at once).
+// Rows of eight chunks lie two to a 256-byte line, and do the same with one bit less.
+template <int DP>
+__device__ inline int swizzle(int row)
+{
+    return DP >= 128 ? ((row & 3) << 2 | (row >> 2 & 3)) : ((row >> 1 & 1) << 2 | (row >> 2 & 3));
+}
+
+__device__ inline const char *key_base(const AttnArgs &a, const Seq &s, int head, bool value)
+{
+    const char *p = static_cast<const char *>(value ? a.v : a.k);
+    const int64_t row = value ? a.v_row : a.k_row, hd = value ? a.v_head : a.k_head;
+    return p + 2 * ((int64_t)s.k0 * row + (int64_t)head * hd);
+}
+
+// A buffer over `rows` rows of D values from p, rows row_bytes apart; reads outside give 0.
+__device__ inline __amdgpu_buffer_rsrc_t rows_buffer(const char *p, int rows, int row_bytes, int D)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), (short)0,
+                                             rows > 0 ? (rows - 1) * row_bytes + 2 * D : 0, kBufferWord3);
+}
+
+// Direct load of 16 bytes per lane to LDS at dst + 16 * lane.
+__device__ inline void load_lds16(__amdgpu_buffer_rsrc_t from, char *dst, uint32_t offset)
+{
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the 16-byte form
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)dst, 16, offset, 0, 0, 0);
+#endif
+}
+
+// ------------------------------------------------------------------------- prompt kernel
+//
+// k_attn_tile: 128 rows of a sequence against a slice of its keys, 64 at a time. Each of four waves
+// holds 32 rows (32x32x16 MFMA); K and V blocks go to LDS by direct loads, the next block's while
+// this one is multiplied (two buffers each, one barrier per block).
+
+constexpr int kTileRows = 128, kTileKeys = 64;
+
+template <typename E, int DP, bool PART, bool WIDE>
+__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
+{
+    using V8 = typename Elem<E>::v8;
+    constexpr int CPR = DP / 8;                          // 16-byte chunks of a row
+    constexpr int NS = DP / 16, ND = DP / 32;            // MFMA steps over D, 32-wide tiles of D
+    constexpr int LOADS = kTileKeys * CPR / 256;         // direct loads per wave and block
+    __shared__ __attribute__((aligned(1024))) char kbuf0[kTileKeys * DP * 2], kbuf1[kTileKeys * DP * 2];
+    __shared__ __attribute__((aligned(1024))) char vbuf0[kTileKeys * DP * 2], vbuf1[kTileKeys * DP * 2];
+    __shared__ int poison;  // a masked block of V held an infinity or NaN
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int col = lane & 31, h = lane >> 5;
+    const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+    Item it;
+    if (!find_item(a, kTileRows, id, false, it))
+        return;
+    const Seq s = it.s;
+
+    // this lane's row
+    const int rows = s.nq * a.G;
+    const int row = it.tile * kTileRows + 32 * wave + col;
+    const int token = row / a.G, qh = head * a.G + row % a.G;
+    const bool live = row < rows;
+    const int limit = live ? row_limit(a, s, token) : 0;
+    // the keys of the tile, and those that every live row of the wave sees
+    const int last = min(rows, (it.tile + 1) * kTileRows) - 1;
+    const int lo = (int)min((int64_t)it.piece * it.unit * kUnit, (int64_t)s.nk);
+    const int hi = min((int)min((int64_t)(it.piece + 1) * it.unit * kUnit, (int64_t)s.nk), row_limit(a, s, last / a.G));
+    const int first = it.tile * kTileRows + 32 * wave;
+    const int wfull = first < rows ? row_limit(a, s, first / a.G) : 0;
+    const int gfull = row_limit(a, s, it.tile * kTileRows / a.G);  // keys that every row of the tile sees
+    const int wmost = first < rows ? row_limit(a, s, min(rows - 1, first + 31) / a.G) : 0;
+
+    // Q^T operands: lane (col, h) holds values 16 st + 8 h .. + 7 of its row
+    V8 qf[NS];
+    {
+        const char *p = static_cast<const char *>(a.q) + 2 * ((int64_t)(s.q0 + token) * a.q_row + (int64_t)qh * a.q_head);
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            u32x4 x = {0, 0, 0, 0};
+            if (live && 16 * st + 8 * h < a.D)
+                x = *reinterpret_cast<const u32x4 *>(p + 2 * (16 * st + 8 * h));
+            qf[st] = __builtin_bit_cast(V8, x);
+        }
+    }
+
+    // direct loads: chunk L of a block (row L / CPR, place L % CPR) receives the row's chunk
+    // place ^ swizzle(row)
+    const int krow_bytes = (int)(2 * a.k_row), vrow_bytes = (int)(2 * a.v_row);
+    uint32_t koff[LOADS], voff[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int L = (wave * LOADS + i) * 64 + lane, r = L / CPR, c = (L % CPR) ^ swizzle<DP>(r);
+        const bool in = c * 8 < a.D;
+        koff[i] = in ? (uint32_t)(r * krow_bytes + c * 16) : kOutside;
+        voff[i] = in ? (uint32_t)(r * vrow_bytes + c * 16) : kOutside;
+    }
+    const char *kp = key_base(a, s, head, false), *vp = key_base(a, s, head, true);
+    auto issue = [&](int key, char *kd, char *vd) {
+        const int n = min(kTileKeys, s.nk - key);
+        const __amdgpu_buffer_rsrc_t kr = rows_buffer(kp + (int64_t)key * krow_bytes, n, krow_bytes, a.D);
+        const __amdgpu_buffer_rsrc_t vr = rows_buffer(vp + (int64_t)key * vrow_bytes, n, vrow_bytes, a.D);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            load_lds16(kr, kd + (wave * LOADS + i) * 1024, koff[i]);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            load_lds16(vr, vd + (wave * LOADS + i) * 1024, voff[i]);
+    };
+
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[d][i] = 0.f;
+    float m = -INFINITY, l = 0.f;  // l: this lane's keys only until the end
+    const float c2 = a.scale_log2;
+
+    // V^T operand address parts: lane i of 16 reads 8 bytes of row i / 4 of its 4 x 16 block
+    const int tr_row = 4 * h + (lane & 15) / 4, tr_col = (lane >> 4 & 1) * 32 + (lane & 3) * 8;  // bytes
+    auto v_frag = [&](const char *vb, int dt, int t) {
+        u32x4 x;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+            const int r = 16 * t + 8 * jj + tr_row;
+            const int byte = dt * 64 + tr_col;
+            const char *p = vb + r * (DP * 2) + (((byte >> 4) ^ swizzle<DP>(r)) << 4) + (byte & 15);
+            const u32x2 half = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+            x[2 * jj] = half[0];
+            x[2 * jj + 1] = half[1];
+        }
+        return x;
+    };
+
+    auto block = [&](int key, const char *kb, const char *vb) {
+        if (key >= wmost)
+            return;  // nothing of it is seen by this wave
+        f32x16 sc[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sc[b][i] = 0.f;
+            const int r = 32 * b + col;
+            const char *p = kb + r * (DP * 2);
+            const int sw = swizzle<DP>(r);
+#pragma unroll
+            for (int st = 0; st < NS; ++st) {
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(p + (((2 * st + h) ^ sw) << 4));
+                sc[b] = Elem<E>::mma32(__builtin_bit_cast(V8, x), qf[st], sc[b]);
+            }
+        }
+        // register i of block b: key + 32 b + 8 (i / 4) + 4 h + i % 4
+        const bool masked = key + kTileKeys > wfull;
+        if (masked) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (key + 32 * b + 8 * (i / 4) + 4 * h + i % 4 >= limit)
+                        sc[b][i] = -INFINITY;
+        }
+        float mx = sc[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                mx = fmaxf(mx, sc[b][i]);
+        mx = fmaxf(mx, other_half(mx));
+        if (__any((mx - m) * c2 > kRescale || (m == -INFINITY && mx > -INFINITY))) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.f : exp2_fast((m - mn) * c2);
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] *= f;
+            m = mn;
+        }
+        const float ref = m == -INFINITY ? 0.f : m * c2;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                sc[b][i] = exp2_fast(__builtin_fmaf(sc[b][i], c2, -ref));
+                l += sc[b][i];
+            }
+        // P^T operands: slot j of step t is register 8 (t % 2) + j of block t / 2
+        u32x4 pf[4], pr[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p0 = sc[t / 2][8 * (t % 2) + 2 * j], p1 = sc[t / 2][8 * (t % 2) + 2 * j + 1];
+                pf[t][j] = pack2<E>(p0, p1);
+                if constexpr (WIDE) {
+                    const f32x2 back = unpack2<E>(pf[t][j]);
+                    pr[t][j] = pack2<E>(p0 - back[0], p1 - back[1]);
+                }
+            }
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const V8 x = __builtin_bit_cast(V8, v_frag(vb, d, t));
+                o[d] = Elem<E>::mma32(x, __builtin_bit_cast(V8, pf[t]), o[d]);
+                if constexpr (WIDE)
+                    o[d] = Elem<E>::mma32(x, __builtin_bit_cast(V8, pr[t]), o[d]);
+            }
+    };
+
+    // This wave's loads have arrived and its reads of the other buffer are done; then all waves'.
+    auto arrive = [] {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // Masked block of V: infinities and NaNs to 0, by the whole workgroup.
+    auto clean = [&](int key, char *vb) {
+        if (key + kTileKeys <= gfull)
+            return;
+#pragma unroll
+        for (int i = 0; i < kTileKeys * CPR / 256; ++i) {
+            u32x4 *p = reinterpret_cast<u32x4 *>(vb + (i * 256 + threadIdx.x) * 16);
+            const u32x4 x = *p;
+            if (not_finite<E>(x[0]) || not_finite<E>(x[1]) || not_finite<E>(x[2]) || not_finite<E>(x[3])) {
+                *p = u32x4{finite_part<E>(x[0]), finite_part<E>(x[1]), finite_part<E>(x[2]), finite_part<E>(x[3])};
+                poison = 1;
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    if (threadIdx.x == 0)
+        poison = 0;
+    if (lo < hi) {
+        issue(lo, kbuf0, vbuf0);
+        for (int key = lo; key < hi; key += 2 * kTileKeys) {
+            arrive();
+            if (key + kTileKeys < hi)
+                issue(key + kTileKeys, kbuf1, vbuf1);
+            clean(key, vbuf0);
+            block(key, kbuf0, vbuf0);
+            if (key + kTileKeys >= hi)
+                break;
+            arrive();
+            if (key + 2 * kTileKeys < hi)
+                issue(key + 2 * kTileKeys, kbuf0, vbuf0);
+            clean(key + kTileKeys, vbuf1);
+            block(key + kTileKeys, kbuf1, vbuf1);
+        }
+    }
+    __syncthreads();
+    if (__builtin_expect(poison, 0)) {
+        // The cleaned blocks again, from memory: what they lost goes to the rows that see it.
+        const int from = lo + max(0, gfull - lo) / kTileKeys * kTileKeys;
+        for (int key = from; key < min(hi, limit); ++key) {
+            const char *p = vp + (int64_t)key * vrow_bytes;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int e = 32 * d + 8 * (i / 4) + 4 * h + i % 4;
+                    if (e < a.D) {
+                        const float x = (float)reinterpret_cast<const E *>(p)[e];
+                        if (!(fabsf(x) < INFINITY))
+                            o[d][i] += x;
+                    }
+                }
+        }
+    }
+
+    l += other_half(l);
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
+    const float lse = l == 0.f ? -INFINITY : m * c2 * kLn2 + logf(l);
+    if (!live)
+        return;
+    const bool part = PART && (a.pieced || it.pieces > 1);
+    if (part) {
+        const int64_t slot = blockIdx.x;
+        const int r = 32 * wave + col;
+        float *dst = a.ws_o + (slot * kTileRows + r) * a.D;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int e = 32 * d + 8 * b + 4 * h;
+                if (e < a.D) {
+                    const float x[4] = {o[d][4 * b] * inv, o[d][4 * b + 1] * inv, o[d][4 * b + 2] * inv,
+                                        o[d][4 * b + 3] * inv};
+                    store4(dst + e, x);
+                }
+            }
+        if (h == 0)
+            a.ws_l[slot * kTileRows + r] = lse;
+        return;
+    }
+    const int64_t at = (int64_t)(s.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int e = 32 * d + 8 * b + 4 * h;
+            if (e < a.D) {
+                const float x[4] = {o[d][4 * b] * inv, o[d][4 * b + 1] * inv, o[d][4 * b + 2] * inv,
+                                    o[d][4 * b + 3] * inv};
+                if constexpr (WIDE)
+                    store4(static_cast<float *>(a.out) + at + e, x);
+                else
+                    store4(static_cast<E *>(a.out) + at + e, x);
+            }
+        }
+    if (a.lse && h == 0)
+        a.lse[(int64_t)(s.q0 + token) * a.Hq + qh] = lse;
+}
+
+// -------------------------------------------------------------------- few-rows kernel
+//
+// k_attn_few: 16 rows (a decode step's heads of one group, a short draft) against a slice of their
+// keys; bound by the bytes of K and V. Each of four waves takes every fourth block of 32 keys on its
+// own: K goes from memory straight into the registers of the S^T operand (16x16x32 MFMA: lane (r, g)
+// holds 16 bytes of key r), V through a private piece of LDS for the transposing read, and the next
+// block's loads are issued before this block is used, so that no barrier and no other wave is waited
+// for until the four partial results are joined at the end.
+
+constexpr int kFewRows = 16, kFewKeys = 32, kFewWaves = 4;
+
+template <typename E, int DP, bool WIDE>
+__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
+{
+    using V8 = typename Elem<E>::v8;
+    constexpr int CPR = DP / 8;
+    constexpr int NS = DP / 32, ND = DP / 16;
+    constexpr int LOADS = kFewKeys * CPR / 64;  // 16-byte V loads per lane and block
+    constexpr int kVBytes = kFewKeys * DP * 2;
+    static_assert(kVBytes >= kFewRows * DP * 4, "the waves' partial outputs reuse the V blocks");
+    __shared__ __attribute__((aligned(1024))) char vlds[kFewWaves][kVBytes];
+    __shared__ float stat[kFewWaves][2][kFewRows];
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+    Item it;
+    if (!find_item(a, kFewRows, id, false, it))
+        return;
+    const Seq s = it.s;
+    const int rows = s.nq * a.G;
+    const int row = it.tile * kFewRows + col;
+    const int token = row / a.G, qh = head * a.G + row % a.G;
+    const bool live = row < rows;
+    const int limit = live ? row_limit(a, s, token) : 0;
+    const int first = it.tile * kFewRows, last = min(rows, first + kFewRows) - 1;
+    const int lo = (int)min((int64_t)it.piece * it.unit * kUnit, (int64_t)s.nk);
+    const int hi = min((int)min((int64_t)(it.piece + 1) * it.unit * kUnit, (int64_t)s.nk), row_limit(a, s, last / a.G));
+    const int wfull = row_limit(a, s, first / a.G);
+
+    V8 qf[NS];
+    {
+        const char *p = static_cast<const char *>(a.q) + 2 * ((int64_t)(s.q0 + token) * a.q_row + (int64_t)qh * a.q_head);
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            u32x4 x = {0, 0, 0, 0};
+            if (live && 32 * st + 8 * g < a.D)
+                x = *reinterpret_cast<const u32x4 *>(p + 2 * (32 * st + 8 * g));
+            qf[st] = __builtin_bit_cast(V8, x);
+        }
+    }
+    const int krow_bytes = (int)(2 * a.k_row), vrow_bytes = (int)(2 * a.v_row);
+    const char *kp = key_base(a, s, head, false), *vp = key_base(a, s, head, true);
+    uint32_t koff[NS], voff[LOADS];
+#pragma unroll
+    for (int st = 0; st < NS; ++st)
+        koff[st] = 32 * st + 8 * g < a.D ? (uint32_t)(col * krow_bytes + 64 * st + 16 * g) : kOutside;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int L = i * 64 + lane, r = L / CPR, c = L % CPR;
+        voff[i] = c * 8 < a.D ? (uint32_t)(r * vrow_bytes + c * 16) : kOutside;
+    }
+    struct Block {
+        u32x4 k[2][NS], v[LOADS];
+    };
+    auto fetch = [&](int key, Block &x) {
+        const int n = s.nk - key;  // <= 0: nothing is read
+        const __amdgpu_buffer_rsrc_t kr = rows_buffer(kp + (int64_t)key * krow_bytes, min(kFewKeys, n), krow_bytes, a.D);
+        const __amdgpu_buffer_rsrc_t vr = rows_buffer(vp + (int64_t)key * vrow_bytes, min(kFewKeys, n), vrow_bytes, a.D);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int st = 0; st < NS; ++st)
+                x.k[b][st] = __builtin_amdgcn_raw_buffer_load_b128(
+                    kr, koff[st] == kOutside ? kOutside : koff[st] + b * 16 * krow_bytes, 0, 0);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            x.v[i] = __builtin_amdgcn_raw_buffer_load_b128(vr, voff[i], 0, 0);
+    };
+
+    f32x4 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+        o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    const float c2 = a.scale_log2;
+    char *vb = vlds[wave];
+    const int tr_row = 4 * g + (lane & 15) / 4, tr_col = (lane & 3) * 8;
+    auto v_frag = [&](int dt) {
+        u32x4 x;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+            const int r = 16 * jj + tr_row;
+            const int byte = dt * 32 + tr_col;
+            const char *p = vb + r * (DP * 2) + (((byte >> 4) ^ swizzle<DP>(r)) << 4) + (byte & 15);
+            const u32x2 half = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+            x[2 * jj] = half[0];
+            x[2 * jj + 1] = half[1];
+        }
+        return x;
+    };
+    bool poison = false;  // a masked block of V held an infinity or NaN
+    auto block = [&](int key, Block &x) {
+        f32x4 sc[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            sc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < NS; ++st)
+                sc[b] = Elem<E>::mma16(__builtin_bit_cast(V8, x.k[b][st]), qf[st], sc[b]);
+        }
+        // register i of block b: key + 16 b + 4 g + i
+        const bool masked = key + kFewKeys > wfull;
+        if (masked) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (key + 16 * b + 4 * g + i >= limit)
+                        sc[b][i] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                if (not_finite<E>(x.v[i][0]) || not_finite<E>(x.v[i][1]) || not_finite<E>(x.v[i][2]) ||
+                    not_finite<E>(x.v[i][3])) {
+                    poison = true;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x.v[i][j] = finite_part<E>(x.v[i][j]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int L = i * 64 + lane, r = L / CPR, c = (L % CPR) ^ swizzle<DP>(r);
+            *reinterpret_cast<u32x4 *>(vb + r * (DP * 2) + c * 16) = x.v[i];
+        }
+        float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                         fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        if (__any((mx - m) * c2 > kRescale || (m == -INFINITY && mx > -INFINITY))) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.f : exp2_fast((m - mn) * c2);
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                o[d] *= f;
+            m = mn;
+        }
+        const float ref = m == -INFINITY ? 0.f : m * c2;
+        u32x4 pf, pr;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sc[b][i] = exp2_fast(__builtin_fmaf(sc[b][i], c2, -ref));
+                l += sc[b][i];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                pf[2 * b + j] = pack2<E>(sc[b][2 * j], sc[b][2 * j + 1]);
+                if constexpr (WIDE) {
+                    const f32x2 back = unpack2<E>(pf[2 * b + j]);
+                    pr[2 * b + j] = pack2<E>(sc[b][2 * j] - back[0], sc[b][2 * j + 1] - back[1]);
+                }
+            }
+        }
+        // This wave's LDS writes before its reads: LDS operations of a wave complete in order, so
+        // only the compiler has to keep them so.
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            const V8 v = __builtin_bit_cast(V8, v_frag(d));
+            o[d] = Elem<E>::mma16(v, __builtin_bit_cast(V8, pf), o[d]);
+            if constexpr (WIDE)
+                o[d] = Elem<E>::mma16(v, __builtin_bit_cast(V8, pr), o[d]);
+        }
+        asm volatile("" ::: "memory");
+    };
+
+    constexpr int kStride = kFewWaves * kFewKeys;
+    const int k0 = lo + wave * kFewKeys;
+    if (k0 < hi) {
+        Block x, y;
+        fetch(k0, x);
+        for (int key = k0; key < hi; key += 2 * kStride) {
+            fetch(key + kStride, y);
+            block(key, x);
+            if (key + kStride >= hi)
+                break;
+            fetch(key + 2 * kStride, x);
+            block(key + kStride, y);
+        }
+    }
+    if (__builtin_expect(__any(poison), 0)) {
+        // The cleaned blocks again, from memory: what they lost goes to the rows that see it.
+        for (int key = k0; key < hi; key += kStride) {
+            if (key + kFewKeys <= wfull)
+                continue;
+            for (int j = key; j < min(min(key + kFewKeys, hi), limit); ++j) {
+                const E *p = reinterpret_cast<const E *>(vp + (int64_t)j * vrow_bytes);
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int e = 16 * d + 4 * g + i;
+                        if (e < a.D) {
+                            const float v = (float)p[e];
+                            if (!(fabsf(v) < INFINITY))
+                                o[d][i] += v;
+                        }
+                    }
+            }
+        }
+    }
+
+    // join the four waves: common maximum, then the sums
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+        stat[wave][0][col] = m;
+        stat[wave][1][col] = l;
+    }
+    __syncthreads();
+    float mall = stat[0][0][col];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w)
+        mall = fmaxf(mall, stat[w][0][col]);
+    float lall = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+        const float mw = stat[w][0][col];
+        lall += mw == -INFINITY ? stat[w][1][col] : stat[w][1][col] * exp2_fast((mw - mall) * c2);  // 0, or NaN scores
+    }
+    const float inv = lall > 0.f ? 1.f / lall : (lall == 0.f ? 0.f : lall);
+    const float f = m == -INFINITY ? inv : exp2_fast((m - mall) * c2) * inv;
+    const float lse = lall == 0.f ? -INFINITY : mall * c2 * kLn2 + logf(lall);
+    // wave's O^T to LDS as [row][D]: 4 values of row col per register group
+    float *mine = reinterpret_cast<float *>(vlds[wave]);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        const f32x4 x = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o[d] * f;
+        *reinterpret_cast<f32x4 *>(mine + col * DP + ((4 * d + g) ^ (col & 7)) * 4) = x;
+    }
+    __syncthreads();
+    const bool part = a.pieced || it.pieces > 1;
+    for (int e = threadIdx.x; e < kFewRows * (DP / 4); e += 256) {
+        const int r = e / (DP / 4), c = e % (DP / 4);
+        const int rr = it.tile * kFewRows + r;
+        if (rr >= rows || c * 4 >= a.D)
+            continue;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w)
+            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(vlds[w]) + r * DP + (c ^ (r & 7)) * 4);
+        const float x[4] = {sum[0], sum[1], sum[2], sum[3]};
+        if (part) {
+            store4(a.ws_o + ((int64_t)blockIdx.x * kFewRows + r) * a.D + 4 * c, x);
+        } else {
+            const int64_t at = (int64_t)(s.q0 + rr / a.G) * a.o_row + (int64_t)(head * a.G + rr % a.G) * a.o_head + 4 * c;
+            if constexpr (WIDE)
+                store4(static_cast<float *>(a.out) + at, x);
+            else
+                store4(static_cast<E *>(a.out) + at, x);
+        }
+    }
+    if (wave == 0 && g == 0 && live) {
+        if (part)
+            a.ws_l[(int64_t)blockIdx.x * kFewRows + col] = lse;
+        else if (a.lse)
+            a.lse[(int64_t)(s.q0 + token) * a.Hq + qh] = lse;
+    }
+}
+
+// ------------------------------------------------------------------------------- joining
+//
+// k_attn_combine: a row's slices, and with a shared prefix the prefix's slices of the same row,
+// joined by their lse: out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max). One workgroup
+// per (row tile, key head) and eight rows; 32 lanes read a row.
+
+template <typename TO>
+__global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, int bm, int pre_bm)
+{
+    const int lane = threadIdx.x & 63;
+    const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+    Item it;
+    if (!find_item(a, bm, id, true, it))
+        return;
+    const bool shared = pre.shared;
+    if (!shared && it.pieces == 1)
+        return;  // written by its one item
+    const int rows = it.s.nq * a.G;
+    const int r = blockIdx.y * 8 + threadIdx.x / 32;
+    const int row = it.tile * bm + r;
+    const int slot = first_item(a, it, bm);
+    if (slot + it.pieces > a.items)
+        return;  // more tiles than sequences that do not overlap can have: not computed
+    // the prefix's items of this row
+    int pslot = 0, pn = 0, prow = 0;
+    if (shared) {
+        Item p;
+        find_item(pre, pre_bm, 0, true, p);
+        const int all = it.s.q0 * pre.G + row;  // T * heads < 2^31
+        p.tile = min(all, pre.T * pre.G - 1) / pre_bm;
+        prow = all % pre_bm;
+        pslot = first_item(pre, p, pre_bm);
+        pn = p.pieces;
+    }
+    if (r >= bm || row >= rows)
+        return;
+    const int n = it.pieces + pn, l32 = lane & 31;
+    auto lse_at = [&](int i) {
+        return i < it.pieces ? a.ws_l[((int64_t)(slot + i) * a.Hkv + head) * bm + r]
+                             : pre.ws_l[((int64_t)(pslot + i - it.pieces) * a.Hkv + head) * pre_bm + prow];
+    };
+    auto out_at = [&](int i) {
+        return i < it.pieces ? a.ws_o + (((int64_t)(slot + i) * a.Hkv + head) * bm + r) * a.D
+                             : pre.ws_o + (((int64_t)(pslot + i - it.pieces) * a.Hkv + head) * pre_bm + prow) * a.D;
+    };
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int i = l32; i < n; i += 32) {
+        const float v = lse_at(i);
+        nan = nan || v != v;
+        mx = fmaxf(mx, v);
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+        mx = fmaxf(mx, __shfl_xor(mx, d));
+        nan = __shfl_xor((int)nan, d) || nan;
+    }
+    const int token = row / a.G, qh = head * a.G + row % a.G;
+    const int64_t at = (int64_t)(it.s.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
+    float total = 0.f;
+    for (int c = 4 * l32; c < a.D; c += 128) {
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        total = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float v = lse_at(i);
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(out_at(i) + c);
+            if (v != -INFINITY) {  // an empty slice: its out is 0 as well
+                const float w = mx == INFINITY ? 1.f : expf(v - mx);
+                total += w;
+                sum += x * w;
+            }
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const float y[4] = {sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv};
+        store4(static_cast<TO *>(a.out) + at + c, y);
+    }
+    if (a.lse && l32 == 0)
+        a.lse[(int64_t)(it.s.q0 + token) * a.Hq + qh] = nan ? NAN : mx == -INFINITY ? -INFINITY : mx + logf(total);
+}
+
+// --------------------------------------------------------------------------------- plans
+
+template <typename E, int DP, bool WIDE>
+hipError_t run_part(const AttnArgs &a, const AttnPart &p, hipStream_t s)
+{
+    const unsigned grid = (unsigned)(p.items * a.Hkv);
+    if (p.bm == kFewRows)
+        k_attn_few<E, DP, WIDE><<<grid, 256, 0, s>>>(a);
+    else if (p.target)
+        k_attn_tile<E, DP, true, WIDE><<<grid, 256, 0, s>>>(a);
+    else
+        k_attn_tile<E, DP, false, WIDE><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename E, bool WIDE>
+hipError_t run_dim(const AttnArgs &a, const AttnPart &p, hipStream_t s)
+{
+    if (a.D <= 64)
+        return run_part<E, 64, WIDE>(a, p, s);
+    if (a.D <= 128)
+        return run_part<E, 128, WIDE>(a, p, s);
+    return run_part<E, 256, WIDE>(a, p, s);
+}
+
+hipError_t run_type(const AttnArgs &a, const AttnPart &p, int type, int out_type, hipStream_t s)
+{
+    const bool wide = out_type == kF32;
+    if (type == kBF16)
+        return wide ? run_dim<bf16_t, true>(a, p, s) : run_dim<bf16_t, false>(a, p, s);
+    return wide ? run_dim<f16_t, true>(a, p, s) : run_dim<f16_t, false>(a, p, s);
+}
+
+AttnPart plan_part(int64_t rows, int64_t seqs, int64_t Hkv, bool always)  // seqs: with rows of their own
+{
+    AttnPart p;
+    // mean rows of a sequence: up to 16, one small tile each
+    p.bm = rows <= kFewRows * seqs ? kFewRows : kTileRows;
+    p.tiles = rows / p.bm + seqs;  // upper bound of sum of ceil(rows_b / bm)
+    const int64_t target = (512 + Hkv - 1) / Hkv;
+    p.target = p.bm == kFewRows || always || p.tiles < target ? target : 0;
+    p.min_units = 2;
+    // sum of tiles * ceil(units / slice) <= work / slice + tiles, work / slice <= target up to the
+    // rounding of the fp32 sum
+    p.items = p.tiles + (p.target ? p.target + 8 : 0);
+    return p;
+}
+
+}  // namespace
+
+AttnPlan attn_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t P)
+{
+    AttnPlan p{};
+    const int64_t rows = T * (Hq / Hkv);
+    p.main = plan_part(rows, B < T ? B : T, Hkv, P > 0);
+    p.main.o_off = 0;
+    auto slots = [&](const AttnPart &x) { return x.target ? x.items * Hkv * x.bm : (int64_t)0; };
+    int64_t at = round_up(slots(p.main) * D * 4, 256);
+    p.main.l_off = at;
+    at += round_up(slots(p.main) * 4, 256);
+    if (P > 0) {
+        p.pre = plan_part(rows, 1, Hkv, true);
+        p.pre.o_off = at;
+        at += round_up(slots(p.pre) * D * 4, 256);
+        p.pre.l_off = at;
+        at += round_up(slots(p.pre) * 4, 256);
+    }
+    p.bytes = (size_t)at;
+    return p;
+}
+
+hipError_t launch_attention(const AttnArgs &args, const AttnArgs &prefix, const AttnPlan &p, int type, int out_type,
+                            hipStream_t s)
+{
+    AttnArgs a = args, pre = prefix;
+    char *ws = reinterpret_cast<char *>(args.ws_o);
+    a.target = (int)p.main.target;
+    a.items = (int)p.main.items;
+    a.min_units = p.main.min_units;
+    a.ws_o = reinterpret_cast<float *>(ws + p.main.o_off);
+    a.ws_l = reinterpret_cast<float *>(ws + p.main.l_off);
+    a.pieced = prefix.shared;
+    if (prefix.shared) {
+        pre.target = (int)p.pre.target;
+        pre.items = (int)p.pre.items;
+        pre.min_units = p.pre.min_units;
+        pre.ws_o = reinterpret_cast<float *>(ws + p.pre.o_off);
+        pre.ws_l = reinterpret_cast<float *>(ws + p.pre.l_off);
+        pre.pieced = 1;
+        if (hipError_t e = run_type(pre, p.pre, type, out_type, s))
+            return e;
+    }
+    if (hipError_t e = run_type(a, p.main, type, out_type, s))
+        return e;
+    if (!p.main.target)
+        return hipSuccess;
+    const dim3 grid((unsigned)(p.main.tiles * a.Hkv), (unsigned)(p.main.bm / 8));
+    if (out_type == kF32)
+        k_attn_combine<float><<<grid, 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
+    else if (type == kBF16)
+        k_attn_combine<bf16_t><<<grid, 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
+    else
+        k_attn_combine<f16_t><<<grid, 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
+    return hipGetLastError();
+}
+
+}  // namespace bt

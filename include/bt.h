@@ -457,6 +457,51 @@ bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int
                           int32_t interleaved, const int32_t *rows, int64_t kv_rows, void *q, void *k, void *v,
                           int32_t out_type, const int64_t *strides, void *stream);
 
+/*
+ * bt_attention -- softmax attention over packed sequences with grouped heads: whole prompts,
+ * prompts continued behind cached keys, decode steps over a cache, and batches that share a
+ * prefix. Query head h reads key head h / (heads / kv_heads).
+ *   sequence b   its queries are rows q_start[b] .. q_start[b+1] - 1 of q (n of them); its keys
+ *                and values are rows k_start[b] .. k_start[b] + k_len[b] - 1 of k and v (packed
+ *                prompts, or any rows of a cache; sequences may share rows). q_start [seqs + 1],
+ *                k_start and k_len [seqs]: int32 on the device. The q ranges must not overlap;
+ *                ranges that leave the arrays are cut to them.
+ *   causal       != 0: query i of n sees keys j <= k_len - n + i (the last query sees all);
+ *                0: every query sees all k_len keys.
+ *   out          row t, head h: sum_j softmax(scale * q . k)_j v_j over the keys seen; 0 when
+ *                there are none. Rows of q that belong to no sequence are not written.
+ *   lse          [tokens, heads] fp32 or NULL: ln sum_j exp(scale * q . k_j); -inf for no keys.
+ *   prefix       > 0: every query also sees all `prefix` rows of prefix_k / prefix_v, ahead of its
+ *                sequence's own keys; they are read once for all of the batch's queries.
+ * type: BT_BF16 or BT_F16, of q, k, v and the prefix; out_type: the same or BT_F32. Scores,
+ * statistics and sums are fp32; probabilities are rounded to `type` for the product with V (with
+ * fp32 outputs they are carried to twice that precision). Results do not depend on timing. Values
+ * of K and V that a query does not see do not reach it, infinities and NaNs included.
+ * head_dim: a multiple of 8 up to BT_ATTENTION_MAX_HEAD_DIM. Strides are in elements; q, k, v and
+ * the prefix: 16-byte aligned with strides multiples of 8, row strides of k, v and the prefix at
+ * most 2^23; out: aligned to four elements. tokens <= BT_MAX_DIM, tokens * heads < 2^31, scale
+ * finite and positive. out and lse must not overlap the inputs.
+ *   workspace    bt_attention_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim, prefix)
+ *                bytes of device scratch, 256-byte aligned, or NULL when that is 0; contents on
+ *                entry are ignored. Calls sharing one must not overlap.
+ */
+#define BT_ATTENTION_MAX_HEAD_DIM 256
+typedef struct {
+    int64_t tokens, keys, seqs, prefix; /* rows of q; of k and v; sequences; prefix rows */
+    int64_t heads, kv_heads, head_dim;
+    int32_t type, out_type, causal;
+    float scale;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    int64_t prefix_k_row, prefix_k_head, prefix_v_row, prefix_v_head;
+    int64_t out_row, out_head;
+} bt_attention_shape;
+size_t bt_attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads,
+                                    int64_t head_dim, int64_t prefix);
+bt_status bt_attention(const bt_attention_shape *shape, const void *q, const void *k, const void *v,
+                       const int32_t *q_start, const int32_t *k_start, const int32_t *k_len,
+                       const void *prefix_k, const void *prefix_v, void *out, float *lse,
+                       void *workspace, void *stream);
+
 /* Static text for a status code. */
 const char *bt_status_str(bt_status s);
 
