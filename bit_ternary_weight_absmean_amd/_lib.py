@@ -8,16 +8,6 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libbt.so")
 
-class AttentionShape(ctypes.Structure):
-    """bt_attention_shape."""
-
-    _fields_ = ([(n, ctypes.c_int64) for n in ("tokens", "keys", "seqs", "prefix", "heads", "kv_heads", "head_dim")]
-                + [(n, ctypes.c_int32) for n in ("type", "out_type", "causal")] + [("scale", ctypes.c_float)]
-                + [(n, ctypes.c_int64) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head",
-                                                 "prefix_k_row", "prefix_k_head", "prefix_v_row", "prefix_v_head",
-                                                 "out_row", "out_head")])
-
-
 # Every function declared in include/bt.h, with (restype, argtypes).
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 SIGNATURES = {

@@ -7,11 +7,13 @@ returned status. Nothing here computes any part of the method.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
-from ._lib import AttentionShape, check, lib
+from ._lib import check, lib
 
 GEMV_AUTO, GEMV_DOT4, GEMV_MFMA, GEMV_LUT, GEMV_STAGED = 0, 1, 2, 3, 4
 GEMV_MAX_M = 16
@@ -423,11 +425,36 @@ def _need_strided(t, name: str, dtype, shape, device, output: bool = False):
 
 def _call(dev, fn, *args):
     """A library call on ``dev``'s current stream; ``dev`` need not be the current device."""
-    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
-        check(fn(*args, _stream(dev)))
+    if dev.index == _current_device():
+        status = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            check(fn(*args, _stream(dev)))
+            status = fn(*args, _raw_stream(dev.index))
+    if status:
+        check(status)
+
+
+# torch.cuda.current_stream(i).cuda_stream and torch.cuda.current_device() without the objects around
+# them: a decode step's calls are shorter than those take.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _as_is(dev, *tensors):
+    """Whether every (tensor, dtype, shape) is a contiguous tensor of that type and shape on ``dev``: the
+    usual case, in as few steps as possible. Where not, the checks proper say what is wrong (or that a
+    strided tensor is fine)."""
+    for t, dtype, shape in tensors:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+                and t.is_contiguous()):
+            return False
+    return True
+
+
+@lru_cache(maxsize=4096)
+def _workspace_bytes(name: str, *sizes: int) -> int:
+    """A workspace size query of the library (a function of the sizes alone)."""
+    return int(getattr(lib(), name)(*sizes))
 
 
 LORA_MAX_RANK = 256  # BT_LORA_MAX_RANK
@@ -465,8 +492,10 @@ class LoraAdapters:
         _need(self.scale, "scale", torch.float32, (L,), dev)
         if self.ranks is not None:
             _need(self.ranks, "ranks", torch.int32, (L,), dev)
-        arr = None if self.group_rows is None else (ctypes.c_int64 * groups)(*self.group_rows)
-        object.__setattr__(self, "_groups", (arr, groups))
+        arr = None if self.group_rows is None else struct.pack(f"{groups}q", *self.group_rows)
+        for name, value in (("_groups", (arr, groups)), ("_dev", dev), ("_shape", (L, N, R)),
+                            ("_K", self.A.shape[2]), ("_type", _TYPES[self.B.dtype])):
+            object.__setattr__(self, name, value)
 
     @property
     def K(self) -> int:
@@ -483,7 +512,7 @@ class LoraAdapters:
 
 def lora_workspace_bytes(M: int, adapters: LoraAdapters) -> int:
     """bt_lora_workspace_bytes for M tokens."""
-    return int(lib().bt_lora_workspace_bytes(M, adapters.K, adapters.rank, adapters._groups[1]))
+    return _workspace_bytes("bt_lora_workspace_bytes", M, adapters.K, adapters.rank, adapters._groups[1])
 
 
 def lora_workspace(M: int, adapters: LoraAdapters) -> torch.Tensor:
@@ -495,28 +524,31 @@ def lora_apply(X: torch.Tensor, adapters: LoraAdapters, index: torch.Tensor, bas
                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """bt_lora_apply: ``base`` (None: zeros) plus each token's low-rank product. ``index`` [M] int32 names
     the token's adapter (outside [0, L): none). ``out`` may be ``base``. Returns out [M, N] fp32."""
-    B = adapters.B
-    dev = B.device
+    B, dev = adapters.B, adapters._dev
+    (L, N, R), K = adapters._shape, adapters._K
+    arr, groups = adapters._groups
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X must be a tensor [M, K]")
-    M, (L, N, R), K = X.shape[0], B.shape, adapters.A.shape[2]
-    _need(X, "X", torch.float32, (M, K), dev)
-    _need(index, "index", torch.int32, (M,), dev)
-    if base is not None:
-        _need(base, "base", torch.float32, (M, N), dev)
+    M = X.shape[0]
+    f32 = torch.float32
+    if not (_as_is(dev, (X, f32, (M, K)), (index, torch.int32, (M,)))
+            and (base is None or _as_is(dev, (base, f32, (M, N)))) and (out is None or _as_is(dev, (out, f32, (M, N))))):
+        _need(X, "X", f32, (M, K), dev)
+        _need(index, "index", torch.int32, (M,), dev)
+        if base is not None:
+            _need(base, "base", f32, (M, N), dev)
+        if out is not None:
+            _need(out, "out", f32, (M, N), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=dev)
-    else:
-        _need(out, "out", torch.float32, (M, N), dev)
-    arr, groups = adapters._groups
-    need = int(lib().bt_lora_workspace_bytes(M, K, R, groups))
+        out = torch.empty((M, N), dtype=f32, device=dev)
+    need = _workspace_bytes("bt_lora_workspace_bytes", M, K, R, groups)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     else:
         _need_bytes(workspace, "workspace", need, dev)
-    _call(dev, lib().bt_lora_apply, _ptr(adapters.A), _ptr(B), _TYPES[B.dtype], _ptr(adapters.scale),
-          _ptr(adapters.ranks), L, R, None if arr is None else ctypes.addressof(arr), groups, _ptr(index), _ptr(X),
-          _ptr(base), M, N, K, _ptr(out), _ptr(workspace))
+    _call(dev, lib().bt_lora_apply, adapters.A.data_ptr(), B.data_ptr(), adapters._type, adapters.scale.data_ptr(),
+          _ptr(adapters.ranks), L, R, arr, groups, index.data_ptr(), X.data_ptr(), _ptr(base), M, N, K,
+          out.data_ptr(), workspace.data_ptr())
     return out
 
 
@@ -542,23 +574,27 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, inv_freq: to
         raise ValueError(f"qkv must be [M, values], got shape {tuple(qkv.shape)}")
     if heads < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError(f"heads = {heads} must be a positive multiple of kv_heads = {kv_heads}")
-    M, total = qkv.shape[0], heads + 2 * kv_heads
-    if qkv.shape[1] == 0 or qkv.shape[1] % total:
-        raise ValueError(f"qkv rows of {qkv.shape[1]} values are not {total} heads")
-    D, dev = qkv.shape[1] // total, qkv.device
-    _need_strided(qkv, "qkv", qkv.dtype, qkv.shape, dev)
+    (M, values), total, dev = qkv.shape, heads + 2 * kv_heads, qkv.device
+    if values == 0 or values % total:
+        raise ValueError(f"qkv rows of {values} values are not {total} heads")
+    D = values // total
+    if not (_on_device(qkv) and qkv.is_contiguous()):
+        _need_strided(qkv, "qkv", qkv.dtype, qkv.shape, dev)
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
+        if w is not None and not _as_is(dev, (w, torch.float32, (D,))):
             _need(w, name, torch.float32, (D,), dev)
     rot = 0
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be a 1-D tensor of rot_dim / 2 angles")
-        rot = 2 * inv_freq.shape[0]
-        _need(inv_freq, "inv_freq", torch.float64, None, dev)
-        _need(positions, "positions", torch.int32, (M,), dev)
+        half = inv_freq.shape[0]
+        rot = 2 * half
+        if not _as_is(dev, (inv_freq, torch.float64, (half,)), (positions, torch.int32, (M,))):
+            _need(inv_freq, "inv_freq", torch.float64, None, dev)
+            _need(positions, "positions", torch.int32, (M,), dev)
     if rows is not None:
-        _need(rows, "rows", torch.int32, (M,), dev)
+        if not _as_is(dev, (rows, torch.int32, (M,))):
+            _need(rows, "rows", torch.int32, (M,), dev)
         if out is None:
             raise ValueError("rows names rows of the k and v given in out")
     if out is None:
@@ -569,22 +605,26 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, inv_freq: to
         q, k, v = out
     out_type = _type_of(q, "q", _TYPES)
     room = k.shape[0] if rows is not None and isinstance(k, torch.Tensor) and k.dim() == 3 else M
-    _need_strided(q, "q", q.dtype, (M, heads, D), dev, output=True)
-    _need_strided(k, "k", q.dtype, (room, kv_heads, D), dev, output=True)
-    _need_strided(v, "v", q.dtype, (room, kv_heads, D), dev, output=True)
-    strides = (ctypes.c_int64 * 6)(q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1))
-    _call(dev, lib().bt_qk_norm_rope, _ptr(qkv), in_type, qkv.stride(0), M, heads, kv_heads, D, _ptr(q_weight),
-          _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot, int(interleaved), _ptr(rows), room,
-          _ptr(q), _ptr(k), _ptr(v), out_type, ctypes.addressof(strides))
+    dt, kv = q.dtype, (room, kv_heads, D)
+    if not _as_is(dev, (q, dt, (M, heads, D)), (k, dt, kv), (v, dt, kv)):
+        _need_strided(q, "q", dt, (M, heads, D), dev, output=True)
+        _need_strided(k, "k", dt, kv, dev, output=True)
+        _need_strided(v, "v", dt, kv, dev, output=True)
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    _call(dev, lib().bt_qk_norm_rope, qkv.data_ptr(), in_type, qkv.stride(0), M, heads, kv_heads, D, _ptr(q_weight),
+          _ptr(k_weight), eps, _ptr(positions), _ptr(inv_freq), rot, interleaved, _ptr(rows), room, q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), out_type, _SIX.pack(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1]))
     return q, k, v
 
 
+_SIX = struct.Struct("6q")
+_ATTENTION_SHAPE = struct.Struct("7q3if12q")  # bt_attention_shape
 _HALF = {torch.bfloat16: 1, torch.float16: 2}
 
 
 def attention_workspace_bytes(tokens: int, seqs: int, heads: int, kv_heads: int, head_dim: int, prefix: int = 0) -> int:
     """bt_attention_workspace_bytes: the scratch of an attention call (0: none)."""
-    return int(lib().bt_attention_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim, prefix))
+    return _workspace_bytes("bt_attention_workspace_bytes", tokens, seqs, heads, kv_heads, head_dim, prefix)
 
 
 def attention_workspace(q: torch.Tensor, k: torch.Tensor, seqs: int,
@@ -619,12 +659,15 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.
     (T, heads, D), (S, kv_heads), B, dev, dt = q.shape, k.shape[:2], k_len.shape[0], q.device, q.dtype
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
         raise ValueError(f"{heads} heads are not a positive multiple of {kv_heads} key heads")
-    _need_strided(q, "q", dt, q.shape, dev)
-    _need_strided(k, "k", dt, (S, kv_heads, D), dev)
-    _need_strided(v, "v", dt, (S, kv_heads, D), dev)
-    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
-    _need(k_start, "k_start", torch.int32, (B,), dev)
-    _need(k_len, "k_len", torch.int32, (B,), dev)
+    kv, i32 = (S, kv_heads, D), torch.int32
+    if not (_on_device(q) and _as_is(dev, (q, dt, q.shape), (k, dt, kv), (v, dt, kv), (q_start, i32, (B + 1,)),
+                                     (k_start, i32, (B,)), (k_len, i32, (B,)))):
+        _need_strided(q, "q", dt, q.shape, dev)
+        _need_strided(k, "k", dt, kv, dev)
+        _need_strided(v, "v", dt, kv, dev)
+        _need(q_start, "q_start", i32, (B + 1,), dev)
+        _need(k_start, "k_start", i32, (B,), dev)
+        _need(k_len, "k_len", i32, (B,), dev)
     P, pk, pv = 0, (0, 0), (0, 0)
     if (prefix_k is None) != (prefix_v is None):
         raise ValueError("prefix_k and prefix_v come together")
@@ -632,27 +675,31 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.
         if not isinstance(prefix_k, torch.Tensor) or prefix_k.dim() != 3:
             raise ValueError("prefix_k must be a tensor [P, kv_heads, D]")
         P = prefix_k.shape[0]
-        _need_strided(prefix_k, "prefix_k", dt, (P, kv_heads, D), dev)
-        _need_strided(prefix_v, "prefix_v", dt, (P, kv_heads, D), dev)
+        if not _as_is(dev, (prefix_k, dt, (P, kv_heads, D)), (prefix_v, dt, (P, kv_heads, D))):
+            _need_strided(prefix_k, "prefix_k", dt, (P, kv_heads, D), dev)
+            _need_strided(prefix_v, "prefix_v", dt, (P, kv_heads, D), dev)
         pk, pv = prefix_k.stride(), prefix_v.stride()
     if out is None:
         out = torch.empty((T, heads, D), dtype=out_dtype or dt, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    if out.dtype not in (dt, torch.float32):
+    ot = out.dtype
+    if ot is not dt and ot is not torch.float32:
         raise TypeError(f"out must be {dt} or torch.float32, got {out.dtype}")
-    _need_strided(out, "out", out.dtype, (T, heads, D), dev, output=True)
-    if lse is not None:
+    if not _as_is(dev, (out, ot, (T, heads, D))):
+        _need_strided(out, "out", ot, (T, heads, D), dev, output=True)
+    if lse is not None and not _as_is(dev, (lse, torch.float32, (T, heads))):
         _need(lse, "lse", torch.float32, (T, heads), dev)
-    need = attention_workspace_bytes(T, B, heads, kv_heads, D, P)
+    need = _workspace_bytes("bt_attention_workspace_bytes", T, B, heads, kv_heads, D, P)
     if workspace is not None:
         _need_bytes(workspace, "workspace", need, dev)
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
-    shape = AttentionShape(T, S, B, P, heads, kv_heads, D, kind, _TYPES[out.dtype], int(causal),
-                           D ** -0.5 if scale is None else scale, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], pk[0],
-                           pk[1], pv[0], pv[1], os[0], os[1])
-    _call(dev, lib().bt_attention, ctypes.addressof(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(q_start), _ptr(k_start),
-          _ptr(k_len), _ptr(prefix_k), _ptr(prefix_v), _ptr(out), _ptr(lse), _ptr(workspace))
+    shape = _ATTENTION_SHAPE.pack(T, S, B, P, heads, kv_heads, D, kind, _TYPES[ot], causal,
+                                  D ** -0.5 if scale is None else scale, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+                                  pk[0], pk[1], pv[0], pv[1], os[0], os[1])
+    _call(dev, lib().bt_attention, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_start.data_ptr(),
+          k_start.data_ptr(), k_len.data_ptr(), _ptr(prefix_k), _ptr(prefix_v), out.data_ptr(), _ptr(lse),
+          _ptr(workspace))
     return out, lse

@@ -127,6 +127,16 @@ __device__ inline float other_half(float v)  // the value of lane ^ 32
     return __uint_as_float((threadIdx.x & 32) ? p[0] : p[1]);
 }
 
+// op over the lanes l % 16 of the wave, in every lane
+template <typename Op>
+__device__ inline float across_quarters(float v, Op op)
+{
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
 // ---------------------------------------------------------------------------- work items
 
 struct Seq {
@@ -158,14 +168,21 @@ struct Item {
     int base;  // first item of the sequence
 };
 
-__device__ inline int wave_scan(int v)  // inclusive
+// Inclusive sum over the wave's lanes, without LDS: within rows of 16 by row shifts, then the last
+// lane of a row (of two rows) added to the rows behind it.
+template <int CTRL, int ROWS>
+__device__ inline int shifted_in(int v)
 {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(v, d);
-        v += lane >= d ? o : 0;
-    }
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ inline int wave_scan(int v)
+{
+    v += shifted_in<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8
+    v += shifted_in<0x112, 0xF>(v);
+    v += shifted_in<0x114, 0xF>(v);
+    v += shifted_in<0x118, 0xF>(v);
+    v += shifted_in<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+    v += shifted_in<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
     return v;
 }
 
@@ -188,9 +205,9 @@ __device__ inline int slice_units(const AttnArgs &a, int bm, const Seq &mine, in
             const Seq s = load_seq(a, c + lane);
             work += (float)row_tiles(a, s, bm) * (float)key_units(s);
         }
-#pragma unroll
-    for (int d = 32; d; d /= 2)
-        work += __shfl_xor(work, d);
+    work = __uint_as_float(wave_reduce_bits(__float_as_uint(work), [](uint32_t x, uint32_t y) {
+        return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+    }));
     const float per = ceilf(work / (float)a.target);
     return max(a.min_units, (int)fminf(per, 1e9f));
 }
@@ -202,6 +219,17 @@ __device__ inline bool find_item(const AttnArgs &a, int bm, int id, bool by_tile
 {
     const int lane = threadIdx.x & 63;
     const int nseq = a.shared ? 1 : a.B;
+    if (nseq == 1) {  // nothing to search
+        it.s = load_seq(a, 0);
+        it.b = it.base = 0;
+        const int n = row_tiles(a, it.s, bm);
+        const float work = (float)n * (float)key_units(it.s);
+        it.unit = a.target ? max(a.min_units, (int)fminf(ceilf(work / (float)a.target), 1e9f)) : 1 << 30;
+        it.pieces = pieces_of(it.s, it.unit);
+        it.tile = by_tile ? id : n - 1 - id / it.pieces;
+        it.piece = by_tile ? 0 : id % it.pieces;
+        return it.tile >= 0 && it.tile < n;
+    }
     Seq mine = {0, 0, 0, 0};
     if (lane < nseq)
         mine = load_seq(a, lane);
@@ -710,8 +738,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
         }
         float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
                          fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx = across_quarters(mx, [](float x, float y) { return fmaxf(x, y); });
         if (__any((mx - m) * c2 > kRescale || (m == -INFINITY && mx > -INFINITY))) {
             const float mn = fmaxf(m, mx);
             const float f = mn == -INFINITY ? 1.f : exp2_fast((m - mn) * c2);
@@ -789,8 +816,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
     }
 
     // join the four waves: common maximum, then the sums
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
+    l = across_quarters(l, [](float x, float y) { return x + y; });
     if (g == 0) {
         stat[wave][0][col] = m;
         stat[wave][1][col] = l;
@@ -849,13 +875,17 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
 // ------------------------------------------------------------------------------- joining
 //
 // k_attn_combine: a row's slices, and with a shared prefix the prefix's slices of the same row,
-// joined by their lse: out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max). One workgroup
-// per (row tile, key head) and eight rows; 32 lanes read a row.
+// joined by their lse: out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max). 32 lanes read a
+// row; GP such groups share a row's slices (every GP-th each, four in flight) and are joined in LDS.
+// Latency is all there is to it, so where a row has many slices GP is 8.
 
-template <typename TO>
+template <typename TO, int GP>
 __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, int bm, int pre_bm)
 {
-    const int lane = threadIdx.x & 63;
+    constexpr int ROWS = 8 / GP;  // of a workgroup
+    __shared__ f32x4 sums[8][2][32];
+    __shared__ float stat[8][2];
+    const int l32 = threadIdx.x & 31, group = threadIdx.x >> 5, part = group % GP;
     const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
     Item it;
     if (!find_item(a, bm, id, true, it))
@@ -864,67 +894,111 @@ __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, 
     if (!shared && it.pieces == 1)
         return;  // written by its one item
     const int rows = it.s.nq * a.G;
-    const int r = blockIdx.y * 8 + threadIdx.x / 32;
+    const int r = blockIdx.y * ROWS + group / GP;
     const int row = it.tile * bm + r;
     const int slot = first_item(a, it, bm);
     if (slot + it.pieces > a.items)
         return;  // more tiles than sequences that do not overlap can have: not computed
+    if (it.tile * bm + (int)blockIdx.y * ROWS >= rows)
+        return;
+    const bool live = r < bm && row < rows;
     // the prefix's items of this row
     int pslot = 0, pn = 0, prow = 0;
     if (shared) {
         Item p;
         find_item(pre, pre_bm, 0, true, p);
-        const int all = it.s.q0 * pre.G + row;  // T * heads < 2^31
-        p.tile = min(all, pre.T * pre.G - 1) / pre_bm;
+        const int all = min(it.s.q0 * pre.G + row, pre.T * pre.G - 1);  // T * heads < 2^31
+        p.tile = all / pre_bm;
         prow = all % pre_bm;
         pslot = first_item(pre, p, pre_bm);
         pn = p.pieces;
     }
-    if (r >= bm || row >= rows)
-        return;
-    const int n = it.pieces + pn, l32 = lane & 31;
-    auto lse_at = [&](int i) {
-        return i < it.pieces ? a.ws_l[((int64_t)(slot + i) * a.Hkv + head) * bm + r]
-                             : pre.ws_l[((int64_t)(pslot + i - it.pieces) * a.Hkv + head) * pre_bm + prow];
-    };
-    auto out_at = [&](int i) {
-        return i < it.pieces ? a.ws_o + (((int64_t)(slot + i) * a.Hkv + head) * bm + r) * a.D
-                             : pre.ws_o + (((int64_t)(pslot + i - it.pieces) * a.Hkv + head) * pre_bm + prow) * a.D;
-    };
-    float mx = -INFINITY;
-    bool nan = false;
-    for (int i = l32; i < n; i += 32) {
-        const float v = lse_at(i);
-        nan = nan || v != v;
-        mx = fmaxf(mx, v);
-    }
+    const int n = it.pieces + pn;
+    float m = -INFINITY, total = 0.f;
+    f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+    const int c0 = 4 * l32 < a.D ? 4 * l32 : 0, c1 = 128 + 4 * l32 < a.D ? 128 + 4 * l32 : 0;
+    if (live)
+        for (int i = part; i < n; i += 4 * GP) {
+            float v[4];
+            f32x4 x0[4], x1[4];
 #pragma unroll
-    for (int d = 16; d; d /= 2) {
-        mx = fmaxf(mx, __shfl_xor(mx, d));
-        nan = __shfl_xor((int)nan, d) || nan;
+            for (int u = 0; u < 4; ++u) {
+                const int j = min(i + u * GP, n - 1);
+                const bool own = j < it.pieces;
+                const int64_t at = own ? ((int64_t)(slot + j) * a.Hkv + head) * bm + r
+                                       : ((int64_t)(pslot + j - it.pieces) * a.Hkv + head) * pre_bm + prow;
+                const float *o = (own ? a.ws_o : pre.ws_o) + at * a.D;
+                v[u] = (own ? a.ws_l : pre.ws_l)[at];
+                x0[u] = *reinterpret_cast<const f32x4 *>(o + c0);
+                if (a.D > 128)
+                    x1[u] = *reinterpret_cast<const f32x4 *>(o + c1);
+            }
+            float mx = m;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (i + u * GP >= n) {  // the last slice again: not taken (0 * inf would be NaN)
+                    v[u] = -INFINITY;
+                    x0[u] = x1[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+                mx = fmaxf(mx, v[u]);
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx, f = expf(m - ref);
+            total *= f;
+            s0 *= f;
+            s1 *= f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float w = expf(v[u] - ref);
+                total += w;
+                s0 += x0[u] * w;
+                if (a.D > 128)
+                    s1 += x1[u] * w;
+            }
+            m = mx;
+        }
+    if constexpr (GP > 1) {
+        sums[group][0][l32] = s0;
+        sums[group][1][l32] = s1;
+        if (l32 == 0) {
+            stat[group][0] = m;
+            stat[group][1] = total;
+        }
+        __syncthreads();
+        if (part)
+            return;
+        float mx = m;
+#pragma unroll
+        for (int q = 1; q < GP; ++q)
+            mx = fmaxf(mx, stat[group + q][0]);
+        const float ref = mx == -INFINITY ? 0.f : mx, f = expf(m - ref);
+        total *= f;
+        s0 *= f;
+        s1 *= f;
+#pragma unroll
+        for (int q = 1; q < GP; ++q) {
+            const float w = expf(stat[group + q][0] - ref);
+            total += stat[group + q][1] * w;
+            s0 += sums[group + q][0][l32] * w;
+            s1 += sums[group + q][1][l32] * w;
+        }
+        m = mx;
     }
+    if (!live)
+        return;
     const int token = row / a.G, qh = head * a.G + row % a.G;
     const int64_t at = (int64_t)(it.s.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
-    float total = 0.f;
-    for (int c = 4 * l32; c < a.D; c += 128) {
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        total = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float v = lse_at(i);
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(out_at(i) + c);
-            if (v != -INFINITY) {  // an empty slice: its out is 0 as well
-                const float w = mx == INFINITY ? 1.f : expf(v - mx);
-                total += w;
-                sum += x * w;
-            }
-        }
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        const float y[4] = {sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv};
-        store4(static_cast<TO *>(a.out) + at + c, y);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    TO *dst = static_cast<TO *>(a.out) + at;
+    if (4 * l32 < a.D) {
+        const float y[4] = {s0[0] * inv, s0[1] * inv, s0[2] * inv, s0[3] * inv};
+        store4(dst + 4 * l32, y);
+    }
+    if (128 + 4 * l32 < a.D) {
+        const float y[4] = {s1[0] * inv, s1[1] * inv, s1[2] * inv, s1[3] * inv};
+        store4(dst + 128 + 4 * l32, y);
     }
     if (a.lse && l32 == 0)
-        a.lse[(int64_t)(it.s.q0 + token) * a.Hq + qh] = nan ? NAN : mx == -INFINITY ? -INFINITY : mx + logf(total);
+        a.lse[(int64_t)(it.s.q0 + token) * a.Hq + qh] = total == 0.f ? -INFINITY : m + logf(total);
 }
 
 // --------------------------------------------------------------------------------- plans
@@ -958,6 +1032,18 @@ hipError_t run_type(const AttnArgs &a, const AttnPart &p, int type, int out_type
     if (type == kBF16)
         return wide ? run_dim<bf16_t, true>(a, p, s) : run_dim<bf16_t, false>(a, p, s);
     return wide ? run_dim<f16_t, true>(a, p, s) : run_dim<f16_t, false>(a, p, s);
+}
+
+template <typename TO>
+hipError_t run_combine(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, bool many, hipStream_t s)
+{
+    const unsigned tiles = (unsigned)(p.main.tiles * a.Hkv);
+    const unsigned rows = (unsigned)p.main.bm;
+    if (many)
+        k_attn_combine<TO, 8><<<dim3(tiles, rows), 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
+    else
+        k_attn_combine<TO, 1><<<dim3(tiles, (rows + 7) / 8), 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
+    return hipGetLastError();
 }
 
 AttnPart plan_part(int64_t rows, int64_t seqs, int64_t Hkv, bool always)  // seqs: with rows of their own
@@ -1023,14 +1109,11 @@ hipError_t launch_attention(const AttnArgs &args, const AttnArgs &prefix, const 
         return e;
     if (!p.main.target)
         return hipSuccess;
-    const dim3 grid((unsigned)(p.main.tiles * a.Hkv), (unsigned)(p.main.bm / 8));
-    if (out_type == kF32)
-        k_attn_combine<float><<<grid, 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
-    else if (type == kBF16)
-        k_attn_combine<bf16_t><<<grid, 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
-    else
-        k_attn_combine<f16_t><<<grid, 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
-    return hipGetLastError();
+    // Rows of few-row tiles and of a shared prefix have many slices, those of cut prompts two or three.
+    const bool many = p.main.bm == kFewRows || prefix.shared;
+    return out_type == kF32   ? run_combine<float>(a, pre, p, many, s)
+           : type == kBF16 ? run_combine<bf16_t>(a, pre, p, many, s)
+                              : run_combine<f16_t>(a, pre, p, many, s);
 }
 
 }  // namespace bt
