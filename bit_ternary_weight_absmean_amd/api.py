@@ -622,16 +622,17 @@ _ATTENTION_SHAPE = struct.Struct("7q3if12q")  # bt_attention_shape
 _HALF = {torch.bfloat16: 1, torch.float16: 2}
 
 
-def attention_workspace_bytes(tokens: int, seqs: int, heads: int, kv_heads: int, head_dim: int, prefix: int = 0) -> int:
+def attention_workspace_bytes(tokens: int, keys: int, seqs: int, heads: int, kv_heads: int, head_dim: int,
+                              prefix: int = 0) -> int:
     """bt_attention_workspace_bytes: the scratch of an attention call (0: none)."""
-    return _workspace_bytes("bt_attention_workspace_bytes", tokens, seqs, heads, kv_heads, head_dim, prefix)
+    return _workspace_bytes("bt_attention_workspace_bytes", tokens, keys, seqs, heads, kv_heads, head_dim, prefix)
 
 
 def attention_workspace(q: torch.Tensor, k: torch.Tensor, seqs: int,
                         prefix_k: torch.Tensor | None = None) -> torch.Tensor | None:
     """A workspace for attention of these arrays in ``seqs`` sequences (its contents do not matter), or
     None where none is needed."""
-    n = attention_workspace_bytes(q.shape[0], seqs, q.shape[1], k.shape[1], q.shape[2],
+    n = attention_workspace_bytes(q.shape[0], k.shape[0], seqs, q.shape[1], k.shape[1], q.shape[2],
                                   0 if prefix_k is None else prefix_k.shape[0])
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
@@ -690,7 +691,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.
         _need_strided(out, "out", ot, (T, heads, D), dev, output=True)
     if lse is not None and not _as_is(dev, (lse, torch.float32, (T, heads))):
         _need(lse, "lse", torch.float32, (T, heads), dev)
-    need = _workspace_bytes("bt_attention_workspace_bytes", T, B, heads, kv_heads, D, P)
+    need = _workspace_bytes("bt_attention_workspace_bytes", T, S, B, heads, kv_heads, D, P)
     if workspace is not None:
         _need_bytes(workspace, "workspace", need, dev)
     elif need:

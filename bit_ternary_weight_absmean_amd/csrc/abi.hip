@@ -114,13 +114,14 @@ bt_status read_groups(const int64_t *group_rows, int64_t ngroups, int64_t N, bt:
 }
 
 // Shape checks of bt_attention that its workspace size shares.
-bt_status check_attention(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
-                          int64_t prefix, bt::AttnPlan &plan)
+bt_status check_attention(int64_t tokens, int64_t keys, int64_t seqs, int64_t heads, int64_t kv_heads,
+                          int64_t head_dim, int64_t prefix, bt::AttnPlan &plan)
 {
     if (tokens < 0 || tokens > BT_MAX_DIM || seqs < 0 || seqs > BT_MAX_DIM)
         return fail(BT_ERR_SHAPE, "tokens = %lld or seqs = %lld outside [0, 2^23]", (long long)tokens, (long long)seqs);
-    if (prefix < 0 || prefix > INT32_MAX - 64)
-        return fail(BT_ERR_SHAPE, "prefix = %lld outside [0, 2^31 - 65]", (long long)prefix);
+    if (keys < 0 || keys > INT32_MAX - 64 || prefix < 0 || prefix > INT32_MAX - 64)
+        return fail(BT_ERR_SHAPE, "keys = %lld or prefix = %lld outside [0, 2^31 - 65]", (long long)keys,
+                    (long long)prefix);
     if (heads < 1 || kv_heads < 1 || heads > 65536 || heads % kv_heads)
         return fail(BT_ERR_SHAPE, "heads = %lld, kv_heads = %lld: heads must be a multiple of kv_heads, at most 65536",
                     (long long)heads, (long long)kv_heads);
@@ -132,9 +133,10 @@ bt_status check_attention(int64_t tokens, int64_t seqs, int64_t heads, int64_t k
     plan = bt::AttnPlan{};
     if (tokens == 0 || seqs == 0)
         return BT_OK;
-    plan = bt::attn_plan(tokens, seqs, heads, kv_heads, head_dim, prefix);
-    if (plan.main.items * kv_heads >= 1 << 24 || plan.pre.items * kv_heads >= 1 << 24)
-        return fail(BT_ERR_SHAPE, "%lld work items for one launch", (long long)(plan.main.items * kv_heads));
+    plan = bt::attn_plan(tokens, keys, seqs, heads, kv_heads, head_dim, prefix);
+    if ((plan.main.items + plan.pre.items) * kv_heads >= 1 << 24)
+        return fail(BT_ERR_SHAPE, "%lld work items for one launch",
+                    (long long)((plan.main.items + plan.pre.items) * kv_heads));
     return BT_OK;
 }
 
@@ -751,11 +753,11 @@ bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int
                       "bt_qk_norm_rope launch");
 }
 
-size_t bt_attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
-                                    int64_t prefix)
+size_t bt_attention_workspace_bytes(int64_t tokens, int64_t keys, int64_t seqs, int64_t heads, int64_t kv_heads,
+                                    int64_t head_dim, int64_t prefix)
 {
     bt::AttnPlan plan;
-    if (check_attention(tokens, seqs, heads, kv_heads, head_dim, prefix, plan))
+    if (check_attention(tokens, keys, seqs, heads, kv_heads, head_dim, prefix, plan))
         return 0;
     return plan.bytes;
 }
@@ -768,10 +770,8 @@ bt_status bt_attention(const bt_attention_shape *shape, const void *q, const voi
         return fail(BT_ERR_NULL, "shape is NULL");
     const bt_attention_shape &s = *shape;
     bt::AttnPlan plan;
-    if (bt_status e = check_attention(s.tokens, s.seqs, s.heads, s.kv_heads, s.head_dim, s.prefix, plan))
+    if (bt_status e = check_attention(s.tokens, s.keys, s.seqs, s.heads, s.kv_heads, s.head_dim, s.prefix, plan))
         return e;
-    if (s.keys < 0 || s.keys > INT32_MAX - 64)
-        return fail(BT_ERR_SHAPE, "keys = %lld outside [0, 2^31 - 65]", (long long)s.keys);
     if (!(s.scale > 0.0f) || !(s.scale < 1.0e30f))
         return fail(BT_ERR_SHAPE, "scale must be finite and positive");
     if ((s.type != BT_BF16 && s.type != BT_F16) || (s.out_type != s.type && s.out_type != BT_F32))

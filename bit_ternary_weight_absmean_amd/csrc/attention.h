@@ -36,7 +36,7 @@ struct AttnPlan {
     size_t bytes;
 };
 
-AttnPlan attn_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t P);
+AttnPlan attn_plan(int64_t T, int64_t S, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t P);
 hipError_t launch_attention(const AttnArgs &args, const AttnArgs &prefix, const AttnPlan &p, int type, int out_type,
                             hipStream_t s);
 

@@ -36,6 +36,8 @@
 // k_attn_combine joins them in slice order. No atomics, so results do not depend on timing.
 #include <math.h>
 
+#include <type_traits>
+
 #include "attention.h"
 #include "bt_internal.h"
 #include "convert.h"
@@ -315,26 +317,31 @@ __device__ inline void load_lds16(__amdgpu_buffer_rsrc_t from, char *dst, uint32
 
 // ------------------------------------------------------------------------- prompt kernel
 //
-// k_attn_tile: 128 rows of a sequence against a slice of its keys, 64 at a time. Each of four waves
-// holds 32 rows (32x32x16 MFMA); K and V blocks go to LDS by direct loads, the next block's while
-// this one is multiplied (two buffers each, one barrier per block).
+// attn_tile: 32 rows per wave (32x32x16 MFMA) against a slice of the tile's keys, 64 at a time. K and
+// V blocks go to LDS by direct loads, the next block's while this one is used (two buffers each).
+//
+// A block is two phases: from the scores to the probabilities on the vector unit, then this block's
+// product with V and the next block's scores on the matrix cores. Kept apart (the probabilities are
+// pinned at the end of the first phase), the matrix phase is one unbroken run of 32 MFMAs fed from LDS,
+// and the two waves of a SIMD, which belong to different workgroups, alternate: a 7B prompt of 8192
+// tokens takes 541 us (1.02 PFLOP/s; a large bf16 matrix product of the library reaches 1.38 on the
+// same card), against 592-620 us with scores, softmax and V's product in sequence. Eight waves of one
+// workgroup in two groups held half a block apart by barriers: 597-620 us; a raised wave priority in
+// the matrix phase: 549 us.
 
 constexpr int kTileRows = 128, kTileKeys = 64;
 
 template <typename E, int DP, bool PART, bool WIDE>
-__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
+__device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kbuf0, char *kbuf1, char *vbuf0,
+                                          char *vbuf1, int &poison)
 {
     using V8 = typename Elem<E>::v8;
     constexpr int CPR = DP / 8;                          // 16-byte chunks of a row
     constexpr int NS = DP / 16, ND = DP / 32;            // MFMA steps over D, 32-wide tiles of D
     constexpr int LOADS = kTileKeys * CPR / 256;         // direct loads per wave and block
-    __shared__ __attribute__((aligned(1024))) char kbuf0[kTileKeys * DP * 2], kbuf1[kTileKeys * DP * 2];
-    __shared__ __attribute__((aligned(1024))) char vbuf0[kTileKeys * DP * 2], vbuf1[kTileKeys * DP * 2];
-    __shared__ int poison;  // a masked block of V held an infinity or NaN
-
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 31, h = lane >> 5;
-    const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+    const int id = block / a.Hkv, head = block % a.Hkv;
     Item it;
     if (!find_item(a, kTileRows, id, false, it))
         return;
@@ -380,16 +387,14 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
         voff[i] = in ? (uint32_t)(r * vrow_bytes + c * 16) : kOutside;
     }
     const char *kp = key_base(a, s, head, false), *vp = key_base(a, s, head, true);
-    auto issue = [&](int key, char *kd, char *vd) {
-        const int n = min(kTileKeys, s.nk - key);
-        const __amdgpu_buffer_rsrc_t kr = rows_buffer(kp + (int64_t)key * krow_bytes, n, krow_bytes, a.D);
-        const __amdgpu_buffer_rsrc_t vr = rows_buffer(vp + (int64_t)key * vrow_bytes, n, vrow_bytes, a.D);
+    auto issue = [&](const char *base, int row_bytes, const uint32_t (&off)[LOADS], int key, char *dst) __attribute__((always_inline)) {
+        if (key >= hi)
+            return;
+        const __amdgpu_buffer_rsrc_t from =
+            rows_buffer(base + (int64_t)key * row_bytes, min(kTileKeys, s.nk - key), row_bytes, a.D);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i)
-            load_lds16(kr, kd + (wave * LOADS + i) * 1024, koff[i]);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            load_lds16(vr, vd + (wave * LOADS + i) * 1024, voff[i]);
+            load_lds16(from, dst + (wave * LOADS + i) * 1024, off[i]);
     };
 
     f32x16 o[ND];
@@ -401,43 +406,28 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
     float m = -INFINITY, l = 0.f;  // l: this lane's keys only until the end
     const float c2 = a.scale_log2;
 
-    // V^T operand address parts: lane i of 16 reads 8 bytes of row i / 4 of its 4 x 16 block
-    const int tr_row = 4 * h + (lane & 15) / 4, tr_col = (lane >> 4 & 1) * 32 + (lane & 3) * 8;  // bytes
-    auto v_frag = [&](const char *vb, int dt, int t) {
-        u32x4 x;
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-            const int r = 16 * t + 8 * jj + tr_row;
-            const int byte = dt * 64 + tr_col;
-            const char *p = vb + r * (DP * 2) + (((byte >> 4) ^ swizzle<DP>(r)) << 4) + (byte & 15);
-            const u32x2 half = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
-            x[2 * jj] = half[0];
-            x[2 * jj + 1] = half[1];
-        }
-        return x;
-    };
-
-    auto block = [&](int key, const char *kb, const char *vb) {
-        if (key >= wmost)
-            return;  // nothing of it is seen by this wave
-        f32x16 sc[2];
+    // S^T of a block; register i of half b: key + 32 b + 8 (i / 4) + 4 h + i % 4. Operand addresses are a
+    // lane's base with bits flipped by the (constant) step.
+    f32x16 sc[2];
+    const int kbase = col * (DP * 2) + ((h ^ swizzle<DP>(col)) << 4);
+    auto scores = [&](const char *kb) __attribute__((always_inline)) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 sc[b][i] = 0.f;
-            const int r = 32 * b + col;
-            const char *p = kb + r * (DP * 2);
-            const int sw = swizzle<DP>(r);
 #pragma unroll
             for (int st = 0; st < NS; ++st) {
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(p + (((2 * st + h) ^ sw) << 4));
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(kb + (kbase ^ (st << 5)) + b * 32 * DP * 2);
                 sc[b] = Elem<E>::mma32(__builtin_bit_cast(V8, x), qf[st], sc[b]);
             }
         }
-        // register i of block b: key + 32 b + 8 (i / 4) + 4 h + i % 4
-        const bool masked = key + kTileKeys > wfull;
-        if (masked) {
+    };
+    // The vector phase: probabilities of the block, as P^T operands (slot j of step t is register
+    // 8 (t % 2) + j of half t / 2).
+    u32x4 pf[4], pr[4];
+    auto soften = [&](int key) __attribute__((always_inline)) {
+        if (key + kTileKeys > wfull) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -465,48 +455,68 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
         }
         const float ref = m == -INFINITY ? 0.f : m * c2;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sc[b][i] = exp2_fast(__builtin_fmaf(sc[b][i], c2, -ref));
-                l += sc[b][i];
-            }
-        // P^T operands: slot j of step t is register 8 (t % 2) + j of block t / 2
-        u32x4 pf[4], pr[4];
-#pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p0 = sc[t / 2][8 * (t % 2) + 2 * j], p1 = sc[t / 2][8 * (t % 2) + 2 * j + 1];
-                pf[t][j] = pack2<E>(p0, p1);
+                float p[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    p[e] = exp2_fast(__builtin_fmaf(sc[t / 2][8 * (t % 2) + 2 * j + e], c2, -ref));
+                    l += p[e];
+                }
+                pf[t][j] = pack2<E>(p[0], p[1]);
                 if constexpr (WIDE) {
                     const f32x2 back = unpack2<E>(pf[t][j]);
-                    pr[t][j] = pack2<E>(p0 - back[0], p1 - back[1]);
+                    pr[t][j] = pack2<E>(p[0] - back[0], p[1] - back[1]);
                 }
             }
+        // done here, not where they are used
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            asm volatile("" : "+v"(pf[t]));
+            if constexpr (WIDE)
+                asm volatile("" : "+v"(pr[t]));
+        }
+    };
+    // The matrix phase. V^T operands: lane i of 16 reads 8 bytes of row i / 4 of its 4 x 16 block of V. Row
+    // 16 t + 8 j + tr_row is swizzled by that of tr_row, with bit 1 flipped by j.
+    const int tr_row = 4 * h + (lane & 15) / 4, tr_col = (lane >> 4 & 1) * 32 + (lane & 3) * 8;  // bytes
+    const int vbase = tr_row * (DP * 2) + (((tr_col >> 4) ^ swizzle<DP>(tr_row)) << 4) + (tr_col & 15);
+    auto weigh = [&](const char *vb) __attribute__((always_inline)) {
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const V8 x = __builtin_bit_cast(V8, v_frag(vb, d, t));
-                o[d] = Elem<E>::mma32(x, __builtin_bit_cast(V8, pf[t]), o[d]);
+                u32x4 x;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const char *p = vb + (vbase ^ (d << 6) ^ (j << 5)) + (16 * t + 8 * j) * DP * 2;
+                    const u32x2 half =
+                        __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+                    x[2 * j] = half[0];
+                    x[2 * j + 1] = half[1];
+                }
+                o[d] = Elem<E>::mma32(__builtin_bit_cast(V8, x), __builtin_bit_cast(V8, pf[t]), o[d]);
                 if constexpr (WIDE)
-                    o[d] = Elem<E>::mma32(x, __builtin_bit_cast(V8, pr[t]), o[d]);
+                    o[d] = Elem<E>::mma32(__builtin_bit_cast(V8, x), __builtin_bit_cast(V8, pr[t]), o[d]);
             }
     };
 
-    // This wave's loads have arrived and its reads of the other buffer are done; then all waves'.
-    auto arrive = [] {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // End of a block: this wave's direct loads have arrived and its LDS reads are done; then all waves'.
+    auto sync = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
+    auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
     // Masked block of V: infinities and NaNs to 0, by the whole workgroup.
-    auto clean = [&](int key, char *vb) {
-        if (key + kTileKeys <= gfull)
+    auto clean = [&](int key, char *vb) __attribute__((always_inline)) {
+        if (key + kTileKeys <= gfull || key >= hi)
             return;
 #pragma unroll
-        for (int i = 0; i < kTileKeys * CPR / 256; ++i) {
+        for (int i = 0; i < LOADS; ++i) {
             u32x4 *p = reinterpret_cast<u32x4 *>(vb + (i * 256 + threadIdx.x) * 16);
             const u32x4 x = *p;
             if (not_finite<E>(x[0]) || not_finite<E>(x[1]) || not_finite<E>(x[2]) || not_finite<E>(x[3])) {
@@ -514,27 +524,39 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
                 poison = 1;
             }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        sync();
     };
     if (threadIdx.x == 0)
         poison = 0;
     if (lo < hi) {
-        issue(lo, kbuf0, vbuf0);
+        issue(kp, krow_bytes, koff, lo, kbuf0);
+        landed();
+        sync();
+        issue(kp, krow_bytes, koff, lo + kTileKeys, kbuf1);
+        issue(vp, vrow_bytes, voff, lo, vbuf0);
+        scores(kbuf0);
+        landed();
+        sync();
+        // K runs one block ahead of V; the last block's matrix phase forms scores from whatever the
+        // other buffer holds, and they are not used.
+        auto one = [&](int key, char *vb, char *kb, char *vnext, char *knext) __attribute__((always_inline)) {
+            issue(kp, krow_bytes, koff, key + 2 * kTileKeys, knext);
+            issue(vp, vrow_bytes, voff, key + kTileKeys, vnext);
+            clean(key, vb);
+            if (key < wmost) {
+                soften(key);
+                
+                scores(kb);
+                weigh(vb);
+                
+            }
+            landed();
+            sync();
+        };
         for (int key = lo; key < hi; key += 2 * kTileKeys) {
-            arrive();
+            one(key, vbuf0, kbuf1, vbuf1, kbuf0);
             if (key + kTileKeys < hi)
-                issue(key + kTileKeys, kbuf1, vbuf1);
-            clean(key, vbuf0);
-            block(key, kbuf0, vbuf0);
-            if (key + kTileKeys >= hi)
-                break;
-            arrive();
-            if (key + 2 * kTileKeys < hi)
-                issue(key + 2 * kTileKeys, kbuf0, vbuf0);
-            clean(key + kTileKeys, vbuf1);
-            block(key + kTileKeys, kbuf1, vbuf1);
+                one(key + kTileKeys, vbuf1, kbuf0, vbuf0, kbuf1);
         }
     }
     __syncthreads();
@@ -564,7 +586,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
         return;
     const bool part = PART && (a.pieced || it.pieces > 1);
     if (part) {
-        const int64_t slot = blockIdx.x;
+        const int64_t slot = block;
         const int r = 32 * wave + col;
         float *dst = a.ws_o + (slot * kTileRows + r) * a.D;
 #pragma unroll
@@ -603,7 +625,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
 
 // -------------------------------------------------------------------- few-rows kernel
 //
-// k_attn_few: 16 rows (a decode step's heads of one group, a short draft) against a slice of their
+// attn_few: 16 rows (a decode step's heads of one group, a short draft) against a slice of their
 // keys; bound by the bytes of K and V. Each of four waves takes every fourth block of 32 keys on its
 // own: K goes from memory straight into the registers of the S^T operand (16x16x32 MFMA: lane (r, g)
 // holds 16 bytes of key r), V through a private piece of LDS for the transposing read, and the next
@@ -613,7 +635,8 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_tile(AttnArgs a)
 constexpr int kFewRows = 16, kFewKeys = 32, kFewWaves = 4;
 
 template <typename E, int DP, bool WIDE>
-__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
+__device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf0, char *buf1,
+                                         float (&stat)[kFewWaves][2][kFewRows])
 {
     using V8 = typename Elem<E>::v8;
     constexpr int CPR = DP / 8;
@@ -621,12 +644,11 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
     constexpr int LOADS = kFewKeys * CPR / 64;  // 16-byte V loads per lane and block
     constexpr int kVBytes = kFewKeys * DP * 2;
     static_assert(kVBytes >= kFewRows * DP * 4, "the waves' partial outputs reuse the V blocks");
-    __shared__ __attribute__((aligned(1024))) char vlds[kFewWaves][kVBytes];
-    __shared__ float stat[kFewWaves][2][kFewRows];
+    auto vlds = [&](int w) { return (w < 2 ? buf0 : buf1) + (w & 1) * kVBytes; };  // wave w's piece
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+    const int id = block / a.Hkv, head = block % a.Hkv;
     Item it;
     if (!find_item(a, kFewRows, id, false, it))
         return;
@@ -687,7 +709,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
         o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
     const float c2 = a.scale_log2;
-    char *vb = vlds[wave];
+    char *vb = vlds(wave);
     const int tr_row = 4 * g + (lane & 15) / 4, tr_col = (lane & 3) * 8;
     auto v_frag = [&](int dt) {
         u32x4 x;
@@ -703,7 +725,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
         return x;
     };
     bool poison = false;  // a masked block of V held an infinity or NaN
-    auto block = [&](int key, Block &x) {
+    auto step = [&](int key, Block &x) __attribute__((always_inline)) {
         f32x4 sc[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -786,11 +808,11 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
         fetch(k0, x);
         for (int key = k0; key < hi; key += 2 * kStride) {
             fetch(key + kStride, y);
-            block(key, x);
+            step(key, x);
             if (key + kStride >= hi)
                 break;
             fetch(key + 2 * kStride, x);
-            block(key + kStride, y);
+            step(key + kStride, y);
         }
     }
     if (__builtin_expect(__any(poison), 0)) {
@@ -836,7 +858,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
     const float f = m == -INFINITY ? inv : exp2_fast((m - mall) * c2) * inv;
     const float lse = lall == 0.f ? -INFINITY : mall * c2 * kLn2 + logf(lall);
     // wave's O^T to LDS as [row][D]: 4 values of row col per register group
-    float *mine = reinterpret_cast<float *>(vlds[wave]);
+    float *mine = reinterpret_cast<float *>(vlds(wave));
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
         const f32x4 x = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o[d] * f;
@@ -852,10 +874,10 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
         f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kFewWaves; ++w)
-            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(vlds[w]) + r * DP + (c ^ (r & 7)) * 4);
+            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(vlds(w)) + r * DP + (c ^ (r & 7)) * 4);
         const float x[4] = {sum[0], sum[1], sum[2], sum[3]};
         if (part) {
-            store4(a.ws_o + ((int64_t)blockIdx.x * kFewRows + r) * a.D + 4 * c, x);
+            store4(a.ws_o + ((int64_t)block * kFewRows + r) * a.D + 4 * c, x);
         } else {
             const int64_t at = (int64_t)(s.q0 + rr / a.G) * a.o_row + (int64_t)(head * a.G + rr % a.G) * a.o_head + 4 * c;
             if constexpr (WIDE)
@@ -866,9 +888,48 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
     }
     if (wave == 0 && g == 0 && live) {
         if (part)
-            a.ws_l[(int64_t)blockIdx.x * kFewRows + col] = lse;
+            a.ws_l[(int64_t)block * kFewRows + col] = lse;
         else if (a.lse)
             a.lse[(int64_t)(s.q0 + token) * a.Hq + qh] = lse;
+    }
+}
+
+// ------------------------------------------------------------------------------- kernels
+//
+// One launch per call, and k_attn_combine behind it where keys are cut. With a shared prefix the
+// prefix's items are the first workgroups of the same launch (PRE), so that neither part waits for the
+// other.
+
+enum Kind { kNone, kFew, kTile };
+
+template <typename E, int DP, bool WIDE, Kind MAIN, Kind PRE, bool PART>
+__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn(AttnArgs a, AttnArgs pre, int pre_blocks)
+{
+    constexpr bool tiles = MAIN == kTile || PRE == kTile;
+    constexpr int bytes = kTileKeys * DP * 2;
+    static_assert(bytes == 2 * kFewKeys * DP * 2, "two waves' pieces of the few-rows kernel");
+    __shared__ __attribute__((aligned(1024))) char buf0[bytes], buf1[bytes];
+    __shared__ __attribute__((aligned(1024))) char buf2[tiles ? bytes : 16], buf3[tiles ? bytes : 16];
+    __shared__ float stat[kFewWaves][2][kFewRows];
+    __shared__ int poison;  // attn_tile: a masked block of V held an infinity or NaN
+    const int block = blockIdx.x;
+    if constexpr (PRE == MAIN) {
+        const bool p = block < pre_blocks;
+        const AttnArgs &x = p ? pre : a;
+        if constexpr (MAIN == kFew)
+            attn_few<E, DP, WIDE>(x, p ? block : block - pre_blocks, buf0, buf1, stat);
+        else
+            attn_tile<E, DP, true, WIDE>(x, p ? block : block - pre_blocks, buf0, buf1, buf2, buf3, poison);
+    } else {
+        if constexpr (PRE == kTile)
+            if (block < pre_blocks) {
+                attn_tile<E, DP, true, WIDE>(pre, block, buf0, buf1, buf2, buf3, poison);
+                return;
+            }
+        if constexpr (MAIN == kFew)
+            attn_few<E, DP, WIDE>(a, block - pre_blocks, buf0, buf1, stat);
+        else
+            attn_tile<E, DP, PART, WIDE>(a, block, buf0, buf1, buf2, buf3, poison);
     }
 }
 
@@ -876,16 +937,18 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn_few(AttnArgs a)
 //
 // k_attn_combine: a row's slices, and with a shared prefix the prefix's slices of the same row,
 // joined by their lse: out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max). 32 lanes read a
-// row; GP such groups share a row's slices (every GP-th each, four in flight) and are joined in LDS.
-// Latency is all there is to it, so where a row has many slices GP is 8.
+// row; the 32 such groups of a workgroup are spread over its (at most 32) rows, so that the slices of
+// few rows are read side by side (four in flight in each group) and joined through LDS. Latency is all
+// there is to it.
 
-template <typename TO, int GP>
-__global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, int bm, int pre_bm)
+constexpr int kJoinRows = 32;  // largest number of rows of a workgroup
+
+template <typename TO>
+__global__ __launch_bounds__(1024) void k_attn_combine(AttnArgs a, AttnArgs pre, int bm, int pre_bm)
 {
-    constexpr int ROWS = 8 / GP;  // of a workgroup
-    __shared__ f32x4 sums[8][2][32];
-    __shared__ float stat[8][2];
-    const int l32 = threadIdx.x & 31, group = threadIdx.x >> 5, part = group % GP;
+    __shared__ f32x4 sums[32][2][32];
+    __shared__ float stat[32][2];
+    const int l32 = threadIdx.x & 31, group = threadIdx.x >> 5;
     const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
     Item it;
     if (!find_item(a, bm, id, true, it))
@@ -894,14 +957,18 @@ __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, 
     if (!shared && it.pieces == 1)
         return;  // written by its one item
     const int rows = it.s.nq * a.G;
-    const int r = blockIdx.y * ROWS + group / GP;
-    const int row = it.tile * bm + r;
     const int slot = first_item(a, it, bm);
     if (slot + it.pieces > a.items)
         return;  // more tiles than sequences that do not overlap can have: not computed
-    if (it.tile * bm + (int)blockIdx.y * ROWS >= rows)
+    const int r0 = blockIdx.y * kJoinRows;
+    const int here = min(min(bm - r0, kJoinRows), rows - it.tile * bm - r0);  // rows of this workgroup
+    if (here <= 0)
         return;
-    const bool live = r < bm && row < rows;
+    const int ways = 32 - __builtin_clz(2 * here - 1) - 1;  // log2 of here rounded up to a power of two
+    const int gp = 32 >> ways;                              // groups of a row
+    const int r = r0 + (group & ((1 << ways) - 1)), part = group >> ways;
+    const int row = it.tile * bm + r;
+    const bool live = r < r0 + here;
     // the prefix's items of this row
     int pslot = 0, pn = 0, prow = 0;
     if (shared) {
@@ -918,12 +985,12 @@ __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, 
     f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
     const int c0 = 4 * l32 < a.D ? 4 * l32 : 0, c1 = 128 + 4 * l32 < a.D ? 128 + 4 * l32 : 0;
     if (live)
-        for (int i = part; i < n; i += 4 * GP) {
+        for (int i = part; i < n; i += 4 * gp) {
             float v[4];
             f32x4 x0[4], x1[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int j = min(i + u * GP, n - 1);
+                const int j = min(i + u * gp, n - 1);
                 const bool own = j < it.pieces;
                 const int64_t at = own ? ((int64_t)(slot + j) * a.Hkv + head) * bm + r
                                        : ((int64_t)(pslot + j - it.pieces) * a.Hkv + head) * pre_bm + prow;
@@ -936,7 +1003,7 @@ __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, 
             float mx = m;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (i + u * GP >= n) {  // the last slice again: not taken (0 * inf would be NaN)
+                if (i + u * gp >= n) {  // the last slice again: not taken (0 * inf would be NaN)
                     v[u] = -INFINITY;
                     x0[u] = x1[u] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
@@ -956,7 +1023,7 @@ __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, 
             }
             m = mx;
         }
-    if constexpr (GP > 1) {
+    if (gp > 1) {
         sums[group][0][l32] = s0;
         sums[group][1][l32] = s1;
         if (l32 == 0) {
@@ -967,19 +1034,18 @@ __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, 
         if (part)
             return;
         float mx = m;
-#pragma unroll
-        for (int q = 1; q < GP; ++q)
-            mx = fmaxf(mx, stat[group + q][0]);
+        for (int q = 1; q < gp; ++q)
+            mx = fmaxf(mx, stat[group + (q << ways)][0]);
         const float ref = mx == -INFINITY ? 0.f : mx, f = expf(m - ref);
         total *= f;
         s0 *= f;
         s1 *= f;
-#pragma unroll
-        for (int q = 1; q < GP; ++q) {
-            const float w = expf(stat[group + q][0] - ref);
-            total += stat[group + q][1] * w;
-            s0 += sums[group + q][0][l32] * w;
-            s1 += sums[group + q][1][l32] * w;
+        for (int q = 1; q < gp; ++q) {
+            const int g = group + (q << ways);
+            const float w = expf(stat[g][0] - ref);
+            total += stat[g][1] * w;
+            s0 += sums[g][0][l32] * w;
+            s1 += sums[g][1][l32] * w;
         }
         m = mx;
     }
@@ -1004,77 +1070,91 @@ __global__ __launch_bounds__(256) void k_attn_combine(AttnArgs a, AttnArgs pre, 
 // --------------------------------------------------------------------------------- plans
 
 template <typename E, int DP, bool WIDE>
-hipError_t run_part(const AttnArgs &a, const AttnPart &p, hipStream_t s)
+hipError_t run_kind(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, hipStream_t s)
 {
-    const unsigned grid = (unsigned)(p.items * a.Hkv);
-    if (p.bm == kFewRows)
-        k_attn_few<E, DP, WIDE><<<grid, 256, 0, s>>>(a);
-    else if (p.target)
-        k_attn_tile<E, DP, true, WIDE><<<grid, 256, 0, s>>>(a);
-    else
-        k_attn_tile<E, DP, false, WIDE><<<grid, 256, 0, s>>>(a);
+    const int pb = (int)(p.pre.items * a.Hkv);
+    const unsigned grid = (unsigned)(p.main.items * a.Hkv + pb);
+    const bool few = p.main.bm == kFewRows, pre_few = p.pre.bm == kFewRows;
+    if (!pb) {
+        if (few)
+            k_attn<E, DP, WIDE, kFew, kNone, true><<<grid, 256, 0, s>>>(a, pre, 0);
+        else if (p.main.target)
+            k_attn<E, DP, WIDE, kTile, kNone, true><<<grid, 256, 0, s>>>(a, pre, 0);
+        else
+            k_attn<E, DP, WIDE, kTile, kNone, false><<<grid, 256, 0, s>>>(a, pre, 0);
+    } else if (few && pre_few) {
+        k_attn<E, DP, WIDE, kFew, kFew, true><<<grid, 256, 0, s>>>(a, pre, pb);
+    } else if (few) {
+        k_attn<E, DP, WIDE, kFew, kTile, true><<<grid, 256, 0, s>>>(a, pre, pb);
+    } else {  // the prefix has all sequences' rows: no fewer than one of them
+        k_attn<E, DP, WIDE, kTile, kTile, true><<<grid, 256, 0, s>>>(a, pre, pb);
+    }
     return hipGetLastError();
 }
 
 template <typename E, bool WIDE>
-hipError_t run_dim(const AttnArgs &a, const AttnPart &p, hipStream_t s)
+hipError_t run_dim(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, hipStream_t s)
 {
     if (a.D <= 64)
-        return run_part<E, 64, WIDE>(a, p, s);
+        return run_kind<E, 64, WIDE>(a, pre, p, s);
     if (a.D <= 128)
-        return run_part<E, 128, WIDE>(a, p, s);
-    return run_part<E, 256, WIDE>(a, p, s);
+        return run_kind<E, 128, WIDE>(a, pre, p, s);
+    return run_kind<E, 256, WIDE>(a, pre, p, s);
 }
 
-hipError_t run_type(const AttnArgs &a, const AttnPart &p, int type, int out_type, hipStream_t s)
+hipError_t run_type(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, int type, int out_type, hipStream_t s)
 {
     const bool wide = out_type == kF32;
     if (type == kBF16)
-        return wide ? run_dim<bf16_t, true>(a, p, s) : run_dim<bf16_t, false>(a, p, s);
-    return wide ? run_dim<f16_t, true>(a, p, s) : run_dim<f16_t, false>(a, p, s);
+        return wide ? run_dim<bf16_t, true>(a, pre, p, s) : run_dim<bf16_t, false>(a, pre, p, s);
+    return wide ? run_dim<f16_t, true>(a, pre, p, s) : run_dim<f16_t, false>(a, pre, p, s);
 }
 
 template <typename TO>
-hipError_t run_combine(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, bool many, hipStream_t s)
+hipError_t run_combine(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, hipStream_t s)
 {
-    const unsigned tiles = (unsigned)(p.main.tiles * a.Hkv);
-    const unsigned rows = (unsigned)p.main.bm;
-    if (many)
-        k_attn_combine<TO, 8><<<dim3(tiles, rows), 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
-    else
-        k_attn_combine<TO, 1><<<dim3(tiles, (rows + 7) / 8), 256, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
+    const dim3 grid((unsigned)(p.main.tiles * a.Hkv), (unsigned)((p.main.bm + kJoinRows - 1) / kJoinRows));
+    k_attn_combine<TO><<<grid, 1024, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
     return hipGetLastError();
 }
 
-AttnPart plan_part(int64_t rows, int64_t seqs, int64_t Hkv, bool always)  // seqs: with rows of their own
+// `rows` rows of `seqs` sequences (those that have rows) over at most `keys` keys each.
+AttnPart plan_part(int64_t rows, int64_t seqs, int64_t keys, int64_t Hkv, bool always)
 {
     AttnPart p;
     // mean rows of a sequence: up to 16, one small tile each
     p.bm = rows <= kFewRows * seqs ? kFewRows : kTileRows;
-    p.tiles = rows / p.bm + seqs;  // upper bound of sum of ceil(rows_b / bm)
-    const int64_t target = (512 + Hkv - 1) / Hkv;
-    p.target = p.bm == kFewRows || always || p.tiles < target ? target : 0;
-    p.min_units = 2;
-    // sum of tiles * ceil(units / slice) <= work / slice + tiles, work / slice <= target up to the
-    // rounding of the fp32 sum
+    p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
+    // Keys are cut so that about `want` workgroups share the work: eight per CU where the bytes of the
+    // keys are all that counts, and fewer for large tiles, whose outputs cost more to join.
+    const bool few = p.bm == kFewRows;
+    const int64_t want = few ? 2048 : 384;
+    const int64_t target = (want + Hkv - 1) / Hkv;
+    p.target = few || always || 3 * p.tiles < target ? target : 0;
+    p.min_units = 4;
+    // Items are sum of tiles * ceil(units / slice) <= work / slice + tiles, work / slice <= target up to
+    // the rounding of the fp32 sum; and no tile has more slices than keys allow.
+    const int64_t most = ((keys + kUnit - 1) / kUnit + p.min_units - 1) / p.min_units;
     p.items = p.tiles + (p.target ? p.target + 8 : 0);
+    if (p.target && p.tiles * (most > 1 ? most : 1) < p.items)
+        p.items = p.tiles * (most > 1 ? most : 1);
     return p;
 }
 
 }  // namespace
 
-AttnPlan attn_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t P)
+AttnPlan attn_plan(int64_t T, int64_t S, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t P)
 {
     AttnPlan p{};
     const int64_t rows = T * (Hq / Hkv);
-    p.main = plan_part(rows, B < T ? B : T, Hkv, P > 0);
+    p.main = plan_part(rows, B < T ? B : T, S, Hkv, P > 0);
     p.main.o_off = 0;
     auto slots = [&](const AttnPart &x) { return x.target ? x.items * Hkv * x.bm : (int64_t)0; };
     int64_t at = round_up(slots(p.main) * D * 4, 256);
     p.main.l_off = at;
     at += round_up(slots(p.main) * 4, 256);
     if (P > 0) {
-        p.pre = plan_part(rows, 1, Hkv, true);
+        p.pre = plan_part(rows, 1, P, Hkv, true);
         p.pre.o_off = at;
         at += round_up(slots(p.pre) * D * 4, 256);
         p.pre.l_off = at;
@@ -1102,18 +1182,14 @@ hipError_t launch_attention(const AttnArgs &args, const AttnArgs &prefix, const 
         pre.ws_o = reinterpret_cast<float *>(ws + p.pre.o_off);
         pre.ws_l = reinterpret_cast<float *>(ws + p.pre.l_off);
         pre.pieced = 1;
-        if (hipError_t e = run_type(pre, p.pre, type, out_type, s))
-            return e;
     }
-    if (hipError_t e = run_type(a, p.main, type, out_type, s))
+    if (hipError_t e = run_type(a, pre, p, type, out_type, s))
         return e;
     if (!p.main.target)
         return hipSuccess;
-    // Rows of few-row tiles and of a shared prefix have many slices, those of cut prompts two or three.
-    const bool many = p.main.bm == kFewRows || prefix.shared;
-    return out_type == kF32   ? run_combine<float>(a, pre, p, many, s)
-           : type == kBF16 ? run_combine<bf16_t>(a, pre, p, many, s)
-                              : run_combine<f16_t>(a, pre, p, many, s);
+    return out_type == kF32 ? run_combine<float>(a, pre, p, s)
+           : type == kBF16  ? run_combine<bf16_t>(a, pre, p, s)
+                            : run_combine<f16_t>(a, pre, p, s);
 }
 
 }  // namespace bt

@@ -481,7 +481,7 @@ bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int
  * the prefix: 16-byte aligned with strides multiples of 8, row strides of k, v and the prefix at
  * most 2^23; out: aligned to four elements. tokens <= BT_MAX_DIM, tokens * heads < 2^31, scale
  * finite and positive. out and lse must not overlap the inputs.
- *   workspace    bt_attention_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim, prefix)
+ *   workspace    bt_attention_workspace_bytes(tokens, keys, seqs, heads, kv_heads, head_dim, prefix)
  *                bytes of device scratch, 256-byte aligned, or NULL when that is 0; contents on
  *                entry are ignored. Calls sharing one must not overlap.
  */
@@ -495,8 +495,8 @@ typedef struct {
     int64_t prefix_k_row, prefix_k_head, prefix_v_row, prefix_v_head;
     int64_t out_row, out_head;
 } bt_attention_shape;
-size_t bt_attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads,
-                                    int64_t head_dim, int64_t prefix);
+size_t bt_attention_workspace_bytes(int64_t tokens, int64_t keys, int64_t seqs, int64_t heads,
+                                    int64_t kv_heads, int64_t head_dim, int64_t prefix);
 bt_status bt_attention(const bt_attention_shape *shape, const void *q, const void *k, const void *v,
                        const int32_t *q_start, const int32_t *k_start, const int32_t *k_len,
                        const void *prefix_k, const void *prefix_v, void *out, float *lse,
