@@ -8,7 +8,7 @@
 // atomics: the same call gives the same bits.
 //
 // The tokens of a tile (16) are worked off adapter by adapter, each adapter's weights being read
-// once for all of the tile's tokens that use it (once per four of them in the few-tokens form). The
+// once for all of the tile's tokens that use it (once per two of them in the few-tokens form). The
 // other tokens of the tile take no part in it: an adapter's weights, whatever they hold, never reach
 // a token that does not use it.
 //  * Few tokens (k_lora_shrink_few, k_lora_expand_few; up to kFewTokens): a workgroup per (tile,
@@ -35,12 +35,13 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 16;        // tokens of a tile
-constexpr int kWaves = 4;
-constexpr int kStepK = 32 * kWaves;  // k of one workgroup step of k_lora_shrink
+constexpr int kWaves = 4;            // of a workgroup of k_lora_shrink_few
+constexpr int kDeepWaves = 8;        // of a workgroup of k_lora_shrink
+constexpr int kStepK = 32 * kDeepWaves;  // k of one workgroup step of k_lora_shrink
 constexpr int kMaxRank = 256;
 constexpr int kFewTokens = 128;      // largest M of the few-tokens kernels
 constexpr int kChunkK = 512;         // k of one wave step of k_lora_shrink_few: 8 per lane
-constexpr int kGroupTok = 4;         // tokens that share one reading of an adapter there
+constexpr int kGroupTok = 2;         // tokens that share one reading of an adapter there
 
 struct LoraArgs {
     const void *A, *B;
@@ -51,9 +52,93 @@ struct LoraArgs {
     int64_t M, N, K;
     int L, R, Rp;  // Rp: R rounded up to 16
     int slices, kslice, leads;  // leads: workgroups per tile of the few-tokens kernels
-    int vec_x, vec_a, vec_b, vec_y;
+    int quads;  // N is a multiple of 4: outputs move four at a time
     RowGroups groups;
 };
+
+// Number of bf16 pieces that an element type is cut into without rounding.
+template <typename W>
+struct Terms {
+    static constexpr int n = 1;
+};
+template <>
+struct Terms<f16_t> {
+    static constexpr int n = 2;
+};
+template <>
+struct Terms<float> {
+    static constexpr int n = 3;
+};
+
+// Memory is read through buffers whose range check gives 0 outside: a lane that wants nothing asks for
+// kOutside, and no load sits in a branch of its own (loads in divergent branches wait for each other).
+constexpr uint32_t kOutside = 0x7FFFFFF0u;
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)min(bytes, (int64_t)0x7FFFFF00),
+                                             0x00020000);
+}
+
+// Eight consecutive values as they are in memory.
+template <typename W>
+struct Raw8 {
+    u32x4 q[sizeof(W) / 2];
+};
+
+// Elements 0 .. n - 1 (n <= 8, none if <= 0) from byte offset `at`; the others are 0. VEC: 16-byte
+// reads; n is then 8 or <= 0.
+template <typename W, bool VEC>
+__device__ inline Raw8<W> fetch8(__amdgpu_buffer_rsrc_t from, uint32_t at, int n)
+{
+    Raw8<W> out;
+    if constexpr (VEC) {
+        const uint32_t off = n > 0 ? at : kOutside;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(W) / 2; ++i)
+            out.q[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, off, 16 * i, 0));
+    } else if constexpr (sizeof(W) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            out.q[j / 4][j % 4] = __builtin_amdgcn_raw_buffer_load_b32(from, j < n ? at + 4 * j : kOutside, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(from, j < n ? at + 2 * j : kOutside, 0, 0);
+            const uint32_t hi =
+                (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(from, j + 1 < n ? at + 2 * j + 2 : kOutside, 0, 0);
+            out.q[0][j / 2] = lo | hi << 16;
+        }
+    }
+    return out;
+}
+
+// Elements from n on set to 0, whatever they hold.
+template <typename W>
+__device__ inline void keep(Raw8<W> &r, int n)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(W) == 4)
+            r.q[j / 4][j % 4] = j < n ? r.q[j / 4][j % 4] : 0u;
+        else
+            r.q[0][j / 2] = j < n ? r.q[0][j / 2] : r.q[0][j / 2] & (j & 1 ? 0x0000FFFFu : 0xFFFF0000u);
+    }
+}
+
+template <typename W>
+__device__ inline float raw_value(const Raw8<W> &r, int j)  // j: a constant once unrolled
+{
+    if constexpr (Terms<W>::n == 3) {
+        return __uint_as_float(r.q[j / 4][j % 4]);
+    } else {
+        const uint32_t u = r.q[0][j / 2];
+        if constexpr (Terms<W>::n == 1)
+            return __uint_as_float(j & 1 ? u & 0xFFFF0000u : u << 16);
+        else
+            return (float)__builtin_bit_cast(f16_t, (uint16_t)(u >> (16 * (j & 1))));
+    }
+}
 
 // Eight values as up to three bf16 operands whose sum is exact.
 template <int TERMS>
@@ -80,53 +165,15 @@ __device__ inline Pieces<TERMS> cut(const float (&x)[8])
 }
 
 template <typename W>
-struct Terms {
-    static constexpr int n = 1;
-};
-template <>
-struct Terms<f16_t> {
-    static constexpr int n = 2;
-};
-template <>
-struct Terms<float> {
-    static constexpr int n = 3;
-};
-
-// Values p[0 .. min(n, 8)) as pieces, zeros behind them (n <= 0: nothing is read). vec: p is
-// 16-byte aligned (32 bytes are then read as 16-byte pieces wherever n >= 8).
-template <typename W>
-__device__ inline Pieces<Terms<W>::n> load_pieces(const W *p, int64_t n, bool vec)
+__device__ inline Pieces<Terms<W>::n> pieces(const Raw8<W> &r)
 {
     if constexpr (Terms<W>::n == 1) {
-        Pieces<1> out;
-        out.p[0] = u32x4{0, 0, 0, 0};
-        if (vec && n >= 8) {
-            out.p[0] = *reinterpret_cast<const u32x4 *>(p);
-        } else {
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n)
-                    out.p[0][j / 2] |= (uint32_t)h[j] << (16 * (j & 1));
-        }
-        return out;
+        return Pieces<1>{{r.q[0]}};
     } else {
-        float x[8] = {};
-        if (vec && n >= 8) {
-            float lo[4], hi[4];
-            load4(p, lo);
-            load4(p + 4, hi);
+        float x[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = lo[j];
-                x[4 + j] = hi[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n)
-                    x[j] = (float)p[j];
-        }
+        for (int j = 0; j < 8; ++j)
+            x[j] = raw_value(r, j);
         return cut<Terms<W>::n>(x);
     }
 }
@@ -160,19 +207,20 @@ __device__ inline int adapter_rank(const LoraArgs &a, int ad)
     return a.ranks ? max(0, min(a.ranks[ad], a.R)) : a.R;
 }
 
-template <typename W, int RT>
-__global__ __launch_bounds__(256) void k_lora_shrink(LoraArgs a)
+// k_lora_shrink: 16 tokens against RT rank tiles of 16; eight waves take every eighth step of 32 k.
+template <typename W, int RT, bool VEC>
+__global__ __launch_bounds__(64 * kDeepWaves) void k_lora_shrink(LoraArgs a)
 {
-    __shared__ f32x4 part[kWaves][RT][64];
+    __shared__ f32x4 part[kDeepWaves][RT][64];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int t = lane & 15, g = lane >> 4;
     const int64_t m0 = (int64_t)blockIdx.x * kTile;
     const int mine = lane_adapter(a, m0, t);
     uint32_t todo = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
     const int tpg = a.Rp / 16, tiles = tpg * a.groups.n;
-    const int64_t k0 = (int64_t)blockIdx.y * a.kslice;
-    const int64_t k1 = min(k0 + a.kslice, a.K);
-    const float *xrow = a.X + min(m0 + t, a.M - 1) * a.K;
+    const int k0 = (int)blockIdx.y * a.kslice, k1 = (int)min((int64_t)k0 + a.kslice, a.K);
+    const int row_x = (int)a.K * 4, row_w = (int)(a.K * sizeof(W));
+    const __amdgpu_buffer_rsrc_t xs = buffer_of(a.X + m0 * a.K, min((int64_t)kTile, a.M - m0) * row_x);
 
     while (todo) {
         const int lead = __builtin_ctz(todo);
@@ -180,38 +228,45 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LoraArgs a)
         const uint32_t same = (uint32_t)__ballot(mine == ad) & 0xFFFFu;
         todo &= ~same;
         const int rank = adapter_rank(a, ad);
-        const W *wrow[RT];
+        // an adapter's A (all groups, at most 8 * 256 rows) is below 2^31 bytes
+        const __amdgpu_buffer_rsrc_t ws =
+            buffer_of(static_cast<const W *>(a.A) + (int64_t)ad * a.groups.n * a.R * a.K, (int64_t)a.groups.n * a.R * row_w);
+        uint32_t at[RT];
+        bool in[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            const int tile = blockIdx.z * RT + i;
-            const int r = (tile % tpg) * 16 + t;
-            wrow[i] = nullptr;
-            if (tile < tiles && r < rank)
-                wrow[i] = static_cast<const W *>(a.A) + ((int64_t)ad * a.groups.n * a.R + (tile / tpg) * a.R + r) * a.K;
+            const int tile = blockIdx.z * RT + i, r = (tile % tpg) * 16 + t;
+            in[i] = tile < tiles && r < rank;
+            at[i] = (uint32_t)((tile / tpg) * a.R + r) * (uint32_t)row_w;
         }
         f32x4 acc[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i)
             acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-        for (int64_t kk = k0 + 32 * wave; kk < k1; kk += kStepK) {
-            const int64_t k = kk + 8 * g;
-            const Pieces<3> x = load_pieces<float>(xrow + k, k1 - k, a.vec_x);
+        for (int kk = k0 + 32 * wave; kk < k1; kk += kStepK) {
+            const int k = kk + 8 * g, n = min(8, k1 - k);
+            const Raw8<float> xr = fetch8<float, VEC>(xs, (uint32_t)t * row_x + 4u * k, n);
+            Raw8<W> wr[RT];
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-                acc[i] = mma(load_pieces<W>(wrow[i] + k, wrow[i] ? k1 - k : 0, a.vec_a), x, acc[i]);
+                wr[i] = fetch8<W, VEC>(ws, at[i] + (uint32_t)sizeof(W) * k, in[i] ? n : 0);
+            const Pieces<3> x = pieces(xr);
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                acc[i] = mma(pieces(wr[i]), x, acc[i]);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i)
             part[wave][i][lane] = acc[i];
         __syncthreads();
-        for (int e = threadIdx.x; e < RT * 64; e += 256) {
+        for (int e = threadIdx.x; e < RT * 64; e += 64 * kDeepWaves) {
             const int i = e >> 6, l = e & 63;
             const int tile = blockIdx.z * RT + i;
             if (tile < tiles && (same >> (l & 15) & 1)) {
                 f32x4 s = part[0][i][l];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w)
+                for (int w = 1; w < kDeepWaves; ++w)
                     s += part[w][i][l];
                 s *= a.scale[ad];
                 const int64_t m = m0 + (l & 15);
@@ -230,33 +285,41 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LoraArgs a)
 // that a wave waits twice: for its tokens' adapters, and for what depends on them.
 constexpr int kExpandN = 64, kExpandT = kExpandN / 16;
 
-template <typename W>
+template <typename W, bool VEC>
 __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs a)
 {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int t = lane & 15, g = lane >> 4;
-    // token tiles vary fastest over workgroups, outputs over a workgroup's waves
-    const int64_t m0 = (int64_t)blockIdx.x * kTile, n0 = ((int64_t)blockIdx.y * 4 + wave) * kExpandN;
+    // outputs vary fastest, over a workgroup's waves and over workgroups
+    const int64_t blocks = (a.N + 4 * kExpandN - 1) / (4 * kExpandN);
+    const int64_t m0 = (int64_t)(blockIdx.x / blocks) * kTile;
+    const int64_t n0 = ((int64_t)(blockIdx.x % blocks) * 4 + wave) * kExpandN;
     if (n0 >= a.N)
         return;
+    const int cols = (int)min((int64_t)kExpandN, a.N - n0);
     const int mine = lane_adapter(a, m0, t);
-    f32x4 y[kExpandT];
+    // this lane's outputs: token t, columns 16 i + 4 g .. + 3 of the wave's
+    const int64_t corner = m0 * a.N + n0;
+    const int64_t span = ((min((int64_t)kTile, a.M - m0) - 1) * a.N + cols) * 4;
+    uint32_t yoff[kExpandT];
 #pragma unroll
     for (int i = 0; i < kExpandT; ++i) {
-        y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int64_t n = n0 + 16 * i + 4 * g;
-        if (a.Y0 && m0 + t < a.M) {
-            const float *p = a.Y0 + (m0 + t) * a.N + n;
-            if (a.vec_y) {
-                if (n < a.N)
-                    y[i] = *reinterpret_cast<const f32x4 *>(p);
-            } else {
+        const int c = 16 * i + 4 * g;
+        yoff[i] = mine > -2 && c < cols ? (uint32_t)(t * a.N + c) * 4u : kOutside;
+    }
+    const __amdgpu_buffer_rsrc_t ys = buffer_of(a.Y0 ? a.Y0 + corner : nullptr, a.Y0 ? span : 0);
+    f32x4 y[kExpandT];
+    if (a.quads) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n + j < a.N)
-                        y[i][j] = p[j];
-            }
-        }
+        for (int i = 0; i < kExpandT; ++i)
+            y[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ys, yoff[i], 0, 0));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kExpandT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                y[i][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                        ys, 16 * i + 4 * g + j < cols ? yoff[i] + 4 * j : kOutside, 0, 0));
     }
     uint32_t todo = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
     const int64_t hrow = min(m0 + t, a.M - 1) * a.groups.n, hstep = a.M * a.groups.n * a.Rp;
@@ -266,9 +329,11 @@ __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs a)
         const uint32_t same = (uint32_t)__ballot(mine == ad) & 0xFFFFu;
         todo &= ~same;
         const int rank = adapter_rank(a, ad);
+        const __amdgpu_buffer_rsrc_t bs = buffer_of(static_cast<const W *>(a.B) + ((int64_t)ad * a.N + n0) * a.R,
+                                                    (int64_t)cols * a.R * sizeof(W));
         for (int grp = 0; grp < a.groups.n; ++grp) {
             const int64_t lo = grp ? a.groups.end[grp - 1] : 0, hi = a.groups.end[grp];
-            if (hi <= n0 || lo >= n0 + kExpandN)
+            if (hi <= n0 || lo >= n0 + cols)
                 continue;
             f32x4 sum[kExpandT];
 #pragma unroll
@@ -276,6 +341,13 @@ __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs a)
                 sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
             for (int rr = 0; rr < a.Rp; rr += 32) {
                 const int r = rr + 8 * g;
+                Raw8<W> wr[kExpandT];
+#pragma unroll
+                for (int i = 0; i < kExpandT; ++i) {
+                    const int c = 16 * i + t;
+                    const bool in = n0 + c >= lo && n0 + c < hi;
+                    wr[i] = fetch8<W, VEC>(bs, (uint32_t)(c * a.R + r) * (uint32_t)sizeof(W), in ? min(8, rank - r) : 0);
+                }
                 // this token's H (other tokens' columns are computed from theirs and not taken)
                 const float *src = a.ws + (hrow + grp) * a.Rp + min(r, a.Rp - 8);
                 f32x4 h0 = {0.f, 0.f, 0.f, 0.f}, h1 = {0.f, 0.f, 0.f, 0.f};
@@ -291,13 +363,13 @@ __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs a)
                     h[4 + j] = r < a.Rp ? h1[j] : 0.f;
                 }
                 const Pieces<3> x = cut<3>(h);
+                if (VEC && (rank & 7) && rr + 32 > rank)
 #pragma unroll
-                for (int i = 0; i < kExpandT; ++i) {
-                    const int64_t n = n0 + 16 * i + t;
-                    const bool in = n >= lo && n < hi;
-                    const W *w = static_cast<const W *>(a.B) + ((int64_t)ad * a.N + (in ? n : lo)) * a.R + r;
-                    sum[i] = mma(load_pieces<W>(w, in ? rank - r : 0, a.vec_b), x, sum[i]);
-                }
+                    for (int i = 0; i < kExpandT; ++i)
+                        keep(wr[i], rank - r);
+#pragma unroll
+                for (int i = 0; i < kExpandT; ++i)
+                    sum[i] = mma(pieces(wr[i]), x, sum[i]);
             }
             if (same >> t & 1)
 #pragma unroll
@@ -305,66 +377,18 @@ __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs a)
                     y[i] += sum[i];
         }
     }
-    if (m0 + t >= a.M)
-        return;
+    const __amdgpu_buffer_rsrc_t out = buffer_of(a.Y + corner, span);
+    if (a.quads) {
 #pragma unroll
-    for (int i = 0; i < kExpandT; ++i) {
-        const int64_t n = n0 + 16 * i + 4 * g;
-        float *p = a.Y + (m0 + t) * a.N + n;
-        if (a.vec_y) {
-            if (n < a.N)
-                *reinterpret_cast<f32x4 *>(p) = y[i];
-        } else {
+        for (int i = 0; i < kExpandT; ++i)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[i]), out, yoff[i], 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kExpandT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (n + j < a.N)
-                    p[j] = y[i][j];
-        }
-    }
-}
-
-// Eight weights p[0 .. min(n, 8)) as fp32, zeros behind them (n <= 0: nothing is read).
-template <typename W>
-struct Raw8 {
-    u32x4 q[Terms<W>::n == 3 ? 2 : 1];
-};
-template <typename W>
-__device__ inline Raw8<W> load_raw(const W *p, int64_t n, bool vec)
-{
-    Raw8<W> out;
-    if (vec && n >= 8) {
-        out.q[0] = *reinterpret_cast<const u32x4 *>(p);
-        if constexpr (Terms<W>::n == 3)
-            out.q[1] = *reinterpret_cast<const u32x4 *>(p + 4);
-        return out;
-    }
-    out.q[0] = u32x4{0, 0, 0, 0};
-    if constexpr (Terms<W>::n == 3) {
-        out.q[1] = u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n)
-                out.q[j / 4][j % 4] = __float_as_uint(p[j]);
-    } else {
-        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n)
-                out.q[0][j / 2] |= (uint32_t)h[j] << (16 * (j & 1));
-    }
-    return out;
-}
-template <typename W>
-__device__ inline float raw_value(const Raw8<W> &r, int j)  // j: a constant once unrolled
-{
-    if constexpr (Terms<W>::n == 3) {
-        return __uint_as_float(r.q[j / 4][j % 4]);
-    } else {
-        const uint32_t u = r.q[0][j / 2];
-        if constexpr (Terms<W>::n == 1)
-            return __uint_as_float(j & 1 ? u & 0xFFFF0000u : u << 16);
-        else
-            return (float)__builtin_bit_cast(f16_t, (uint16_t)(u >> (16 * (j & 1))));
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[i][j]), out,
+                                                      16 * i + 4 * g + j < cols ? yoff[i] + 4 * j : kOutside, 0, 0);
     }
 }
 
@@ -395,12 +419,12 @@ __device__ inline int take_tokens(uint32_t &todo, int (&tok)[kGroupTok])
     return n;
 }
 
-// k_lora_shrink_few: 16 rows of one adapter's A against up to four of its tokens at a time. A lane
+// k_lora_shrink_few: 16 rows of one adapter's A against up to two of its tokens at a time. A lane
 // keeps eight k of the tokens in registers; every row is then one contiguous 1 KiB read of the wave,
 // all sixteen in flight together. The sixteen rows' partial sums are added over the lanes by swaps
 // that halve the number of values each time.
-template <typename W>
-__global__ __launch_bounds__(256) void k_lora_shrink_few(LoraArgs a)
+template <typename W, bool VEC>
+__global__ __launch_bounds__(256, 3) void k_lora_shrink_few(LoraArgs a)
 {
     __shared__ float part[kWaves][kGroupTok][16];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -412,9 +436,13 @@ __global__ __launch_bounds__(256) void k_lora_shrink_few(LoraArgs a)
     const int tpg = a.Rp / 16, grp = blockIdx.z / tpg, r0 = (blockIdx.z % tpg) * 16;
     const int rank = adapter_rank(a, ad);
     const int rows = min(16, rank - r0);  // may be <= 0: H is 0 there
-    const W *w = static_cast<const W *>(a.A) + (((int64_t)ad * a.groups.n + grp) * a.R + r0) * a.K;
+    const int row_w = (int)(a.K * sizeof(W));
+    const __amdgpu_buffer_rsrc_t ws =
+        buffer_of(static_cast<const W *>(a.A) + (((int64_t)ad * a.groups.n + grp) * a.R + r0) * a.K,
+                  (int64_t)max(rows, 0) * row_w);
+    const __amdgpu_buffer_rsrc_t xs = buffer_of(a.X + m0 * a.K, min((int64_t)kTile, a.M - m0) * a.K * 4);
     const float scale = a.scale[ad];
-    const int64_t k0 = (int64_t)blockIdx.y * a.kslice, k1 = min(k0 + a.kslice, a.K);
+    const int k0 = (int)blockIdx.y * a.kslice, k1 = (int)min((int64_t)k0 + a.kslice, a.K);
     while (same) {
         int tok[kGroupTok];
         const int nt = take_tokens(same, tok);
@@ -424,27 +452,29 @@ __global__ __launch_bounds__(256) void k_lora_shrink_few(LoraArgs a)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 acc[i][r] = 0.f;
-        for (int64_t kk = k0 + kChunkK * wave; kk < k1; kk += kChunkK * kWaves) {
-            const int64_t k = kk + 8 * lane;
+        for (int kk = k0 + kChunkK * wave; kk < k1; kk += kChunkK * kWaves) {
+            const int k = kk + 8 * lane, n = min(8, k1 - k);
             Raw8<W> raw[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                raw[r] = load_raw(w + r * a.K + k, r < rows ? k1 - k : 0, a.vec_a);
+            for (int r = 0; r < 16; ++r)  // rows from `rows` on are outside the buffer
+                raw[r] = fetch8<W, VEC>(ws, (uint32_t)r * (uint32_t)row_w + (uint32_t)sizeof(W) * k, n);
+            float x[kGroupTok][8];  // a token that is not there: the last one again
 #pragma unroll
             for (int i = 0; i < kGroupTok; ++i) {
-                if (i >= nt)
-                    break;
-                const Raw8<float> xr = load_raw(a.X + (m0 + tok[i]) * a.K + k, k1 - k, a.vec_x);
-                float x[8];
+                const Raw8<float> xr = fetch8<float, VEC>(xs, (uint32_t)(tok[i] * (int)a.K + k) * 4u, n);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    x[j] = raw_value(xr, j);
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        acc[i][r] = __builtin_fmaf(raw_value(raw[r], j), x[j], acc[i][r]);
+                    x[i][j] = raw_value(xr, j);
             }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = raw_value(raw[r], j);
+#pragma unroll
+                    for (int i = 0; i < kGroupTok; ++i)
+                        acc[i][r] = __builtin_fmaf(v, x[i][j], acc[i][r]);
+                }
         }
 #pragma unroll
         for (int i = 0; i < kGroupTok; ++i) {
@@ -499,7 +529,7 @@ __global__ __launch_bounds__(256) void k_lora_shrink_few(LoraArgs a)
 // broadcasts). Tokens without an adapter are one more group, which only copies Y0.
 constexpr int kFewN = 256, kFewR = 64;
 
-template <typename W>
+template <typename W, bool VEC>
 __global__ __launch_bounds__(256) void k_lora_expand_few(LoraArgs a)
 {
     __shared__ __attribute__((aligned(16))) float hs[kGroupTok][kMaxRank];
@@ -519,11 +549,20 @@ __global__ __launch_bounds__(256) void k_lora_expand_few(LoraArgs a)
         return;
     }
     const int rank = adapter_rank(a, ad);
-    const W *w = static_cast<const W *>(a.B) + ((int64_t)ad * a.N + min(n, a.N - 1)) * a.R;
+    // rows past N are outside the buffer
+    const __amdgpu_buffer_rsrc_t bs = buffer_of(static_cast<const W *>(a.B) + ((int64_t)ad * a.N + nb) * a.R,
+                                                min((int64_t)kFewN, a.N - nb) * a.R * sizeof(W));
+    const uint32_t brow = threadIdx.x * (uint32_t)(a.R * sizeof(W));
+    auto row8 = [&](int r) __attribute__((always_inline)) {
+        Raw8<W> x = fetch8<W, VEC>(bs, brow + (uint32_t)sizeof(W) * r, min(8, rank - r));
+        if (VEC && rank - r < 8)
+            keep(x, rank - r);
+        return x;
+    };
     Raw8<W> raw[kFewR / 8];
 #pragma unroll
     for (int c = 0; c < kFewR / 8; ++c)
-        raw[c] = load_raw(w + 8 * c, rank - 8 * c, a.vec_b);
+        raw[c] = row8(8 * c);
     while (same) {
         int tok[kGroupTok];
         const int nt = take_tokens(same, tok);
@@ -559,7 +598,7 @@ __global__ __launch_bounds__(256) void k_lora_expand_few(LoraArgs a)
                 Raw8<W> v[kFewR / 8];
 #pragma unroll
                 for (int c = 0; c < kFewR / 8; ++c)
-                    v[c] = r0 ? load_raw(w + r0 + 8 * c, rank - r0 - 8 * c, a.vec_b) : raw[c];
+                    v[c] = r0 ? row8(r0 + 8 * c) : raw[c];
 #pragma unroll
                 for (int c = 0; c < kFewR / 8; ++c) {
                     if (r0 + 8 * c >= rank)
@@ -602,46 +641,60 @@ LoraPlan lora_plan(int64_t M, int64_t K, int64_t R, int64_t groups)
     p.ztiles = (rank_tiles + p.rt - 1) / p.rt;
     p.tiles = (M + kTile - 1) / kTile;
     p.leads = (int)(M < kTile ? M : kTile);
-    // K in as many slices as give about four workgroups per CU, each at least one wave step, and no
-    // more than eight (the expand kernels read every slice's partial sums).
+    // K in as many slices as give four workgroups per CU (eight waves each, one is enough), each at least
+    // one step, and few: the expand kernels read every slice's partial sums, and with many tokens they do
+    // so for every 64 outputs.
     const int64_t wgs = (p.few ? p.tiles * p.leads : p.tiles) * p.ztiles;
     const int64_t unit = p.few ? kChunkK : kStepK;             // smallest slice
     const int64_t whole = p.few ? kChunkK * kWaves : kStepK;   // k of a workgroup step
     const int64_t steps = K > 0 ? (K + whole - 1) / whole : 1;
-    int64_t slices = (1024 + wgs - 1) / wgs;
+    const int64_t want = p.few ? 1024 : 256, most = p.few ? 8 : 4;
+    int64_t slices = (want + wgs - 1) / wgs;
     slices = slices < steps ? slices : steps;
-    slices = slices < 8 ? slices : 8;
+    slices = slices < most ? slices : most;
     const int64_t k = K > 0 ? K : 1;
     p.kslice = round_up((k + slices - 1) / slices, unit);
     p.slices = (int)((k + p.kslice - 1) / p.kslice);
     return p;
 }
 
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+template <typename W, bool VEC>
+hipError_t launch_shrink(const LoraArgs &a, const LoraPlan &p, hipStream_t s)
+{
+    const dim3 grid((unsigned)(p.tiles * (p.few ? p.leads : 1)), (unsigned)p.slices, (unsigned)p.ztiles);
+    if (p.few)
+        k_lora_shrink_few<W, VEC><<<grid, 64 * kWaves, 0, s>>>(a);
+    else if (p.rt == 1)
+        k_lora_shrink<W, 1, VEC><<<grid, 64 * kDeepWaves, 0, s>>>(a);
+    else if (p.rt == 2)
+        k_lora_shrink<W, 2, VEC><<<grid, 64 * kDeepWaves, 0, s>>>(a);
+    else
+        k_lora_shrink<W, 4, VEC><<<grid, 64 * kDeepWaves, 0, s>>>(a);
+    return hipGetLastError();
+}
 
+template <typename W, bool VEC>
+hipError_t launch_expand(const LoraArgs &a, const LoraPlan &p, hipStream_t s)
+{
+    if (p.few) {
+        const dim3 grid((unsigned)(p.tiles * p.leads), (unsigned)((a.N + kFewN - 1) / kFewN));
+        k_lora_expand_few<W, VEC><<<grid, 256, 0, s>>>(a);
+    } else {
+        const int64_t blocks = p.tiles * ((a.N + 4 * kExpandN - 1) / (4 * kExpandN));
+        k_lora_expand<W, VEC><<<(unsigned)blocks, 256, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+// 16-byte reads where rows are whole eights of values and start on 4 bytes (a buffer load's alignment).
 template <typename W>
 hipError_t launch_weights(const LoraArgs &a, const LoraPlan &p, hipStream_t s)
 {
-    if (p.few) {
-        const unsigned gx = (unsigned)(p.tiles * p.leads);
-        k_lora_shrink_few<W><<<dim3(gx, (unsigned)p.slices, (unsigned)p.ztiles), 256, 0, s>>>(a);
-        if (hipError_t e = hipGetLastError())
-            return e;
-        k_lora_expand_few<W><<<dim3(gx, (unsigned)((a.N + kFewN - 1) / kFewN)), 256, 0, s>>>(a);
-        return hipGetLastError();
-    }
-    const dim3 shrink((unsigned)p.tiles, (unsigned)p.slices, (unsigned)p.ztiles);
-    if (p.rt == 1)
-        k_lora_shrink<W, 1><<<shrink, 256, 0, s>>>(a);
-    else if (p.rt == 2)
-        k_lora_shrink<W, 2><<<shrink, 256, 0, s>>>(a);
-    else
-        k_lora_shrink<W, 4><<<shrink, 256, 0, s>>>(a);
-    if (hipError_t e = hipGetLastError())
+    const bool vec_a = a.K % 8 == 0 && (reinterpret_cast<uintptr_t>(a.A) & 3) == 0;
+    const bool vec_b = a.R % 8 == 0 && (reinterpret_cast<uintptr_t>(a.B) & 3) == 0;
+    if (hipError_t e = vec_a ? launch_shrink<W, true>(a, p, s) : launch_shrink<W, false>(a, p, s))
         return e;
-    const dim3 expand((unsigned)p.tiles, (unsigned)((a.N + 4 * kExpandN - 1) / (4 * kExpandN)));
-    k_lora_expand<W><<<expand, 256, 0, s>>>(a);
-    return hipGetLastError();
+    return vec_b ? launch_expand<W, true>(a, p, s) : launch_expand<W, false>(a, p, s);
 }
 
 }  // namespace
@@ -656,7 +709,6 @@ hipError_t launch_lora(const void *A, const void *B, int w_type, const float *sc
                        int64_t M, int64_t N, int64_t K, float *Y, void *workspace, hipStream_t s)
 {
     const LoraPlan p = lora_plan(M, K, R, groups.n);
-    const int wb = type_bytes(w_type);
     LoraArgs a;
     a.A = A;
     a.B = B;
@@ -676,10 +728,7 @@ hipError_t launch_lora(const void *A, const void *B, int w_type, const float *sc
     a.leads = p.leads;
     a.slices = p.slices;
     a.kslice = (int)p.kslice;
-    a.vec_x = al16(X) && K % 4 == 0;
-    a.vec_a = al16(A) && K * wb % 16 == 0;
-    a.vec_b = al16(B) && R * wb % 16 == 0;
-    a.vec_y = al16(Y) && (!Y0 || al16(Y0)) && N % 4 == 0;
+    a.quads = N % 4 == 0;
     a.groups = groups;
     switch (w_type) {
     case kBF16: return launch_weights<bf16_t>(a, p, s);
