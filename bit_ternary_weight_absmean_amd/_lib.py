@@ -40,8 +40,7 @@ SIGNATURES = {
     "bt_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "bt_lora_apply": (_i32, [_vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
                              _vp]),
-    "bt_qk_norm_rope": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _i64, _i32,
-                               _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "bt_qk_norm_rope": (_i32, [_vp] * 11),
     "bt_attention_workspace_bytes": (_sz, [_i64] * 7),
     "bt_attention": (_i32, [_vp] * 13),
     "bt_status_str": (ctypes.c_char_p, [_i32]),

@@ -440,15 +440,12 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
-def _as_is(dev, *tensors):
-    """Whether every (tensor, dtype, shape) is a contiguous tensor of that type and shape on ``dev``: the
-    usual case, in as few steps as possible. Where not, the checks proper say what is wrong (or that a
-    strided tensor is fine)."""
-    for t, dtype, shape in tensors:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-                and t.is_contiguous()):
-            return False
-    return True
+def _is(t, dtype, shape, device) -> bool:
+    """Whether t is a contiguous tensor of that type and shape on device number ``device``: the usual
+    case, in as few steps as possible (a decode step's calls take a few microseconds). Where not, the
+    checks proper say what is wrong, or find that a strided tensor will do."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous())
 
 
 @lru_cache(maxsize=4096)
@@ -531,8 +528,9 @@ def lora_apply(X: torch.Tensor, adapters: LoraAdapters, index: torch.Tensor, bas
         raise ValueError("X must be a tensor [M, K]")
     M = X.shape[0]
     f32 = torch.float32
-    if not (_as_is(dev, (X, f32, (M, K)), (index, torch.int32, (M,)))
-            and (base is None or _as_is(dev, (base, f32, (M, N)))) and (out is None or _as_is(dev, (out, f32, (M, N))))):
+    at = X.get_device()
+    if not (X.device == dev and _is(X, f32, (M, K), at) and _is(index, torch.int32, (M,), at)
+            and (base is None or _is(base, f32, (M, N), at)) and (out is None or _is(out, f32, (M, N), at))):
         _need(X, "X", f32, (M, K), dev)
         _need(index, "index", torch.int32, (M,), dev)
         if base is not None:
@@ -574,27 +572,29 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, inv_freq: to
         raise ValueError(f"qkv must be [M, values], got shape {tuple(qkv.shape)}")
     if heads < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError(f"heads = {heads} must be a positive multiple of kv_heads = {kv_heads}")
-    (M, values), total, dev = qkv.shape, heads + 2 * kv_heads, qkv.device
+    (M, values), total, dev, at = qkv.shape, heads + 2 * kv_heads, qkv.device, qkv.get_device()
+    f32, i32 = torch.float32, torch.int32
     if values == 0 or values % total:
         raise ValueError(f"qkv rows of {values} values are not {total} heads")
     D = values // total
     if not (_on_device(qkv) and qkv.is_contiguous()):
         _need_strided(qkv, "qkv", qkv.dtype, qkv.shape, dev)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and not _as_is(dev, (w, torch.float32, (D,))):
-            _need(w, name, torch.float32, (D,), dev)
+    if q_weight is not None and not _is(q_weight, f32, (D,), at):
+        _need(q_weight, "q_weight", f32, (D,), dev)
+    if k_weight is not None and not _is(k_weight, f32, (D,), at):
+        _need(k_weight, "k_weight", f32, (D,), dev)
     rot = 0
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be a 1-D tensor of rot_dim / 2 angles")
         half = inv_freq.shape[0]
         rot = 2 * half
-        if not _as_is(dev, (inv_freq, torch.float64, (half,)), (positions, torch.int32, (M,))):
+        if not (_is(inv_freq, torch.float64, (half,), at) and _is(positions, i32, (M,), at)):
             _need(inv_freq, "inv_freq", torch.float64, None, dev)
-            _need(positions, "positions", torch.int32, (M,), dev)
+            _need(positions, "positions", i32, (M,), dev)
     if rows is not None:
-        if not _as_is(dev, (rows, torch.int32, (M,))):
-            _need(rows, "rows", torch.int32, (M,), dev)
+        if not _is(rows, i32, (M,), at):
+            _need(rows, "rows", i32, (M,), dev)
         if out is None:
             raise ValueError("rows names rows of the k and v given in out")
     if out is None:
@@ -606,18 +606,19 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, inv_freq: to
     out_type = _type_of(q, "q", _TYPES)
     room = k.shape[0] if rows is not None and isinstance(k, torch.Tensor) and k.dim() == 3 else M
     dt, kv = q.dtype, (room, kv_heads, D)
-    if not _as_is(dev, (q, dt, (M, heads, D)), (k, dt, kv), (v, dt, kv)):
+    if not (_is(q, dt, (M, heads, D), at) and _is(k, dt, kv, at) and _is(v, dt, kv, at)):
         _need_strided(q, "q", dt, (M, heads, D), dev, output=True)
         _need_strided(k, "k", dt, kv, dev, output=True)
         _need_strided(v, "v", dt, kv, dev, output=True)
     qs, ks, vs = q.stride(), k.stride(), v.stride()
-    _call(dev, lib().bt_qk_norm_rope, qkv.data_ptr(), in_type, qkv.stride(0), M, heads, kv_heads, D, _ptr(q_weight),
-          _ptr(k_weight), eps, _ptr(positions), _ptr(inv_freq), rot, interleaved, _ptr(rows), room, q.data_ptr(),
-          k.data_ptr(), v.data_ptr(), out_type, _SIX.pack(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1]))
+    shape = _HEADS_SHAPE.pack(M, heads, kv_heads, D, rot, qkv.stride(0), room, qs[0], qs[1], ks[0], ks[1], vs[0],
+                              vs[1], in_type, out_type, interleaved, eps)
+    _call(dev, lib().bt_qk_norm_rope, shape, qkv.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+          _ptr(inv_freq), _ptr(rows), q.data_ptr(), k.data_ptr(), v.data_ptr())
     return q, k, v
 
 
-_SIX = struct.Struct("6q")
+_HEADS_SHAPE = struct.Struct("13q3if")  # bt_heads_shape
 _ATTENTION_SHAPE = struct.Struct("7q3if12q")  # bt_attention_shape
 _HALF = {torch.bfloat16: 1, torch.float16: 2}
 
@@ -661,8 +662,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
         raise ValueError(f"{heads} heads are not a positive multiple of {kv_heads} key heads")
     kv, i32 = (S, kv_heads, D), torch.int32
-    if not (_on_device(q) and _as_is(dev, (q, dt, q.shape), (k, dt, kv), (v, dt, kv), (q_start, i32, (B + 1,)),
-                                     (k_start, i32, (B,)), (k_len, i32, (B,)))):
+    at = q.get_device()
+    if not (_on_device(q) and q.is_contiguous() and _is(k, dt, kv, at) and _is(v, dt, kv, at)
+            and _is(q_start, i32, (B + 1,), at) and _is(k_start, i32, (B,), at) and _is(k_len, i32, (B,), at)):
         _need_strided(q, "q", dt, q.shape, dev)
         _need_strided(k, "k", dt, kv, dev)
         _need_strided(v, "v", dt, kv, dev)
@@ -676,7 +678,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.
         if not isinstance(prefix_k, torch.Tensor) or prefix_k.dim() != 3:
             raise ValueError("prefix_k must be a tensor [P, kv_heads, D]")
         P = prefix_k.shape[0]
-        if not _as_is(dev, (prefix_k, dt, (P, kv_heads, D)), (prefix_v, dt, (P, kv_heads, D))):
+        if not (_is(prefix_k, dt, (P, kv_heads, D), at) and _is(prefix_v, dt, (P, kv_heads, D), at)):
             _need_strided(prefix_k, "prefix_k", dt, (P, kv_heads, D), dev)
             _need_strided(prefix_v, "prefix_v", dt, (P, kv_heads, D), dev)
         pk, pv = prefix_k.stride(), prefix_v.stride()
@@ -687,9 +689,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.
     ot = out.dtype
     if ot is not dt and ot is not torch.float32:
         raise TypeError(f"out must be {dt} or torch.float32, got {out.dtype}")
-    if not _as_is(dev, (out, ot, (T, heads, D))):
+    if not _is(out, ot, (T, heads, D), at):
         _need_strided(out, "out", ot, (T, heads, D), dev, output=True)
-    if lse is not None and not _as_is(dev, (lse, torch.float32, (T, heads))):
+    if lse is not None and not _is(lse, torch.float32, (T, heads), at):
         _need(lse, "lse", torch.float32, (T, heads), dev)
     need = _workspace_bytes("bt_attention_workspace_bytes", T, S, B, heads, kv_heads, D, P)
     if workspace is not None:

@@ -712,44 +712,47 @@ bt_status bt_lora_apply(const void *A, const void *B, int32_t w_type, const floa
                       "bt_lora_apply launch");
 }
 
-bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int64_t M, int64_t heads,
-                          int64_t kv_heads, int64_t head_dim, const float *q_weight, const float *k_weight, float eps,
-                          const int32_t *positions, const double *inv_freq, int64_t rot_dim, int32_t interleaved,
-                          const int32_t *rows, int64_t kv_rows, void *q, void *k, void *v, int32_t out_type,
-                          const int64_t *strides, void *stream)
+bt_status bt_qk_norm_rope(const bt_heads_shape *shape, const void *qkv, const float *q_weight, const float *k_weight,
+                          const int32_t *positions, const double *inv_freq, const int32_t *rows, void *q, void *k,
+                          void *v, void *stream)
 {
-    if (M < 0 || M > BT_MAX_DIM)
-        return fail(BT_ERR_SHAPE, "M = %lld outside [0, 2^23]", (long long)M);
-    if (heads < 1 || kv_heads < 1 || heads > 65536 || heads % kv_heads)
+    if (!shape)
+        return fail(BT_ERR_NULL, "shape is NULL");
+    const bt_heads_shape &s = *shape;
+    if (s.tokens < 0 || s.tokens > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "tokens = %lld outside [0, 2^23]", (long long)s.tokens);
+    if (s.heads < 1 || s.kv_heads < 1 || s.heads > 65536 || s.heads % s.kv_heads)
         return fail(BT_ERR_SHAPE, "heads = %lld, kv_heads = %lld: heads must be a multiple of kv_heads, at most 65536",
-                    (long long)heads, (long long)kv_heads);
-    if (head_dim < 8 || head_dim > BT_ROPE_MAX_HEAD_DIM || head_dim % 8)
-        return fail(BT_ERR_SHAPE, "head_dim = %lld is not a multiple of 8 in [8, %d]", (long long)head_dim,
+                    (long long)s.heads, (long long)s.kv_heads);
+    if (s.head_dim < 8 || s.head_dim > BT_ROPE_MAX_HEAD_DIM || s.head_dim % 8)
+        return fail(BT_ERR_SHAPE, "head_dim = %lld is not a multiple of 8 in [8, %d]", (long long)s.head_dim,
                     BT_ROPE_MAX_HEAD_DIM);
-    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8)
-        return fail(BT_ERR_SHAPE, "rot_dim = %lld is not a multiple of 8 in [0, head_dim]", (long long)rot_dim);
-    if (!(eps >= 0.0f) || eps > 3.0e38f)
+    if (s.rot_dim < 0 || s.rot_dim > s.head_dim || s.rot_dim % 8)
+        return fail(BT_ERR_SHAPE, "rot_dim = %lld is not a multiple of 8 in [0, head_dim]", (long long)s.rot_dim);
+    if (!(s.eps >= 0.0f) || s.eps > 3.0e38f)
         return fail(BT_ERR_SHAPE, "eps must be finite and not negative");
-    if (!known_type(in_type) || !known_type(out_type))
-        return fail(BT_ERR_UNSUPPORTED, "unknown element type %d or %d", in_type, out_type);
-    if (kv_rows < 0 || kv_rows > INT32_MAX || (!rows && kv_rows < M))
-        return fail(BT_ERR_SHAPE, "kv_rows = %lld for M = %lld tokens", (long long)kv_rows, (long long)M);
-    if (M == 0)
+    if (!known_type(s.in_type) || !known_type(s.out_type))
+        return fail(BT_ERR_UNSUPPORTED, "unknown element type %d or %d", s.in_type, s.out_type);
+    if (s.kv_rows < 0 || s.kv_rows > INT32_MAX || (!rows && s.kv_rows < s.tokens))
+        return fail(BT_ERR_SHAPE, "kv_rows = %lld for %lld tokens", (long long)s.kv_rows, (long long)s.tokens);
+    if (s.tokens == 0)
         return ok();
-    if (!qkv || !q || !k || !v || !strides || (rot_dim > 0 && (!positions || !inv_freq)))
-        return fail(BT_ERR_NULL, "NULL qkv, q, k, v, strides, positions or inv_freq");
-    const uintptr_t ib = 4 * type_size(in_type), ob = 4 * type_size(out_type);
-    bool quads = qkv_row % 4 == 0 && qkv_row >= 0;
-    for (int i = 0; i < 6; ++i)
-        quads = quads && strides[i] % 4 == 0 && strides[i] >= 0;
+    if (!qkv || !q || !k || !v || (s.rot_dim > 0 && (!positions || !inv_freq)))
+        return fail(BT_ERR_NULL, "NULL qkv, q, k, v, positions or inv_freq");
+    const uintptr_t ib = 4 * type_size(s.in_type), ob = 4 * type_size(s.out_type);
+    const int64_t strides[7] = {s.q_row, s.q_head, s.k_row, s.k_head, s.v_row, s.v_head, s.qkv_row};
+    bool quads = true;
+    for (int64_t x : strides)
+        quads = quads && x % 4 == 0 && x >= 0;
     if (!quads || !aligned(qkv, ib) || !aligned(q, ob) || !aligned(k, ob) || !aligned(v, ob) ||
         !aligned(q_weight, 16) || !aligned(k_weight, 16))
         return fail(BT_ERR_ALIGN, "arrays and strides must be aligned to four elements");
     if (!aligned(positions, 4) || !aligned(rows, 4) || !aligned(inv_freq, 8))
         return fail(BT_ERR_ALIGN, "positions, rows and inv_freq must be aligned to their elements");
-    return hip_status(bt::launch_qk_norm_rope(qkv, in_type, qkv_row, M, heads, kv_heads, head_dim, q_weight, k_weight,
-                                              eps, positions, inv_freq, rot_dim, interleaved != 0, rows, kv_rows, q, k,
-                                              v, out_type, strides, static_cast<hipStream_t>(stream)),
+    return hip_status(bt::launch_qk_norm_rope(qkv, s.in_type, s.qkv_row, s.tokens, s.heads, s.kv_heads, s.head_dim,
+                                              q_weight, k_weight, s.eps, positions, inv_freq, s.rot_dim,
+                                              s.interleaved != 0, rows, s.kv_rows, q, k, v, s.out_type, strides,
+                                              static_cast<hipStream_t>(stream)),
                       "bt_qk_norm_rope launch");
 }
 

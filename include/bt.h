@@ -431,31 +431,35 @@ bt_status bt_lora_apply(const void *A, const void *B, int32_t w_type, const floa
  * bt_qk_norm_rope -- from the fused QKV rows of a projection, in one pass: the norm of every
  * query and key head, the rotation by the token's position, and the conversion of Q, K and V
  * to the attention's type, K and V optionally straight into cache rows.
- *   qkv       [M] rows of (heads + 2 * kv_heads) * head_dim values of in_type (Q heads, K
+ *   qkv       `tokens` rows of (heads + 2 * kv_heads) * head_dim values of in_type (Q heads, K
  *             heads, V heads), qkv_row elements apart.
  *   q_weight, k_weight  [head_dim] fp32, or NULL for no norm:
  *             x * weight / sqrt(mean(x^2) + eps) per head.
  *   rotation  of each head's first rot_dim values by t = positions[m] * inv_freq[p]:
  *             (a, b) -> (a cos t - b sin t, b cos t + a sin t) for the pairs
  *             (p, p + rot_dim/2), or (2p, 2p + 1) with interleaved != 0. inv_freq [rot_dim/2]
- *             fp64; the angle is formed and reduced in fp64. positions [M] int32. Both may be
- *             NULL when rot_dim == 0.
- *   rows      NULL: token m's K and V go to row m of k and v (kv_rows >= M). Else [M] int32:
+ *             fp64; the angle is formed and reduced in fp64. positions [tokens] int32. Both may
+ *             be NULL when rot_dim == 0.
+ *   rows      NULL: token m's K and V go to row m of k and v (kv_rows >= tokens). Else [tokens] int32:
  *             they go to row rows[m]; tokens with a row outside [0, kv_rows) write no K and V.
  *             Rows that no token names stay as they are. Two tokens of one call must not name
  *             the same row (which of them it then holds is unspecified).
- *   q, k, v   outputs of out_type, value d of head h of row r at r * strides[2i] +
- *             h * strides[2i+1] + d, i = 0, 1, 2 (strides: HOST array of 6, in elements). They
- *             must not overlap each other or the inputs.
+ *   q, k, v   outputs of out_type, value d of head h of row r at r * x_row + h * x_head + d
+ *             (strides in elements). They must not overlap each other or the inputs.
  * head_dim and rot_dim are multiples of 8, rot_dim <= head_dim <= BT_ROPE_MAX_HEAD_DIM,
  * heads a multiple of kv_heads. Arrays and strides are aligned to four elements.
  */
 #define BT_ROPE_MAX_HEAD_DIM 512
-bt_status bt_qk_norm_rope(const void *qkv, int32_t in_type, int64_t qkv_row, int64_t M, int64_t heads,
-                          int64_t kv_heads, int64_t head_dim, const float *q_weight, const float *k_weight,
-                          float eps, const int32_t *positions, const double *inv_freq, int64_t rot_dim,
-                          int32_t interleaved, const int32_t *rows, int64_t kv_rows, void *q, void *k, void *v,
-                          int32_t out_type, const int64_t *strides, void *stream);
+typedef struct {
+    int64_t tokens, heads, kv_heads, head_dim, rot_dim;
+    int64_t qkv_row, kv_rows; /* elements between rows of qkv; rows of k and v */
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    int32_t in_type, out_type, interleaved;
+    float eps;
+} bt_heads_shape;
+bt_status bt_qk_norm_rope(const bt_heads_shape *shape, const void *qkv, const float *q_weight, const float *k_weight,
+                          const int32_t *positions, const double *inv_freq, const int32_t *rows, void *q, void *k,
+                          void *v, void *stream);
 
 /*
  * bt_attention -- softmax attention over packed sequences with grouped heads: whole prompts,

@@ -1,6 +1,7 @@
 """Refusals of the attention-block operators, by the wrapper and by the C ABI: everything is checked
 on the host before a launch, so these run without a GPU."""
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -107,9 +108,8 @@ def test_lora_apply_refuses(host_ok):  # noqa: F811
 
 def _qk(qkv=FAKE, in_type=F32, ld=8 * 64, M=4, heads=4, kv=2, D=64, qw=0, kw=0, eps=1e-6, pos=FAKE, inv=FAKE, rot=64,
         inter=0, rows=0, kv_rows=4, q=FAKE, k=FAKE, v=FAKE, out_type=BF16, strides=(256, 64, 128, 64, 128, 64)):
-    arr = (ctypes.c_int64 * 6)(*strides)
-    return bt.lib().bt_qk_norm_rope(qkv, in_type, ld, M, heads, kv, D, qw, kw, eps, pos, inv, rot, inter, rows, kv_rows,
-                                    q, k, v, out_type, ctypes.addressof(arr), None)
+    shape = struct.pack("13q3if", M, heads, kv, D, rot, ld, kv_rows, *strides, in_type, out_type, inter, eps)
+    return bt.lib().bt_qk_norm_rope(shape, qkv, qw, kw, pos, inv, rows, q, k, v, None)
 
 
 def test_qk_norm_rope_abi_refusals():
@@ -129,6 +129,7 @@ def test_qk_norm_rope_abi_refusals():
     assert _qk(strides=(256, 64, 128, 64, -128, 64)) == BT_ERR_ALIGN
     assert _qk(pos=FAKE + 2) == BT_ERR_ALIGN and _qk(inv=FAKE + 4) == BT_ERR_ALIGN
     assert _qk(M=0, kv_rows=0) == BT_OK
+    assert bt.lib().bt_qk_norm_rope(None, *[FAKE] * 9, None) == BT_ERR_NULL
 
 
 def test_qk_norm_rope_refuses(host_ok):  # noqa: F811
