@@ -329,37 +329,44 @@ __device__ inline void load_lds16(__amdgpu_buffer_rsrc_t from, char *dst, uint32
 // workgroup in two groups held half a block apart by barriers: 597-620 us; a raised wave priority in
 // the matrix phase: 549 us.
 
-constexpr int kTileRows = 128, kTileKeys = 64;
+// HALVES == 2, for calls whose tiles of 128 rows would not fill the CUs: 64 rows, and the waves of a pair
+// take the two halves of every block's keys and are joined at the end. Twice the workgroups, each with half
+// the time per block (packed 2B prompts of 2048 tokens: BT_NOTE2).
 
-template <typename E, int DP, bool PART, bool WIDE>
+constexpr int kTileRows = 128, kSmallRows = 64, kTileKeys = 64;
+
+template <typename E, int DP, bool PART, bool WIDE, int HALVES>
 __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kbuf0, char *kbuf1, char *vbuf0,
                                           char *vbuf1, int &poison)
 {
     using V8 = typename Elem<E>::v8;
+    constexpr int ROWS = kTileRows / HALVES, KB = 2 / HALVES;  // rows of the tile, 32-key parts per wave
     constexpr int CPR = DP / 8;                          // 16-byte chunks of a row
     constexpr int NS = DP / 16, ND = DP / 32;            // MFMA steps over D, 32-wide tiles of D
     constexpr int LOADS = kTileKeys * CPR / 256;         // direct loads per wave and block
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 31, h = lane >> 5;
+    const int rg = HALVES == 2 ? wave & 1 : wave;        // the wave's 32 rows
+    const int part0 = HALVES == 2 ? wave >> 1 : 0;       // its first 32-key part of a block
     const int id = block / a.Hkv, head = block % a.Hkv;
     Item it;
-    if (!find_item(a, kTileRows, id, false, it))
+    if (!find_item(a, ROWS, id, false, it))
         return;
     const Seq s = it.s;
 
     // this lane's row
     const int rows = s.nq * a.G;
-    const int row = it.tile * kTileRows + 32 * wave + col;
+    const int row = it.tile * ROWS + 32 * rg + col;
     const int token = row / a.G, qh = head * a.G + row % a.G;
     const bool live = row < rows;
     const int limit = live ? row_limit(a, s, token) : 0;
     // the keys of the tile, and those that every live row of the wave sees
-    const int last = min(rows, (it.tile + 1) * kTileRows) - 1;
+    const int last = min(rows, (it.tile + 1) * ROWS) - 1;
     const int lo = (int)min((int64_t)it.piece * it.unit * kUnit, (int64_t)s.nk);
     const int hi = min((int)min((int64_t)(it.piece + 1) * it.unit * kUnit, (int64_t)s.nk), row_limit(a, s, last / a.G));
-    const int first = it.tile * kTileRows + 32 * wave;
+    const int first = it.tile * ROWS + 32 * rg;
     const int wfull = first < rows ? row_limit(a, s, first / a.G) : 0;
-    const int gfull = row_limit(a, s, it.tile * kTileRows / a.G);  // keys that every row of the tile sees
+    const int gfull = row_limit(a, s, it.tile * ROWS / a.G);  // keys that every row of the tile sees
     const int wmost = first < rows ? row_limit(a, s, min(rows - 1, first + 31) / a.G) : 0;
 
     // Q^T operands: lane (col, h) holds values 16 st + 8 h .. + 7 of its row
@@ -408,11 +415,12 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
 
     // S^T of a block; register i of half b: key + 32 b + 8 (i / 4) + 4 h + i % 4. Operand addresses are a
     // lane's base with bits flipped by the (constant) step.
-    f32x16 sc[2];
+    f32x16 sc[KB];
     const int kbase = col * (DP * 2) + ((h ^ swizzle<DP>(col)) << 4);
     auto scores = [&](const char *kb) __attribute__((always_inline)) {
+        kb += part0 * 32 * DP * 2;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < KB; ++b) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 sc[b][i] = 0.f;
@@ -425,19 +433,19 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
     };
     // The vector phase: probabilities of the block, as P^T operands (slot j of step t is register
     // 8 (t % 2) + j of half t / 2).
-    u32x4 pf[4], pr[4];
+    u32x4 pf[2 * KB], pr[2 * KB];
     auto soften = [&](int key) __attribute__((always_inline)) {
         if (key + kTileKeys > wfull) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (key + 32 * b + 8 * (i / 4) + 4 * h + i % 4 >= limit)
+                    if (key + 32 * (part0 + b) + 8 * (i / 4) + 4 * h + i % 4 >= limit)
                         sc[b][i] = -INFINITY;
         }
         float mx = sc[0][0];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 mx = fmaxf(mx, sc[b][i]);
@@ -455,7 +463,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
         }
         const float ref = m == -INFINITY ? 0.f : m * c2;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2 * KB; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float p[2];
@@ -472,7 +480,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
             }
         // done here, not where they are used
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 2 * KB; ++t) {
             asm volatile("" : "+v"(pf[t]));
             if constexpr (WIDE)
                 asm volatile("" : "+v"(pr[t]));
@@ -483,10 +491,11 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
     const int tr_row = 4 * h + (lane & 15) / 4, tr_col = (lane >> 4 & 1) * 32 + (lane & 3) * 8;  // bytes
     const int vbase = tr_row * (DP * 2) + (((tr_col >> 4) ^ swizzle<DP>(tr_row)) << 4) + (tr_col & 15);
     auto weigh = [&](const char *vb) __attribute__((always_inline)) {
+        vb += part0 * 32 * DP * 2;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < 2 * KB; ++t) {
                 u32x4 x;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -559,7 +568,33 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
                 one(key + kTileKeys, vbuf1, kbuf0, vbuf0, kbuf1);
         }
     }
+    l += other_half(l);
     __syncthreads();
+    if constexpr (HALVES == 2) {
+        // the second half's sums to the first half's waves
+        float *sums = reinterpret_cast<float *>(rg ? kbuf1 : kbuf0), *stat = reinterpret_cast<float *>(vbuf0) + 64 * rg;
+        if (part0) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sums[(d * 16 + i) * 64 + lane] = o[d][i];
+            stat[col] = m;
+            stat[32 + col] = l;
+        }
+        __syncthreads();
+        if (part0)
+            return;
+        const float m1 = stat[col], mn = fmaxf(m, m1);
+        const float f0 = m == mn ? 1.f : exp2_fast((m - mn) * c2), f1 = m1 == mn ? 1.f : exp2_fast((m1 - mn) * c2);
+        l = l * f0 + stat[32 + col] * f1;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[d][i] = o[d][i] * f0 + sums[(d * 16 + i) * 64 + lane] * f1;
+        m = mn;
+    }
     if (__builtin_expect(poison, 0)) {
         // The cleaned blocks again, from memory: what they lost goes to the rows that see it.
         const int from = lo + max(0, gfull - lo) / kTileKeys * kTileKeys;
@@ -579,7 +614,6 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
         }
     }
 
-    l += other_half(l);
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
     const float lse = l == 0.f ? -INFINITY : m * c2 * kLn2 + logf(l);
     if (!live)
@@ -587,8 +621,8 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
     const bool part = PART && (a.pieced || it.pieces > 1);
     if (part) {
         const int64_t slot = block;
-        const int r = 32 * wave + col;
-        float *dst = a.ws_o + (slot * kTileRows + r) * a.D;
+        const int r = 32 * rg + col;
+        float *dst = a.ws_o + (slot * ROWS + r) * a.D;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -601,7 +635,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
                 }
             }
         if (h == 0)
-            a.ws_l[slot * kTileRows + r] = lse;
+            a.ws_l[slot * ROWS + r] = lse;
         return;
     }
     const int64_t at = (int64_t)(s.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
@@ -900,12 +934,12 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
 // prefix's items are the first workgroups of the same launch (PRE), so that neither part waits for the
 // other.
 
-enum Kind { kNone, kFew, kTile };
+enum Kind { kNone, kFew, kTile, kSmall };
 
 template <typename E, int DP, bool WIDE, Kind MAIN, Kind PRE, bool PART>
 __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn(AttnArgs a, AttnArgs pre, int pre_blocks)
 {
-    constexpr bool tiles = MAIN == kTile || PRE == kTile;
+    constexpr bool tiles = MAIN >= kTile || PRE >= kTile;
     constexpr int bytes = kTileKeys * DP * 2;
     static_assert(bytes == 2 * kFewKeys * DP * 2, "two waves' pieces of the few-rows kernel");
     __shared__ __attribute__((aligned(1024))) char buf0[bytes], buf1[bytes];
@@ -919,17 +953,17 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn(AttnArgs a, Attn
         if constexpr (MAIN == kFew)
             attn_few<E, DP, WIDE>(x, p ? block : block - pre_blocks, buf0, buf1, stat);
         else
-            attn_tile<E, DP, true, WIDE>(x, p ? block : block - pre_blocks, buf0, buf1, buf2, buf3, poison);
+            attn_tile<E, DP, true, WIDE, 1>(x, p ? block : block - pre_blocks, buf0, buf1, buf2, buf3, poison);
     } else {
         if constexpr (PRE == kTile)
             if (block < pre_blocks) {
-                attn_tile<E, DP, true, WIDE>(pre, block, buf0, buf1, buf2, buf3, poison);
+                attn_tile<E, DP, true, WIDE, 1>(pre, block, buf0, buf1, buf2, buf3, poison);
                 return;
             }
         if constexpr (MAIN == kFew)
             attn_few<E, DP, WIDE>(a, block - pre_blocks, buf0, buf1, stat);
         else
-            attn_tile<E, DP, PART, WIDE>(a, block, buf0, buf1, buf2, buf3, poison);
+            attn_tile<E, DP, PART, WIDE, (MAIN == kSmall ? 2 : 1)>(a, block, buf0, buf1, buf2, buf3, poison);
     }
 }
 
@@ -937,17 +971,17 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn(AttnArgs a, Attn
 //
 // k_attn_combine: a row's slices, and with a shared prefix the prefix's slices of the same row,
 // joined by their lse: out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max). 32 lanes read a
-// row; the 32 such groups of a workgroup are spread over its (at most 32) rows, so that the slices of
-// few rows are read side by side (four in flight in each group) and joined through LDS. Latency is all
-// there is to it.
+// row; the groups of a workgroup are spread over its rows, so that the slices of few rows are read
+// side by side (four in flight in each group) and joined through LDS. Latency is all there is to it:
+// 16 groups cost 0.6-0.9 us more in small calls, 32 groups 1-3 us, fewer workgroups fitting a CU.
 
-constexpr int kJoinRows = 32;  // largest number of rows of a workgroup
+constexpr int kJoinGroups = 8;  // and the largest number of rows of a workgroup
 
 template <typename TO>
-__global__ __launch_bounds__(1024) void k_attn_combine(AttnArgs a, AttnArgs pre, int bm, int pre_bm)
+__global__ __launch_bounds__(32 * kJoinGroups) void k_attn_combine(AttnArgs a, AttnArgs pre, int bm, int pre_bm)
 {
-    __shared__ f32x4 sums[32][2][32];
-    __shared__ float stat[32][2];
+    __shared__ f32x4 sums[kJoinGroups][2][32];
+    __shared__ float stat[kJoinGroups][2];
     const int l32 = threadIdx.x & 31, group = threadIdx.x >> 5;
     const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
     Item it;
@@ -960,12 +994,12 @@ __global__ __launch_bounds__(1024) void k_attn_combine(AttnArgs a, AttnArgs pre,
     const int slot = first_item(a, it, bm);
     if (slot + it.pieces > a.items)
         return;  // more tiles than sequences that do not overlap can have: not computed
-    const int r0 = blockIdx.y * kJoinRows;
-    const int here = min(min(bm - r0, kJoinRows), rows - it.tile * bm - r0);  // rows of this workgroup
+    const int r0 = blockIdx.y * kJoinGroups;
+    const int here = min(min(bm - r0, kJoinGroups), rows - it.tile * bm - r0);  // rows of this workgroup
     if (here <= 0)
         return;
     const int ways = 32 - __builtin_clz(2 * here - 1) - 1;  // log2 of here rounded up to a power of two
-    const int gp = 32 >> ways;                              // groups of a row
+    const int gp = kJoinGroups >> ways;                              // groups of a row
     const int r = r0 + (group & ((1 << ways) - 1)), part = group >> ways;
     const int row = it.tile * bm + r;
     const bool live = r < r0 + here;
@@ -1078,9 +1112,11 @@ hipError_t run_kind(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, h
     if (!pb) {
         if (few)
             k_attn<E, DP, WIDE, kFew, kNone, true><<<grid, 256, 0, s>>>(a, pre, 0);
-        else if (p.main.target)
-            k_attn<E, DP, WIDE, kTile, kNone, true><<<grid, 256, 0, s>>>(a, pre, 0);
-        else
+        else if (p.main.bm == kSmallRows && p.main.target)
+            k_attn<E, DP, WIDE, kSmall, kNone, true><<<grid, 256, 0, s>>>(a, pre, 0);
+        else if (p.main.bm == kSmallRows)
+            k_attn<E, DP, WIDE, kSmall, kNone, false><<<grid, 256, 0, s>>>(a, pre, 0);
+        else  // tiles enough to go uncut
             k_attn<E, DP, WIDE, kTile, kNone, false><<<grid, 256, 0, s>>>(a, pre, 0);
     } else if (few && pre_few) {
         k_attn<E, DP, WIDE, kFew, kFew, true><<<grid, 256, 0, s>>>(a, pre, pb);
@@ -1113,8 +1149,8 @@ hipError_t run_type(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, i
 template <typename TO>
 hipError_t run_combine(const AttnArgs &a, const AttnArgs &pre, const AttnPlan &p, hipStream_t s)
 {
-    const dim3 grid((unsigned)(p.main.tiles * a.Hkv), (unsigned)((p.main.bm + kJoinRows - 1) / kJoinRows));
-    k_attn_combine<TO><<<grid, 1024, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
+    const dim3 grid((unsigned)(p.main.tiles * a.Hkv), (unsigned)((p.main.bm + kJoinGroups - 1) / kJoinGroups));
+    k_attn_combine<TO><<<grid, 32 * kJoinGroups, 0, s>>>(a, pre, p.main.bm, p.pre.bm);
     return hipGetLastError();
 }
 
@@ -1124,6 +1160,8 @@ AttnPart plan_part(int64_t rows, int64_t seqs, int64_t keys, int64_t Hkv, bool a
     AttnPart p;
     // mean rows of a sequence: up to 16, one small tile each
     p.bm = rows <= kFewRows * seqs ? kFewRows : kTileRows;
+    if (p.bm == kTileRows && !always && (rows / kTileRows + seqs) * Hkv < 512)
+        p.bm = kSmallRows;
     p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
     // Keys are cut so that about `want` workgroups share the work: eight per CU where the bytes of the
     // keys are all that counts, and fewer for large tiles, whose outputs cost more to join.
