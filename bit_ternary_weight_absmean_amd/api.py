@@ -457,7 +457,7 @@ def _workspace_bytes(name: str, *sizes: int) -> int:
 LORA_MAX_RANK = 256  # BT_LORA_MAX_RANK
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class LoraAdapters:
     """Low-rank adapters of one projection: ``A`` [L, groups * R, K] and ``B`` [L, N, R] (bf16, fp16 or
     fp32), ``scale`` [L] fp32, optionally the ``ranks`` [L] int32 in use and, for a fused projection, the

@@ -681,8 +681,8 @@ bt_status bt_lora_apply(const void *A, const void *B, int32_t w_type, const floa
         return fail(BT_ERR_SHAPE, "M = %lld or N = %lld outside [0, 2^23]", (long long)M, (long long)N);
     if (bt_status s = check_k(K))
         return s;
-    if (M * N > BT_MAX_MN)
-        return fail(BT_ERR_SHAPE, "M * N = %lld above 2^36", (long long)(M * N));
+    if (M * N > BT_MAX_MN / 2)
+        return fail(BT_ERR_SHAPE, "M * N = %lld above 2^35", (long long)(M * N));
     if (L < 0 || L > INT32_MAX)
         return fail(BT_ERR_SHAPE, "L = %lld outside [0, 2^31)", (long long)L);
     if (R < 1 || R > BT_LORA_MAX_RANK)

@@ -407,7 +407,7 @@ bt_status bt_kernel_plan(int32_t call, int64_t M, int64_t N, int64_t K, int32_t 
  *   A         [L, ngroups * R, K], B [L, N, R], both of type w_type, aligned to their element
  *             (16-byte aligned with K and R multiples of 8 is faster).
  *   scale     [L] fp32. ranks: [L] int32 or NULL (all R); ranks are clamped to [0, R], and
- *             what A and B hold past an adapter's rank is not read.
+ *             what A and B hold past an adapter's rank does not matter.
  *   group_rows  HOST array of ngroups row counts as for bt_pack_weights_rows, or NULL for one
  *             group (ngroups ignored).
  *   adapter   [M] int32 on the device. A token whose entry is outside [0, L) has no adapter:
@@ -417,7 +417,7 @@ bt_status bt_kernel_plan(int32_t call, int64_t M, int64_t N, int64_t K, int32_t 
  *   workspace bt_lora_workspace_bytes(M, K, R, ngroups) bytes of device scratch, 256-byte
  *             aligned; contents on entry are ignored. Calls sharing one must not overlap.
  * Operands are multiplied without rounding them and summed in fp32 in an order that depends on
- * the shape alone (no atomics). 1 <= R <= BT_LORA_MAX_RANK, 0 <= L < 2^31. An adapter's weights
+ * the shape alone (no atomics). 1 <= R <= BT_LORA_MAX_RANK, 0 <= L < 2^31, M * N <= 2^35. An adapter's weights
  * never reach the tokens of another one, whatever they hold.
  */
 #define BT_LORA_MAX_RANK 256

@@ -64,6 +64,8 @@ CASES = [
     (65, 12, 4, 96, 96, False, False, "fp32", "bf16", 77),
     (33, 16, 2, 64, 0, False, True, "fp16", "fp16", 1),
     (40, 5, 5, 24, 24, False, True, "fp32", "fp32", 2 ** 31 - 1),
+    (3, 3, 3, 200, 24, False, True, "fp32", "fp16", 100000),  # nine heads, two to a wave
+    (5, 1, 1, 48, 48, True, True, "bf16", "fp32", 4096),  # three heads, eight to a wave
     (700, 20, 5, 128, 128, False, True, "fp32", "bf16", 8192),
     (2050, 7, 7, 72, 56, True, True, "fp32", "fp32", 8192),
 ]

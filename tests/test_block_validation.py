@@ -28,6 +28,7 @@ def test_lora_abi_refusals():
     assert _lora(M=-1) == BT_ERR_SHAPE
     assert _lora(N=(1 << 23) + 1) == BT_ERR_SHAPE
     assert _lora(M=1 << 23, N=1 << 14) == BT_ERR_SHAPE
+    assert _lora(M=1 << 23, N=(1 << 12) + 1) == BT_ERR_SHAPE  # one launch's work-items
     assert _lora(K=131073) == BT_ERR_SHAPE
     assert _lora(R=0) == BT_ERR_SHAPE
     assert _lora(R=257) == BT_ERR_SHAPE
@@ -160,3 +161,85 @@ def test_qk_norm_rope_refuses(host_ok):  # noqa: F811
         bt.qk_norm_rope(qkv, pos, inv, 2, 1, out=(torch.zeros((3, 64, 2)).transpose(1, 2), k, k.clone()))
     with pytest.raises(TypeError, match="qkv must be one of"):
         bt.qk_norm_rope(qkv.double(), pos, inv, 2, 1)
+
+
+# bt_attention_shape of a small valid call, and the call
+ATT = dict(tokens=6, keys=100, seqs=2, prefix=0, heads=4, kv_heads=2, head_dim=64, type=BF16, out_type=BF16, causal=1,
+           scale=0.125, q_row=256, q_head=64, k_row=128, k_head=64, v_row=128, v_head=64, prefix_k_row=128,
+           prefix_k_head=64, prefix_v_row=128, prefix_v_head=64, out_row=256, out_head=64)
+
+
+def _attention(q=FAKE, k=FAKE, v=FAKE, q_start=FAKE, k_start=FAKE, k_len=FAKE, pk=0, pv=0, out=FAKE, lse=0, ws=FAKE,
+               **change):
+    shape = struct.pack("7q3if12q", *{**ATT, **change}.values())
+    return bt.lib().bt_attention(shape, q, k, v, q_start, k_start, k_len, pk, pv, out, lse, ws, None)
+
+
+def test_attention_abi_refusals():
+    assert bt.lib().bt_attention(None, *[FAKE] * 11, None) == BT_ERR_NULL
+    for change in (dict(tokens=-1), dict(tokens=(1 << 23) + 1), dict(keys=-1), dict(keys=2 ** 31 - 1), dict(seqs=-1),
+                   dict(prefix=-1), dict(heads=5), dict(heads=0), dict(kv_heads=0), dict(heads=65537, kv_heads=65537),
+                   dict(head_dim=60), dict(head_dim=264), dict(head_dim=0), dict(scale=0.0), dict(scale=-1.0),
+                   dict(scale=float("nan")), dict(scale=float("inf")), dict(tokens=1 << 23, heads=256, kv_heads=256),
+                   dict(tokens=1 << 22, seqs=1 << 22, heads=64, kv_heads=64), dict(k_row=(1 << 23) + 8)):
+        assert _attention(**change) == BT_ERR_SHAPE, change
+    for change in (dict(type=F32), dict(type=3), dict(out_type=2), dict(out_type=7)):
+        assert _attention(**change) == BT_ERR_UNSUPPORTED, change
+    for name in ("q", "k", "v", "q_start", "k_start", "k_len", "out", "ws"):
+        assert _attention(**{name: 0}) == BT_ERR_NULL, name
+    assert _attention(prefix=5, pk=FAKE) == BT_ERR_NULL and _attention(prefix=5, pv=FAKE) == BT_ERR_NULL
+    for name in ("q", "k", "v"):
+        assert _attention(**{name: FAKE + 8}) == BT_ERR_ALIGN, name
+    for name in ("q_start", "k_start", "k_len", "lse"):
+        assert _attention(**{name: FAKE + 2}) == BT_ERR_ALIGN, name
+    assert _attention(out=FAKE + 4) == BT_ERR_ALIGN and _attention(ws=FAKE + 128) == BT_ERR_ALIGN
+    for name in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head"):
+        assert _attention(**{name: 132}) == BT_ERR_ALIGN, name
+        assert _attention(**{name: -8}) == BT_ERR_ALIGN, name
+    assert _attention(out_row=258) == BT_ERR_ALIGN and _attention(out_head=-4) == BT_ERR_ALIGN
+    assert _attention(prefix=5, pk=FAKE, pv=FAKE + 8) == BT_ERR_ALIGN
+    assert _attention(prefix=5, pk=FAKE, pv=FAKE, prefix_k_row=12) == BT_ERR_ALIGN
+    assert _attention(tokens=0) == BT_OK and _attention(seqs=0) == BT_OK
+
+
+def test_attention_workspace_bytes():
+    f = bt.lib().bt_attention_workspace_bytes
+    assert f(0, 5, 1, 4, 4, 64, 0) == 0 and f(5, 5, 0, 4, 4, 64, 0) == 0 and f(5, 5, 1, 5, 4, 64, 0) == 0
+    assert f(8192, 8192, 1, 32, 32, 128, 0) == 0  # tiles enough: keys are not cut
+    for sizes in ((1, 1024, 1, 20, 5, 128, 0), (64, 524288, 64, 20, 5, 128, 0), (64, 0, 64, 64, 8, 128, 16384)):
+        n = f(*sizes)
+        assert n > 0 and n % 256 == 0 and n < 1 << 28, sizes
+
+
+def test_attention_refuses(host_ok):  # noqa: F811
+    b16 = torch.bfloat16
+    q, k, qs, ks = torch.zeros((6, 4, 64), dtype=b16), torch.zeros((9, 2, 64), dtype=b16), torch.zeros(
+        3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="q must be one of"):
+        bt.attention(q.float(), k, k, qs, ks, ks)
+    with pytest.raises(ValueError, match="multiple of 3 key heads"):
+        bt.attention(q, torch.zeros((9, 3, 64), dtype=b16), k, qs, ks, ks)
+    with pytest.raises(TypeError, match="v must be"):
+        bt.attention(q, k, k.half(), qs, ks, ks)
+    with pytest.raises(ValueError, match="v must have shape"):
+        bt.attention(q, k, k[:8], qs, ks, ks)
+    with pytest.raises(ValueError, match="q_start must have shape"):
+        bt.attention(q, k, k, ks, ks, ks)
+    with pytest.raises(TypeError, match="k_start must be"):
+        bt.attention(q, k, k, qs, ks.long(), ks)
+    with pytest.raises(ValueError, match="k_len must be"):
+        bt.attention(q, k, k, qs, ks, 5)
+    with pytest.raises(ValueError, match="come together"):
+        bt.attention(q, k, k, qs, ks, ks, prefix_k=k)
+    with pytest.raises(ValueError, match="prefix_v must have shape"):
+        bt.attention(q, k, k, qs, ks, ks, prefix_k=k, prefix_v=k[:4])
+    with pytest.raises(TypeError, match="out must be"):
+        bt.attention(q, k, k, qs, ks, ks, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="overlap itself"):
+        bt.attention(q, k, k, qs, ks, ks, out=q[:1].expand(6, 4, 64))
+    with pytest.raises(ValueError, match="last dimension"):
+        bt.attention(q, k.transpose(1, 2).contiguous().transpose(1, 2), k, qs, ks, ks)
+    with pytest.raises(ValueError, match="lse must have shape"):
+        bt.attention(q, k, k, qs, ks, ks, lse=torch.zeros((4, 6)))
+    with pytest.raises(ValueError, match="workspace holds"):
+        bt.attention(q, k, k, qs, ks, ks, workspace=torch.zeros(8, dtype=torch.uint8))
