@@ -11,10 +11,11 @@
 // once for all of the tile's tokens that use it (once per two of them in the few-tokens form). The
 // other tokens of the tile take no part in it: an adapter's weights, whatever they hold, never reach
 // a token that does not use it.
-//  * Few tokens (k_lora_shrink_few, k_lora_expand_few; up to kFewTokens): a workgroup per (tile,
+//  * Few tokens (k_lora_shrink_few, k_lora_expand_few; see lora_plan): a workgroup per (tile,
 //    first token of an adapter), so that a decode batch's adapters are read side by side; bound by
-//    the bytes of A and B. fp32 FMA: with a token or two per adapter the matrix cores would mostly
-//    multiply columns that are not wanted, and cutting operands for them costs more than the FMAs.
+//    the bytes of A and B. fp32 FMA where at most four of the tile's tokens share the adapter (the matrix
+//    cores would mostly multiply columns that are not wanted, and cutting operands for them costs more
+//    than the FMAs), else the many-tokens form's products for that adapter.
 //  * Many tokens (k_lora_shrink, k_lora_expand): a workgroup walks its tile's adapters (one or two
 //    where prompts are runs) on the matrix cores; bound by the bytes of X, Y0 and Y.
 //
@@ -39,8 +40,10 @@ constexpr int kWaves = 4;            // of a workgroup of k_lora_shrink_few
 constexpr int kDeepWaves = 8;        // of a workgroup of k_lora_shrink
 constexpr int kStepK = 32 * kDeepWaves;  // k of one workgroup step of k_lora_shrink
 constexpr int kMaxRank = 256;
-constexpr int kFewTokens = 128;      // largest M of the few-tokens kernels
+constexpr int kFewTokens = 128;      // M up to which the few-tokens kernels are taken for any adapters,
+constexpr int kFewMixed = 1024, kFewPer = 8;  // and up to which where there are at most so many per adapter
 constexpr int kChunkK = 512;         // k of one wave step of k_lora_shrink_few: 8 per lane
+constexpr int kFewShare = 4;         // tokens of a tile sharing an adapter above which it goes to the matrix cores
 constexpr int kGroupTok = 2;         // tokens that share one reading of an adapter there
 
 struct LoraArgs {
@@ -51,7 +54,7 @@ struct LoraArgs {
     float *Y, *ws;
     int64_t M, N, K;
     int L, R, Rp;  // Rp: R rounded up to 16
-    int slices, kslice, leads;  // leads: workgroups per tile of the few-tokens kernels
+    int slices, kslice, tiles;
     int quads;  // N is a multiple of 4: outputs move four at a time
     RowGroups groups;
 };
@@ -290,28 +293,25 @@ __global__ __launch_bounds__(64 * kDeepWaves) void k_lora_shrink(LoraArgs a)
 constexpr int kStream = 2;  // buffer loads and stores: non-temporal
 constexpr int kExpandN = 64, kExpandT = kExpandN / 16;
 
+struct Slab {
+    float row[kTile][kExpandN + 4];
+};
+
+// The wave's 64 outputs from n0 on of the tokens in `stored`; `mine`: the adapter of token lane % 16.
 template <typename W, bool VEC>
-__global__ __launch_bounds__(256, 3) void k_lora_expand(LoraArgs a)
+__device__ __forceinline__ void expand_tile(const LoraArgs &a, int64_t m0, int64_t n0, int mine, uint32_t stored,
+                                            Slab &slab)
 {
     static_assert(kExpandN == 64 && kExpandT == 4, "sixteen lanes move a row of four values each");
-    __shared__ __attribute__((aligned(16))) float slab[4][kTile][kExpandN + 4];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int t = lane & 15, g = lane >> 4;
-    // outputs vary fastest, over a workgroup's waves and over workgroups
-    const int64_t blocks = (a.N + 4 * kExpandN - 1) / (4 * kExpandN);
-    const int64_t m0 = (int64_t)(blockIdx.x / blocks) * kTile;
-    const int64_t n0 = ((int64_t)(blockIdx.x % blocks) * 4 + wave) * kExpandN;
-    if (n0 >= a.N)
-        return;
+    const int lane = threadIdx.x & 63, t = lane & 15, g = lane >> 4;
     const int cols = (int)min((int64_t)kExpandN, a.N - n0);
-    const int mine = lane_adapter(a, m0, t);
     // this lane's outputs: tokens 4 i + g, columns 4 t .. + 3 of the wave's
     const int64_t corner = m0 * a.N + n0;
     const int64_t span = ((min((int64_t)kTile, a.M - m0) - 1) * a.N + cols) * 4;
     uint32_t yoff[kExpandT];
 #pragma unroll
     for (int i = 0; i < kExpandT; ++i)
-        yoff[i] = m0 + 4 * i + g < a.M && 4 * t < cols ? (uint32_t)((4 * i + g) * a.N + 4 * t) * 4u : kOutside;
+        yoff[i] = (stored >> (4 * i + g) & 1) && 4 * t < cols ? (uint32_t)((4 * i + g) * a.N + 4 * t) * 4u : kOutside;
     const __amdgpu_buffer_rsrc_t ys = buffer_of(a.Y0 ? a.Y0 + corner : nullptr, a.Y0 ? span : 0);
     f32x4 y[kExpandT], acc[kExpandT];
     if (a.quads) {
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(256, 3) void k_lora_expand(LoraArgs a)
 #pragma unroll
     for (int i = 0; i < kExpandT; ++i)
         acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};  // token t, columns 16 i + 4 g .. + 3
-    uint32_t todo = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
+    uint32_t todo = (uint32_t)__ballot(mine >= 0) & stored;
     const int64_t hrow = min(m0 + t, a.M - 1) * a.groups.n, hstep = a.M * a.groups.n * a.Rp;
     while (todo) {
         const int lead = __builtin_ctz(todo);
@@ -389,11 +389,11 @@ __global__ __launch_bounds__(256, 3) void k_lora_expand(LoraArgs a)
     // complete in order)
 #pragma unroll
     for (int i = 0; i < kExpandT; ++i)
-        *reinterpret_cast<f32x4 *>(&slab[wave][t][16 * i + 4 * g]) = acc[i];
+        *reinterpret_cast<f32x4 *>(&slab.row[t][16 * i + 4 * g]) = acc[i];
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < kExpandT; ++i)
-        y[i] += *reinterpret_cast<const f32x4 *>(&slab[wave][4 * i + g][4 * t]);
+        y[i] += *reinterpret_cast<const f32x4 *>(&slab.row[4 * i + g][4 * t]);
     const __amdgpu_buffer_rsrc_t out = buffer_of(a.Y + corner, span);
     if (a.quads) {
 #pragma unroll
@@ -409,11 +409,28 @@ __global__ __launch_bounds__(256, 3) void k_lora_expand(LoraArgs a)
     }
 }
 
-// The leader token of this workgroup of a few-tokens kernel and the tokens that share its adapter;
-// false: the token is not the first one of its adapter, or does not exist.
-__device__ inline bool lead_tokens(const LoraArgs &a, int64_t m0, int lead, int &ad, uint32_t &same)
+template <typename W, bool VEC>
+__global__ __launch_bounds__(256, 3) void k_lora_expand(LoraArgs a)
 {
+    __shared__ __attribute__((aligned(16))) Slab slab[4];
+    const int wave = uniform(threadIdx.x >> 6);
+    // outputs vary fastest, over a workgroup's waves and over workgroups
+    const int64_t blocks = (a.N + 4 * kExpandN - 1) / (4 * kExpandN);
+    const int64_t m0 = (int64_t)(blockIdx.x / blocks) * kTile;
+    const int64_t n0 = ((int64_t)(blockIdx.x % blocks) * 4 + wave) * kExpandN;
+    if (n0 >= a.N)
+        return;
     const int mine = lane_adapter(a, m0, threadIdx.x & 15);
+    expand_tile<W, VEC>(a, m0, n0, mine, (uint32_t)__ballot(mine > -2) & 0xFFFFu, slab[wave]);
+}
+
+// The leader token of this workgroup of a few-tokens kernel and the tokens that share its adapter;
+// false: the token is not the first one of its adapter, or does not exist. (Workgroups go to the eight
+// dies in turn. Tiles vary fastest over them: with leaders fastest, where a tile has one adapter, all
+// the workgroups that have work would be on one die.)
+__device__ inline bool lead_tokens(const LoraArgs &a, int64_t m0, int lead, int &mine, int &ad, uint32_t &same)
+{
+    mine = lane_adapter(a, m0, threadIdx.x & 15);
     ad = __builtin_amdgcn_readlane(mine, lead);
     same = (uint32_t)__ballot(mine == ad) & 0xFFFFu;
     return ad > -2 && __builtin_ctz(same) == lead;
@@ -444,11 +461,12 @@ template <typename W, bool VEC>
 __global__ __launch_bounds__(256, 3) void k_lora_shrink_few(LoraArgs a)
 {
     __shared__ float part[kWaves][kGroupTok][16];
+    __shared__ f32x4 tile[kWaves][64];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int64_t m0 = (int64_t)(blockIdx.x / a.leads) * kTile;
-    int ad;
+    const int64_t m0 = (int64_t)(blockIdx.x % a.tiles) * kTile;
+    int mine, ad;
     uint32_t same;
-    if (!lead_tokens(a, m0, blockIdx.x % a.leads, ad, same) || ad < 0)
+    if (!lead_tokens(a, m0, blockIdx.x / a.tiles, mine, ad, same) || ad < 0)
         return;
     const int tpg = a.Rp / 16, grp = blockIdx.z / tpg, r0 = (blockIdx.z % tpg) * 16;
     const int rank = adapter_rank(a, ad);
@@ -460,6 +478,29 @@ __global__ __launch_bounds__(256, 3) void k_lora_shrink_few(LoraArgs a)
     const __amdgpu_buffer_rsrc_t xs = buffer_of(a.X + m0 * a.K, min((int64_t)kTile, a.M - m0) * a.K * 4);
     const float scale = a.scale[ad];
     const int k0 = (int)blockIdx.y * a.kslice, k1 = (int)min((int64_t)k0 + a.kslice, a.K);
+    if (__builtin_popcount(same) > kFewShare) {
+        // the whole tile on the matrix cores; the four waves take every fourth step of 32 k
+        const int t = lane & 15, g = lane >> 4;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int kk = k0 + 32 * wave; kk < k1; kk += 32 * kWaves) {
+            const int k = kk + 8 * g, n = min(8, k1 - k);
+            const Raw8<float> xr = fetch8<float, VEC>(xs, (uint32_t)(t * (int)a.K + k) * 4u, n);
+            const Raw8<W> wr = fetch8<W, VEC>(ws, (uint32_t)t * (uint32_t)row_w + (uint32_t)sizeof(W) * k, n);
+            acc = mma(pieces(wr), pieces(xr), acc);
+        }
+        tile[wave][lane] = acc;
+        __syncthreads();
+        if (wave == 0 && (same >> t & 1)) {
+            f32x4 s = tile[0][lane];
+#pragma unroll
+            for (int q = 1; q < kWaves; ++q)
+                s += tile[q][lane];
+            *reinterpret_cast<f32x4 *>(a.ws + (((int64_t)blockIdx.y * a.M + m0 + t) * a.groups.n + grp) * a.Rp + r0 +
+                                       4 * g) = s * scale;
+        }
+        return;
+    }
     while (same) {
         int tok[kGroupTok];
         const int nt = take_tokens(same, tok);
@@ -550,12 +591,19 @@ template <typename W, bool VEC>
 __global__ __launch_bounds__(256) void k_lora_expand_few(LoraArgs a)
 {
     __shared__ __attribute__((aligned(16))) float hs[kGroupTok][kMaxRank];
-    const int64_t m0 = (int64_t)(blockIdx.x / a.leads) * kTile;
+    __shared__ __attribute__((aligned(16))) Slab slab[4];
+    const int64_t m0 = (int64_t)(blockIdx.x % a.tiles) * kTile;
     const int64_t nb = (int64_t)blockIdx.y * kFewN, n = nb + threadIdx.x;
-    int ad;
+    int mine, ad;
     uint32_t same;
-    if (!lead_tokens(a, m0, blockIdx.x % a.leads, ad, same))
+    if (!lead_tokens(a, m0, blockIdx.x / a.tiles, mine, ad, same))
         return;
+    if (ad >= 0 && __builtin_popcount(same) > kFewShare) {
+        const int wave = uniform(threadIdx.x >> 6);
+        if (nb + kExpandN * wave < a.N)
+            expand_tile<W, VEC>(a, m0, nb + kExpandN * wave, mine, same, slab[wave]);
+        return;
+    }
     if (ad < 0) {
         if (a.Y0 != a.Y)
             for (; same; same &= same - 1)
@@ -649,11 +697,16 @@ struct LoraPlan {
     int64_t kslice, tiles, ztiles;
 };
 
-LoraPlan lora_plan(int64_t M, int64_t K, int64_t R, int64_t groups)
+// The few-tokens form costs a workgroup per token, most of them idle where tokens come in runs; the other
+// form walks a tile's adapters one after the other. 256 tokens in random order over 64 adapters of 7B O,
+// few / many: 32 / 76 us; 1024: 103 / 150 us; in runs over 4 adapters of 2B QKV, 256 tokens: 21 / 12 us;
+// of 7B QKV (rank 64), 512: 66 / 40 us. Which one it will be is device data; adapters that tokens hardly
+// share are taken for the first.
+LoraPlan lora_plan(int64_t M, int64_t K, int64_t R, int64_t groups, bool few)
 {
     LoraPlan p;
     const int64_t rank_tiles = round_up(R, 16) / 16 * groups;
-    p.few = M <= kFewTokens;
+    p.few = few;
     p.rt = p.few ? 1 : rank_tiles >= 3 ? 4 : (int)rank_tiles;
     p.ztiles = (rank_tiles + p.rt - 1) / p.rt;
     p.tiles = (M + kTile - 1) / kTile;
@@ -718,14 +771,18 @@ hipError_t launch_weights(const LoraArgs &a, const LoraPlan &p, hipStream_t s)
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t groups)
 {
-    return (size_t)lora_plan(M, K, R, groups).slices * M * groups * round_up(R, 16) * 4;
+    // for either form: which one is taken depends on the number of adapters
+    const int few = lora_plan(M, K, R, groups, true).slices, many = lora_plan(M, K, R, groups, false).slices;
+    const int slices = M <= kFewTokens ? few : M > kFewMixed ? many : few > many ? few : many;
+    return (size_t)slices * M * groups * round_up(R, 16) * 4;
 }
 
 hipError_t launch_lora(const void *A, const void *B, int w_type, const float *scale, const int32_t *ranks, int64_t L,
                        int64_t R, const RowGroups &groups, const int32_t *adapter, const float *X, const float *Y0,
                        int64_t M, int64_t N, int64_t K, float *Y, void *workspace, hipStream_t s)
 {
-    const LoraPlan p = lora_plan(M, K, R, groups.n);
+    const bool few = M <= kFewTokens || (M <= kFewMixed && M <= kFewPer * L);
+    const LoraPlan p = lora_plan(M, K, R, groups.n, few);
     LoraArgs a;
     a.A = A;
     a.B = B;
@@ -742,7 +799,7 @@ hipError_t launch_lora(const void *A, const void *B, int w_type, const float *sc
     a.L = (int)L;
     a.R = (int)R;
     a.Rp = (int)round_up(R, 16);
-    a.leads = p.leads;
+    a.tiles = (int)p.tiles;
     a.slices = p.slices;
     a.kslice = (int)p.kslice;
     a.quads = N % 4 == 0;

@@ -416,8 +416,8 @@ bt_status bt_kernel_plan(int32_t call, int64_t M, int64_t N, int64_t K, int32_t 
  *             and must not overlap the inputs otherwise.
  *   workspace bt_lora_workspace_bytes(M, K, R, ngroups) bytes of device scratch, 256-byte
  *             aligned; contents on entry are ignored. Calls sharing one must not overlap.
- * Operands are multiplied without rounding them and summed in fp32 in an order that depends on
- * the shape alone (no atomics). 1 <= R <= BT_LORA_MAX_RANK, 0 <= L < 2^31, M * N <= 2^35. An adapter's weights
+ * Operands are multiplied without rounding them and summed in fp32 without atomics: the same call
+ * gives the same bits. 1 <= R <= BT_LORA_MAX_RANK, 0 <= L < 2^31, M * N <= 2^35. An adapter's weights
  * never reach the tokens of another one, whatever they hold.
  */
 #define BT_LORA_MAX_RANK 256
