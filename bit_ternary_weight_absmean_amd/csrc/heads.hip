@@ -7,7 +7,8 @@
 //   pairs are (p, p + rot/2), or (2p, 2p + 1) when interleaved, p < rot/2; the elements from
 //   rot on stay as normalized. V heads are only converted.
 //
-// Bound: bytes. Every QKV value is read once and written once; the rest is kept below that.
+// Bound: bytes. Every QKV value is read once and written once; the rest is kept below that (16384 tokens
+// of 64 + 2 * 8 heads of 128, fp32 to bf16: 195-208 us, 4.8-5.2 TB/s; a large copy moves 4.9).
 //  * Eight values per lane as two 4-value pieces chosen so that both halves of a lane's four
 //    pairs are its own (pieces at 4i and rot/2 + 4i, or 8i and 8i + 4): the rotation needs no
 //    exchange between lanes, and the sum of squares one reduction over the head's lanes
