@@ -119,17 +119,17 @@ bt_status check_attention(int64_t tokens, int64_t keys, int64_t seqs, int64_t he
 {
     if (tokens < 0 || tokens > BT_MAX_DIM || seqs < 0 || seqs > BT_MAX_DIM)
         return fail(BT_ERR_SHAPE, "tokens = %lld or seqs = %lld outside [0, 2^23]", (long long)tokens, (long long)seqs);
-    if (keys < 0 || keys > INT32_MAX - 64 || prefix < 0 || prefix > INT32_MAX - 64)
-        return fail(BT_ERR_SHAPE, "keys = %lld or prefix = %lld outside [0, 2^31 - 65]", (long long)keys,
-                    (long long)prefix);
+    // row and key numbers, and those a few blocks past the last, fit 32 bits
+    if (keys < 0 || keys > BT_ATTENTION_MAX_KEYS || prefix < 0 || prefix > BT_ATTENTION_MAX_KEYS)
+        return fail(BT_ERR_SHAPE, "keys = %lld or prefix = %lld outside [0, 2^30]", (long long)keys, (long long)prefix);
     if (heads < 1 || kv_heads < 1 || heads > 65536 || heads % kv_heads)
         return fail(BT_ERR_SHAPE, "heads = %lld, kv_heads = %lld: heads must be a multiple of kv_heads, at most 65536",
                     (long long)heads, (long long)kv_heads);
     if (head_dim < 8 || head_dim > BT_ATTENTION_MAX_HEAD_DIM || head_dim % 8)
         return fail(BT_ERR_SHAPE, "head_dim = %lld is not a multiple of 8 in [8, %d]", (long long)head_dim,
                     BT_ATTENTION_MAX_HEAD_DIM);
-    if (tokens * heads > INT32_MAX)
-        return fail(BT_ERR_SHAPE, "tokens * heads = %lld not below 2^31", (long long)(tokens * heads));
+    if (tokens * heads > BT_ATTENTION_MAX_KEYS)
+        return fail(BT_ERR_SHAPE, "tokens * heads = %lld above 2^30", (long long)(tokens * heads));
     plan = bt::AttnPlan{};
     if (tokens == 0 || seqs == 0)
         return BT_OK;

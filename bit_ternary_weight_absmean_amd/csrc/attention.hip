@@ -1009,7 +1009,7 @@ __global__ __launch_bounds__(32 * kJoinGroups) void k_attn_combine(AttnArgs a, A
     if (shared) {
         Item p;
         find_item(pre, pre_bm, 0, true, p);
-        const int all = min(it.s.q0 * pre.G + row, pre.T * pre.G - 1);  // T * heads < 2^31
+        const int all = min(it.s.q0 * pre.G + row, pre.T * pre.G - 1);  // T * heads <= 2^30
         p.tile = all / pre_bm;
         prow = all % pre_bm;
         pslot = first_item(pre, p, pre_bm);

@@ -483,13 +483,14 @@ bt_status bt_qk_norm_rope(const bt_heads_shape *shape, const void *qkv, const fl
  * of K and V that a query does not see do not reach it, infinities and NaNs included.
  * head_dim: a multiple of 8 up to BT_ATTENTION_MAX_HEAD_DIM. Strides are in elements; q, k, v and
  * the prefix: 16-byte aligned with strides multiples of 8, row strides of k, v and the prefix at
- * most 2^23; out: aligned to four elements. tokens <= BT_MAX_DIM, tokens * heads < 2^31, scale
- * finite and positive. out and lse must not overlap the inputs.
+ * most 2^23; out: aligned to four elements. tokens <= BT_MAX_DIM; tokens * heads, keys and prefix
+ * at most BT_ATTENTION_MAX_KEYS; scale finite and positive. out and lse must not overlap the inputs.
  *   workspace    bt_attention_workspace_bytes(tokens, keys, seqs, heads, kv_heads, head_dim, prefix)
  *                bytes of device scratch, 256-byte aligned, or NULL when that is 0; contents on
  *                entry are ignored. Calls sharing one must not overlap.
  */
 #define BT_ATTENTION_MAX_HEAD_DIM 256
+#define BT_ATTENTION_MAX_KEYS 1073741824LL /* 2^30 */
 typedef struct {
     int64_t tokens, keys, seqs, prefix; /* rows of q; of k and v; sequences; prefix rows */
     int64_t heads, kv_heads, head_dim;

@@ -177,10 +177,10 @@ def _attention(q=FAKE, k=FAKE, v=FAKE, q_start=FAKE, k_start=FAKE, k_len=FAKE, p
 
 def test_attention_abi_refusals():
     assert bt.lib().bt_attention(None, *[FAKE] * 11, None) == BT_ERR_NULL
-    for change in (dict(tokens=-1), dict(tokens=(1 << 23) + 1), dict(keys=-1), dict(keys=2 ** 31 - 1), dict(seqs=-1),
-                   dict(prefix=-1), dict(heads=5), dict(heads=0), dict(kv_heads=0), dict(heads=65537, kv_heads=65537),
+    for change in (dict(tokens=-1), dict(tokens=(1 << 23) + 1), dict(keys=-1), dict(keys=2 ** 30 + 1), dict(seqs=-1),
+                   dict(prefix=-1), dict(prefix=2 ** 30 + 1), dict(heads=5), dict(heads=0), dict(kv_heads=0), dict(heads=65537, kv_heads=65537),
                    dict(head_dim=60), dict(head_dim=264), dict(head_dim=0), dict(scale=0.0), dict(scale=-1.0),
-                   dict(scale=float("nan")), dict(scale=float("inf")), dict(tokens=1 << 23, heads=256, kv_heads=256),
+                   dict(scale=float("nan")), dict(scale=float("inf")), dict(tokens=(1 << 22) + 1, heads=256, kv_heads=1),
                    dict(tokens=1 << 22, seqs=1 << 22, heads=64, kv_heads=64), dict(k_row=(1 << 23) + 8)):
         assert _attention(**change) == BT_ERR_SHAPE, change
     for change in (dict(type=F32), dict(type=3), dict(out_type=2), dict(out_type=7)):
