@@ -132,6 +132,10 @@ CACHED = [
     # q lengths, k lengths, slab, heads, kv, D, type
     ([1], [1], 1, 20, 5, 128, "bf16"),
     ([1], [777], 1024, 20, 5, 128, "bf16"),
+    ([1], [512], 512, 20, 5, 128, "bf16"),  # uncut, and one key more
+    ([1], [513], 513, 20, 5, 128, "bf16"),
+    ([4, 1], [511, 300], 512, 8, 2, 96, "fp16"),
+    ([4, 1], [513, 300], 513, 8, 2, 96, "fp16"),
     ([1] * 7, [0, 1, 31, 32, 33, 500, 64], 500, 32, 32, 128, "fp16"),
     ([1] * 5, [130, 4000, 3, 128, 127], 4000, 8, 1, 256, "bf16"),
     ([1] * 130, [(37 * i) % 300 for i in range(130)], 300, 16, 2, 64, "bf16"),

@@ -163,8 +163,8 @@ def test_qk_norm_rope_refuses(host_ok):  # noqa: F811
         bt.qk_norm_rope(qkv.double(), pos, inv, 2, 1)
 
 
-# bt_attention_shape of a small valid call, and the call
-ATT = dict(tokens=6, keys=100, seqs=2, prefix=0, heads=4, kv_heads=2, head_dim=64, type=BF16, out_type=BF16, causal=1,
+# bt_attention_shape of a small valid call (with keys enough to need a workspace), and the call
+ATT = dict(tokens=6, keys=2000, seqs=2, prefix=0, heads=4, kv_heads=2, head_dim=64, type=BF16, out_type=BF16, causal=1,
            scale=0.125, q_row=256, q_head=64, k_row=128, k_head=64, v_row=128, v_head=64, prefix_k_row=128,
            prefix_k_head=64, prefix_v_row=128, prefix_v_head=64, out_row=256, out_head=64)
 
@@ -206,6 +206,8 @@ def test_attention_workspace_bytes():
     f = bt.lib().bt_attention_workspace_bytes
     assert f(0, 5, 1, 4, 4, 64, 0) == 0 and f(5, 5, 0, 4, 4, 64, 0) == 0 and f(5, 5, 1, 5, 4, 64, 0) == 0
     assert f(8192, 8192, 1, 32, 32, 128, 0) == 0  # tiles enough: keys are not cut
+    assert f(1, 512, 1, 20, 5, 128, 0) == 0 and f(1, 513, 1, 20, 5, 128, 0) > 0  # few keys: one launch
+    assert f(2, 1024, 2, 20, 5, 128, 0) == 0 and f(2, 1025, 2, 20, 5, 128, 0) > 0
     for sizes in ((1, 1024, 1, 20, 5, 128, 0), (64, 524288, 64, 20, 5, 128, 0), (64, 0, 64, 64, 8, 128, 16384)):
         n = f(*sizes)
         assert n > 0 and n % 256 == 0 and n < 1 << 28, sizes
