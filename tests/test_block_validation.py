@@ -243,5 +243,6 @@ def test_attention_refuses(host_ok):  # noqa: F811
         bt.attention(q, k.transpose(1, 2).contiguous().transpose(1, 2), k, qs, ks, ks)
     with pytest.raises(ValueError, match="lse must have shape"):
         bt.attention(q, k, k, qs, ks, ks, lse=torch.zeros((4, 6)))
+    far = torch.zeros((2000, 2, 64), dtype=b16)  # keys enough to be cut
     with pytest.raises(ValueError, match="workspace holds"):
-        bt.attention(q, k, k, qs, ks, ks, workspace=torch.zeros(8, dtype=torch.uint8))
+        bt.attention(q, far, far, qs, ks, ks, workspace=torch.zeros(8, dtype=torch.uint8))
