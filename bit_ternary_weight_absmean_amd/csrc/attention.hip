@@ -166,8 +166,7 @@ struct Item {
     int tile;           // row tile of the sequence
     int piece, pieces;  // key slice and their number
     int unit;           // units (of kUnit keys) of a slice
-    int b;
-    int base;  // first item of the sequence
+    int base;           // first item of the sequence
 };
 
 // Inclusive sum over the wave's lanes, without LDS: within rows of 16 by row shifts, then the last
@@ -223,7 +222,7 @@ __device__ inline bool find_item(const AttnArgs &a, int bm, int id, bool by_tile
     const int nseq = a.shared ? 1 : a.B;
     if (nseq == 1) {  // nothing to search
         it.s = load_seq(a, 0);
-        it.b = it.base = 0;
+        it.base = 0;
         const int n = row_tiles(a, it.s, bm);
         const float work = (float)n * (float)key_units(it.s);
         it.unit = a.target ? max(a.min_units, (int)fminf(ceilf(work / (float)a.target), 1e9f)) : 1 << 30;
@@ -250,7 +249,6 @@ __device__ inline bool find_item(const AttnArgs &a, int bm, int id, bool by_tile
             it.s.nq = __builtin_amdgcn_readlane(mine.nq, l);
             it.s.k0 = __builtin_amdgcn_readlane(mine.k0, l);
             it.s.nk = __builtin_amdgcn_readlane(mine.nk, l);
-            it.b = c + l;
             it.base = items_before + __builtin_amdgcn_readlane(ii - items, l);
             const int tbase = tiles_before + __builtin_amdgcn_readlane(ti - tiles, l);
             it.pieces = uniform(pieces_of(it.s, it.unit));
@@ -328,7 +326,7 @@ __device__ inline void load_lds16(__amdgpu_buffer_rsrc_t from, char *dst, uint32
 // same card), against 592-620 us with scores, softmax and V's product in sequence. Eight waves of one
 // workgroup in two groups held half a block apart by barriers: 597-620 us; a raised wave priority in
 // the matrix phase: 549 us.
-
+//
 // HALVES == 2, for calls whose tiles of 128 rows would not fill the CUs: 64 rows, and the waves of a pair
 // take the two halves of every block's keys and are joined at the end. Twice the workgroups, each with half
 // the time per block (packed 2B prompts of 2048 tokens: 28.8 us with 128 rows, 26.2 with 64).
