@@ -6,7 +6,9 @@
 //
 // One pass over the keys with a running maximum m and sum l per row (both fp32; scores are kept in
 // powers of two, so exp is one v_exp_f32 of an FMA). A row's accumulator is rescaled only when its
-// maximum rose by more than 2^8: probabilities are relative to the reference m, whatever it is.
+// maximum rose by more than a factor 2^kRise: probabilities are relative to the reference m, whatever it
+// is. The sum l takes a block's probabilities as one term, so that many small ones behind a large one are
+// not lost to it one by one (the matrix cores add eight products at a time to an accumulator).
 //
 // Rows. The G = heads / kv_heads query heads of a key head read the same keys, so a tile's rows are
 // (token, head of the group) pairs: row r of a sequence is token r / G, head r % G of the group. A
@@ -21,7 +23,11 @@
 //
 // Rounding: scores, statistics and accumulators are fp32. Probabilities are rounded to the type of V
 // for the matrix cores, which is of the order of the output's own rounding where the output has that
-// type; for fp32 outputs they are carried as two such values (the rounded one and the rest).
+// type; for fp32 outputs they are carried as two such values (the rounded one and the rest). fp16
+// probabilities, and their rests, are rounded absolutely below 2^-14. All fp16 ones therefore carry a factor
+// 2^9 (so does l, and it cancels), and a maximum may rise by 2^6 only: the largest lies between 2^9 and
+// 2^15, and the absolute rounding is at most 2^-34 of it, a hundredth of what the fp32 accumulators round
+// (2^-24 for eight keys). 2^13 and 2^2 rescale more often: 7B prompt of 8192 tokens 546 us against 541.
 //
 // Masked places. Scores of unseen keys are replaced, never added to, so what K holds there does not
 // matter; keys past a sequence's end are not read at all. An unseen value meets a probability of
@@ -54,7 +60,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kUnit = 64;             // keys: granularity of the key slices
-constexpr float kRescale = 8.0f;      // exponent by which a maximum may rise without rescaling
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kBufferWord3 = 0x00020000;
 constexpr uint32_t kOutside = 0x7FFFFFF0u;  // a buffer offset past every record
@@ -66,6 +71,9 @@ struct Elem<bf16_t> {
     typedef bf16_t v8 __attribute__((ext_vector_type(8)));
     typedef bf16_t v2 __attribute__((ext_vector_type(2)));
     static constexpr uint32_t kExp = 0x7F80u;
+    static constexpr float kRise = 8.0f;    // exponent by which a maximum may rise without rescaling
+    static constexpr float kRaised = 0.0f;  // exponent of the probabilities at the reference
+    static constexpr float kLower = 1.0f;   // 2^-kRaised
     static __device__ f32x16 mma32(v8 a, v8 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -80,6 +88,9 @@ struct Elem<f16_t> {
     typedef f16_t v8 __attribute__((ext_vector_type(8)));
     typedef f16_t v2 __attribute__((ext_vector_type(2)));
     static constexpr uint32_t kExp = 0x7C00u;
+    static constexpr float kRise = 6.0f;
+    static constexpr float kRaised = 9.0f;
+    static constexpr float kLower = 1.0f / 512.0f;
     static __device__ f32x16 mma32(v8 a, v8 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -448,7 +459,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
             for (int i = 0; i < 16; ++i)
                 mx = fmaxf(mx, sc[b][i]);
         mx = fmaxf(mx, other_half(mx));
-        if (__any((mx - m) * c2 > kRescale || (m == -INFINITY && mx > -INFINITY))) {
+        if (__any((mx - m) * c2 > Elem<E>::kRise || (m == -INFINITY && mx > -INFINITY))) {
             const float mn = fmaxf(m, mx);
             const float f = mn == -INFINITY ? 1.f : exp2_fast((m - mn) * c2);
             l *= f;
@@ -459,7 +470,8 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
                     o[d][i] *= f;
             m = mn;
         }
-        const float ref = m == -INFINITY ? 0.f : m * c2;
+        const float ref = m == -INFINITY ? 0.f : __builtin_fmaf(m, c2, -Elem<E>::kRaised);
+        float lb = 0.f;
 #pragma unroll
         for (int t = 0; t < 2 * KB; ++t)
 #pragma unroll
@@ -468,7 +480,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     p[e] = exp2_fast(__builtin_fmaf(sc[t / 2][8 * (t % 2) + 2 * j + e], c2, -ref));
-                    l += p[e];
+                    lb += p[e];
                 }
                 pf[t][j] = pack2<E>(p[0], p[1]);
                 if constexpr (WIDE) {
@@ -476,7 +488,9 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
                     pr[t][j] = pack2<E>(p[0] - back[0], p[1] - back[1]);
                 }
             }
-        // done here, not where they are used
+        l += lb;
+        // done here, not where they are used (the sum unpinned: 4% more for the 7B prompt)
+        asm volatile("" : "+v"(l));
 #pragma unroll
         for (int t = 0; t < 2 * KB; ++t) {
             asm volatile("" : "+v"(pf[t]));
@@ -613,7 +627,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
     }
 
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
-    const float lse = l == 0.f ? -INFINITY : m * c2 * kLn2 + logf(l);
+    const float lse = l == 0.f ? -INFINITY : m * c2 * kLn2 + logf(l * Elem<E>::kLower);
     if (!live)
         return;
     const bool part = PART && (a.pieced || it.pieces > 1);
@@ -794,7 +808,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
         float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
                          fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
         mx = across_quarters(mx, [](float x, float y) { return fmaxf(x, y); });
-        if (__any((mx - m) * c2 > kRescale || (m == -INFINITY && mx > -INFINITY))) {
+        if (__any((mx - m) * c2 > Elem<E>::kRise || (m == -INFINITY && mx > -INFINITY))) {
             const float mn = fmaxf(m, mx);
             const float f = mn == -INFINITY ? 1.f : exp2_fast((m - mn) * c2);
             l *= f;
@@ -803,14 +817,15 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
                 o[d] *= f;
             m = mn;
         }
-        const float ref = m == -INFINITY ? 0.f : m * c2;
+        const float ref = m == -INFINITY ? 0.f : __builtin_fmaf(m, c2, -Elem<E>::kRaised);
         u32x4 pf, pr;
+        float lb = 0.f;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 sc[b][i] = exp2_fast(__builtin_fmaf(sc[b][i], c2, -ref));
-                l += sc[b][i];
+                lb += sc[b][i];
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -821,6 +836,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
                 }
             }
         }
+        l += lb;
         // This wave's LDS writes before its reads: LDS operations of a wave complete in order, so
         // only the compiler has to keep them so.
         asm volatile("" ::: "memory");
@@ -889,7 +905,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
     }
     const float inv = lall > 0.f ? 1.f / lall : (lall == 0.f ? 0.f : lall);
     const float f = m == -INFINITY ? inv : exp2_fast((m - mall) * c2) * inv;
-    const float lse = lall == 0.f ? -INFINITY : mall * c2 * kLn2 + logf(lall);
+    const float lse = lall == 0.f ? -INFINITY : mall * c2 * kLn2 + logf(lall * Elem<E>::kLower);
     // wave's O^T to LDS as [row][D]: 4 values of row col per register group
     float *mine = reinterpret_cast<float *>(vlds(wave));
 #pragma unroll

@@ -1,0 +1,82 @@
+"""bt_attention where sums and probabilities are at the ends of their ranges, in every form of the kernel:
+few rows, 64-row and 128-row tiles, with and without a prefix."""
+import math
+
+import pytest
+import torch
+
+import bit_ternary_weight_absmean_amd as bt
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+LN2 = math.log(2.0)
+
+
+def note(msg):
+    print(f"[gpu-case] {msg}", flush=True)
+
+
+def i32(values):
+    return torch.tensor(values, dtype=torch.int32, device=DEV)
+
+
+# One query sequence length each (all sequences see the same keys), key heads, sequences, keys, prefix
+FORMS = {
+    "few rows, uncut": (1, 1, 2, 1000, 0),
+    "few rows, long slices": (1, 1, 512, 65536, 0),
+    "64-row tiles, uncut": (8192, 1, 1, 131072, 0),
+    "64-row tiles, slices": (200, 2, 1, 40000, 0),
+    "128-row tiles, uncut": (2048, 32, 1, 30000, 0),
+    "prefix, few rows": (1, 4, 3, 5, 9000),
+    "prefix, tiles": (4096, 8, 1, 64, 20000),
+}
+
+
+@pytest.mark.parametrize("exponent", [16, 25, 26])
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("form", FORMS)
+def test_one_large_probability_and_a_long_flat_tail(form, kind, exponent):
+    """Key j0 has a score of e ln 2 above all others, so each of them has 2^-e of its probability.
+
+    Tolerance. The scale is ln 2 to 2^-24 of itself, so scores in powers of two are whole but for
+    26 * 2^-23, and exp is 2^-e but for 2^-18 relative. From there on sums are exact: eight tail products, which the
+    matrix cores add at once, are 2^(3 - e) of the accumulator, at least one unit in its last place for
+    e <= 26, and a block's tail, which is one term of the sum of probabilities, is a multiple of the
+    same; the relative 2^-18 of a term may move each by half a unit, so 2^-18 of the tail's mass plus 2^-24
+    per block of 64 keys (32 keys to a lane) in a sum that is 1 + n 2^-e. The probabilities, powers of two but
+    for 2^-18, are rounded to the type or two of it: relative to the tail's mass by eps / 2. What is left
+    is the division, the slices' joining (8 roundings), and the output's own rounding. None of it grows with
+    the number of keys other than by 2^-24 per block."""
+    n_q, kv, seqs, S, P = FORMS[form]
+    note(f"attention tail {form} {kind} 2^-{exponent}")
+    dt, D = TYPES[kind], 8
+    j0 = (P or S) // 3  # in the prefix, where there is one
+    scale = LN2
+    q = torch.zeros((n_q * seqs, kv, D), dtype=dt, device=DEV)
+    q[..., 0] = 1
+    k = torch.zeros((S, kv, D), dtype=dt, device=DEV)
+    v = torch.ones((S, kv, D), dtype=dt, device=DEV)
+    pk = torch.zeros((P, kv, D), dtype=dt, device=DEV) if P else None
+    pv = torch.ones((P, kv, D), dtype=dt, device=DEV) if P else None
+    (pk if P else k)[j0, :, 0] = exponent
+    (pv if P else v)[j0, :, 4:] = 0  # dimensions 4 .. 7: the tail's mass alone
+    starts = i32([n_q * b for b in range(seqs + 1)])
+    zeros, lens = i32([0] * seqs), i32([S] * seqs)
+    n = S + P - 1
+    tail = n * 2.0 ** -exponent
+    for out_dtype in (dt, torch.float32):
+        lse = torch.empty((n_q * seqs, kv), device=DEV)
+        out, _ = bt.attention(q, k, v, starts, zeros, lens, causal=False, scale=scale, prefix_k=pk, prefix_v=pv,
+                              out_dtype=out_dtype, lse=lse)
+        eps, half = torch.finfo(dt).eps / 2, torch.finfo(out_dtype).eps / 2
+        part = tail / (1 + tail)
+        unit = (n / 64 + 12) * 2.0 ** -24
+        p_err = (2.0 ** -18 + (eps if out_dtype == dt else eps * eps)) * part + unit
+        one = (out[..., :4].double() - 1).abs().max()
+        assert float(one) <= p_err + half * (1 + 2.0 ** -7), float(one)
+        rest = (out[..., 4:].double() - part).abs().max()
+        # an fp16 output below 2^-14 is rounded absolutely
+        assert float(rest) <= p_err + half * part + (2.0 ** -25 if out_dtype == torch.float16 else 0), float(rest)
+        want = exponent * LN2 + math.log1p(tail)
+        assert float((lse.double() - want).abs().max()) <= p_err + 26 * 2.0 ** -23 + 4 * 2.0 ** -24 * want
