@@ -32,8 +32,12 @@
 // Masked places. Scores of unseen keys are replaced, never added to, so what K holds there does not
 // matter; keys past a sequence's end are not read at all. An unseen value meets a probability of
 // exactly 0, and 0 * inf would still be NaN: in a block whose mask is not full, infinities and NaNs
-// of V are set to 0 before the product, and (only if there were any) added afterwards to the rows
-// that see them.
+// of V are set to 0 before the product.
+//
+// Infinities and NaNs of V that a row sees are its output, whatever their probability (which is positive,
+// but may be 0 in fp32, or have a rest of the other sign): a row whose sum came out infinite or NaN
+// although its probabilities did not, or whose masked blocks were cleaned, goes over the values once more
+// (bad_values), and takes from there what it finds. The joining does the same with its slices.
 //
 // Work split. A work item is (row tile, slice of its keys, key head). Sequence lengths are device
 // data, so every workgroup derives the items from them itself (one wave scan over the sequences).
@@ -123,6 +127,8 @@ __device__ inline bool not_finite(uint32_t p)
     constexpr uint32_t e = Elem<E>::kExp;
     return (p & e) == e || (p >> 16 & e) == e;
 }
+
+__device__ inline bool not_finite(float x) { return !(fabsf(x) < INFINITY); }
 
 // A pair of E values with infinities and NaNs set to 0.
 template <typename E>
@@ -322,6 +328,19 @@ __device__ inline void load_lds16(__amdgpu_buffer_rsrc_t from, char *dst, uint32
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the 16-byte form
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)dst, 16, offset, 0, 0, 0);
 #endif
+}
+
+// Adds to bad what four values at v hold of infinities and NaNs, over rows from .. to - 1.
+template <typename E>
+__device__ inline void bad_values(const char *v, int64_t row_bytes, int from, int to, float (&bad)[4])
+{
+    for (int key = from; key < to; ++key) {
+        float x[4];
+        load4(reinterpret_cast<const E *>(v + key * row_bytes), x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bad[j] += not_finite(x[j]) ? x[j] : 0.f;
+    }
 }
 
 // ------------------------------------------------------------------------- prompt kernel
@@ -566,10 +585,8 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
             clean(key, vb);
             if (key < wmost) {
                 soften(key);
-                
                 scores(kb);
                 weigh(vb);
-                
             }
             landed();
             sync();
@@ -607,23 +624,27 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
                 o[d][i] = o[d][i] * f0 + sums[(d * 16 + i) * 64 + lane] * f1;
         m = mn;
     }
-    if (__builtin_expect(poison, 0)) {
-        // The cleaned blocks again, from memory: what they lost goes to the rows that see it.
-        const int from = lo + max(0, gfull - lo) / kTileKeys * kTileKeys;
-        for (int key = from; key < min(hi, limit); ++key) {
-            const char *p = vp + (int64_t)key * vrow_bytes;
+    bool odd = false;
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int e = 32 * d + 8 * (i / 4) + 4 * h + i % 4;
-                    if (e < a.D) {
-                        const float x = (float)reinterpret_cast<const E *>(p)[e];
-                        if (!(fabsf(x) < INFINITY))
-                            o[d][i] += x;
-                    }
-                }
-        }
+        for (int i = 0; i < 16; ++i)
+            odd = odd || not_finite(o[d][i]);
+    if (__builtin_expect((odd || poison) && live && l > 0.f && l < INFINITY, 0)) {
+        // finite sums lack the cleaned blocks only
+        const int from = odd ? lo : lo + max(0, gfull - lo) / kTileKeys * kTileKeys;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int e = 32 * d + 8 * b + 4 * h;
+                float bad[4] = {0.f, 0.f, 0.f, 0.f};
+                if (e < a.D)
+                    bad_values<E>(vp + 2 * e, vrow_bytes, from, min(hi, limit), bad);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[d][4 * b + i] = bad[i] == 0.f ? o[d][4 * b + i] : bad[i];
+            }
     }
 
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
@@ -683,7 +704,7 @@ constexpr int kFewRows = 16, kFewKeys = 32, kFewWaves = 4;
 
 template <typename E, int DP, bool WIDE>
 __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf0, char *buf1,
-                                         float (&stat)[kFewWaves][2][kFewRows])
+                                         float (&stat)[kFewWaves][4][kFewRows])
 {
     using V8 = typename Elem<E>::v8;
     constexpr int CPR = DP / 8;
@@ -864,45 +885,28 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
             step(key + kStride, y);
         }
     }
-    if (__builtin_expect(__any(poison), 0)) {
-        // The cleaned blocks again, from memory: what they lost goes to the rows that see it.
-        for (int key = k0; key < hi; key += kStride) {
-            if (key + kFewKeys <= wfull)
-                continue;
-            for (int j = key; j < min(min(key + kFewKeys, hi), limit); ++j) {
-                const E *p = reinterpret_cast<const E *>(vp + (int64_t)j * vrow_bytes);
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int e = 16 * d + 4 * g + i;
-                        if (e < a.D) {
-                            const float v = (float)p[e];
-                            if (!(fabsf(v) < INFINITY))
-                                o[d][i] += v;
-                        }
-                    }
-            }
-        }
-    }
-
     // join the four waves: common maximum, then the sums
     l = across_quarters(l, [](float x, float y) { return x + y; });
+    const bool cleaned = __any(poison);
     if (g == 0) {
         stat[wave][0][col] = m;
         stat[wave][1][col] = l;
+        stat[wave][2][col] = cleaned ? 1.f : 0.f;
     }
     __syncthreads();
     float mall = stat[0][0][col];
 #pragma unroll
     for (int w = 1; w < kFewWaves; ++w)
         mall = fmaxf(mall, stat[w][0][col]);
-    float lall = 0.f;
+    float lall = 0.f, cleans = 0.f;  // blocks cleaned by any wave
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) {
+        cleans += stat[w][2][col];
         const float mw = stat[w][0][col];
         lall += mw == -INFINITY ? stat[w][1][col] : stat[w][1][col] * exp2_fast((mw - mall) * c2);  // 0, or NaN scores
     }
+    if (threadIdx.x < kFewRows)
+        stat[0][3][col] = lall;
     const float inv = lall > 0.f ? 1.f / lall : (lall == 0.f ? 0.f : lall);
     const float f = m == -INFINITY ? inv : exp2_fast((m - mall) * c2) * inv;
     const float lse = lall == 0.f ? -INFINITY : mall * c2 * kLn2 + logf(lall * Elem<E>::kLower);
@@ -924,6 +928,17 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
 #pragma unroll
         for (int w = 0; w < kFewWaves; ++w)
             sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(vlds(w)) + r * DP + (c ^ (r & 7)) * 4);
+        // (a sum of four that overflows costs a look that finds nothing)
+        const bool odd = not_finite((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (__builtin_expect((odd || cleans > 0.f) && stat[0][3][r] > 0.f && stat[0][3][r] < INFINITY, 0)) {
+            // finite sums lack the cleaned blocks only
+            const int from = odd ? lo : lo + max(0, wfull - lo) / kFewKeys * kFewKeys;
+            float bad[4] = {0.f, 0.f, 0.f, 0.f};
+            bad_values<E>(vp + 8 * c, vrow_bytes, from, min(hi, row_limit(a, s, rr / a.G)), bad);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum[j] = bad[j] == 0.f ? sum[j] : bad[j];
+        }
         const float x[4] = {sum[0], sum[1], sum[2], sum[3]};
         if (part) {
             store4(a.ws_o + ((int64_t)block * kFewRows + r) * a.D + 4 * c, x);
@@ -959,7 +974,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn(AttnArgs a, Attn
     static_assert(bytes == 2 * kFewKeys * DP * 2, "two waves' pieces of the few-rows kernel");
     __shared__ __attribute__((aligned(1024))) char buf0[bytes], buf1[bytes];
     __shared__ __attribute__((aligned(1024))) char buf2[tiles ? bytes : 16], buf3[tiles ? bytes : 16];
-    __shared__ float stat[kFewWaves][2][kFewRows];
+    __shared__ float stat[kFewWaves][4][kFewRows];
     __shared__ int poison;  // attn_tile: a masked block of V held an infinity or NaN
     const int block = blockIdx.x;
     if constexpr (PRE == MAIN) {
@@ -1100,6 +1115,28 @@ __global__ __launch_bounds__(32 * kJoinGroups) void k_attn_combine(AttnArgs a, A
     }
     if (!live)
         return;
+    const f32x4 both = s0 + s1;
+    const bool odd = not_finite((both[0] + both[1]) + (both[2] + both[3]));
+    if (__builtin_expect(odd && total > 0.f && total < INFINITY, 0)) {
+        // a weight of 0 is too small for fp32, not none: what is infinite or NaN in a slice stays
+        f32x4 b0 = {0.f, 0.f, 0.f, 0.f}, b1 = b0;
+        for (int j = 0; j < n; ++j) {
+            const bool own = j < it.pieces;
+            const int64_t at = own ? ((int64_t)(slot + j) * a.Hkv + head) * bm + r
+                                   : ((int64_t)(pslot + j - it.pieces) * a.Hkv + head) * pre_bm + prow;
+            const float *o = (own ? a.ws_o : pre.ws_o) + at * a.D;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                b0[i] += not_finite(o[c0 + i]) ? o[c0 + i] : 0.f;
+                b1[i] += a.D > 128 && not_finite(o[c1 + i]) ? o[c1 + i] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s0[i] = b0[i] == 0.f ? s0[i] : b0[i];
+            s1[i] = b1[i] == 0.f ? s1[i] : b1[i];
+        }
+    }
     const int token = row / a.G, qh = head * a.G + row % a.G;
     const int64_t at = (int64_t)(it.s.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
     const float inv = total == 0.f ? 0.f : 1.f / total;

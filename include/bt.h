@@ -481,7 +481,8 @@ bt_status bt_qk_norm_rope(const bt_heads_shape *shape, const void *qkv, const fl
  * statistics and sums are fp32; probabilities are rounded to `type` for the product with V (with
  * fp32 outputs they are carried to twice that precision), fp16 ones to no less than 2^-34 of the
  * row's largest (2^-23 and below: absolutely). Results do not depend on timing. Values
- * of K and V that a query does not see do not reach it, infinities and NaNs included.
+ * of K and V that a query does not see do not reach it, infinities and NaNs included; infinities
+ * and NaNs of V that it does see are its output, however small their probability.
  * head_dim: a multiple of 8 up to BT_ATTENTION_MAX_HEAD_DIM. Strides are in elements; q, k, v and
  * the prefix: 16-byte aligned with strides multiples of 8, row strides of k, v and the prefix at
  * most 2^23; out: aligned to four elements. tokens <= BT_MAX_DIM; tokens * heads, keys and prefix

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import bit_ternary_weight_absmean_amd as bt
+from tests import block_ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -80,3 +81,74 @@ def test_one_large_probability_and_a_long_flat_tail(form, kind, exponent):
         assert float(rest) <= p_err + half * part + (2.0 ** -25 if out_dtype == torch.float16 else 0), float(rest)
         want = exponent * LN2 + math.log1p(tail)
         assert float((lse.double() - want).abs().max()) <= p_err + 26 * 2.0 ** -23 + 4 * 2.0 ** -24 * want
+
+
+# q lengths, k lengths, slab, heads, key heads, D, prefix
+BAD_VALUES = {
+    "few rows, uncut": ([1, 4], [400, 300], 500, 4, 1, 128, 0),
+    "few rows, slices": ([1] * 3, [3000, 700, 2100], 3000, 8, 2, 64, 0),
+    "64-row tiles, slices": ([200], [2000], 0, 8, 2, 128, 0),
+    "64-row tiles, uncut": ([400] * 12, [400] * 12, 0, 8, 4, 80, 0),
+    "128-row tiles, uncut": ([700] * 4, [700] * 4, 0, 32, 8, 128, 0),
+    "128-row tiles, D 256": ([500] * 9, [500] * 9, 0, 16, 16, 256, 0),
+    "prefix, few rows": ([1, 1, 2], [100, 0, 90], 100, 4, 4, 128, 1500),
+    "prefix, tiles and few rows": ([1] * 40, [(7 * i) % 60 for i in range(40)], 64, 8, 2, 64, 1500),
+    "prefix, tiles": ([150, 20], [150, 25], 160, 6, 3, 80, 700),
+}
+
+
+@pytest.mark.parametrize("scale", [0.1, 5.0])
+@pytest.mark.parametrize("out_type", ["type", "fp32"])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("form", BAD_VALUES)
+def test_infinities_and_nans_that_a_row_sees_are_its_output(form, kind, out_type, scale):
+    """In fully visible blocks as in masked ones, however small the probability (with a scale of 5 nearly
+    all are 0 in fp32) and whatever its rest; and columns that hold none are as if there were none."""
+    q_len, k_len, slab, heads, kv, D, P = BAD_VALUES[form]
+    note(f"attention bad values {form} {kind} {out_type} scale={scale}")
+    dt = TYPES[kind]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(31)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV).to(dt)  # noqa: E731
+    q_start = [sum(q_len[:b]) for b in range(len(q_len) + 1)]
+    k_start = [b * slab if slab else sum(k_len[:b]) for b in range(len(k_len))]
+    S = len(k_len) * slab if slab else sum(k_len)
+    q, k, v = rnd(q_start[-1], heads, D), rnd(S, kv, D), rnd(S, kv, D)
+    pk, pv = (rnd(P, kv, D), rnd(P, kv, D)) if P else (None, None)
+
+    def place(rows, first, n):
+        """Early, middle and late keys of n from `first` on, each in dimensions of its own."""
+        if n > 6:
+            rows[first + 2, :, 1] = math.inf
+            rows[first + 3, :, 2] = -math.inf
+            rows[first + 4, :, D - 1] = math.nan
+            rows[first + 2, :, 4] = math.inf
+            rows[first + n // 2, :, 4] = -math.inf
+            rows[first + n // 2, :, 5] = math.inf
+            rows[first + n - 1, :, 6] = -math.inf
+            rows[first + n - 2, :, 8 % D] = math.nan
+
+    for b in range(len(k_len)):
+        if b != 1:  # one sequence has none
+            place(v, k_start[b], k_len[b])
+    if P:
+        pv[7, :, 9] = math.inf
+        pv[P - 1, :, 10] = -math.inf
+        pv[P // 2, :, 11] = math.nan
+    args = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in (q_start, k_start, k_len)]
+    out_dtype = torch.float32 if out_type == "fp32" else dt
+
+    def run(values, prefix_values):
+        lse = torch.empty((q.shape[0], heads), device=DEV)
+        out, _ = bt.attention(q, k, values, *args, scale=scale, prefix_k=pk, prefix_v=prefix_values, lse=lse,
+                              out_dtype=out_dtype)
+        return out, lse
+
+    out, lse = run(v, pv)
+    ref, _ = block_ref.attention(q, k, v, q_start, k_start, k_len, True, scale, prefix_k=pk, prefix_v=pv)
+    for name, test in (("nan", torch.isnan), ("inf", lambda t: t == math.inf), ("-inf", lambda t: t == -math.inf)):
+        assert torch.equal(test(out), test(ref)), (name, int((test(out) != test(ref)).sum()))
+    zero = lambda t: None if t is None else torch.where(torch.isfinite(t), t, torch.zeros_like(t))  # noqa: E731
+    plain, plain_lse = run(zero(v), zero(pv))
+    fine = torch.isfinite(ref)
+    assert torch.equal(out[fine], plain[fine]) and torch.equal(lse, plain_lse)
