@@ -122,13 +122,11 @@ __device__ inline f32x2 unpack2(uint32_t p)
 
 // Does a pair of E values hold an infinity or NaN?
 template <typename E>
-__device__ inline bool not_finite(uint32_t p)
+__device__ inline bool pair_not_finite(uint32_t p)
 {
     constexpr uint32_t e = Elem<E>::kExp;
     return (p & e) == e || (p >> 16 & e) == e;
 }
-
-__device__ inline bool not_finite(float x) { return !(fabsf(x) < INFINITY); }
 
 // A pair of E values with infinities and NaNs set to 0.
 template <typename E>
@@ -559,7 +557,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
         for (int i = 0; i < LOADS; ++i) {
             u32x4 *p = reinterpret_cast<u32x4 *>(vb + (i * 256 + threadIdx.x) * 16);
             const u32x4 x = *p;
-            if (not_finite<E>(x[0]) || not_finite<E>(x[1]) || not_finite<E>(x[2]) || not_finite<E>(x[3])) {
+            if (pair_not_finite<E>(x[0]) || pair_not_finite<E>(x[1]) || pair_not_finite<E>(x[2]) || pair_not_finite<E>(x[3])) {
                 *p = u32x4{finite_part<E>(x[0]), finite_part<E>(x[1]), finite_part<E>(x[2]), finite_part<E>(x[3])};
                 poison = 1;
             }
@@ -813,8 +811,8 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
                         sc[b][i] = -INFINITY;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i)
-                if (not_finite<E>(x.v[i][0]) || not_finite<E>(x.v[i][1]) || not_finite<E>(x.v[i][2]) ||
-                    not_finite<E>(x.v[i][3])) {
+                if (pair_not_finite<E>(x.v[i][0]) || pair_not_finite<E>(x.v[i][1]) || pair_not_finite<E>(x.v[i][2]) ||
+                    pair_not_finite<E>(x.v[i][3])) {
                     poison = true;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)

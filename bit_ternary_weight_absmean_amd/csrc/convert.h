@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 namespace bt {
@@ -44,6 +45,8 @@ __device__ inline void store4(T *p, const float (&v)[4])
     const f32x4 f = {v[0], v[1], v[2], v[3]};
     *reinterpret_cast<typename vec4_of<T>::type *>(p) = __builtin_convertvector(f, typename vec4_of<T>::type);
 }
+
+__device__ inline bool not_finite(float x) { return !(fabsf(x) < INFINITY); }
 
 inline int type_bytes(int type) { return type == kF32 ? 4 : 2; }
 

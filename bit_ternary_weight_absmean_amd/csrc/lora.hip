@@ -25,6 +25,11 @@
 // two and an fp32 weight three, and the piece products are summed in fp32: 3, 6 or 8 MFMAs for
 // one (of fp32 weights' nine, the last is left out: below 2^-30 of the whole). fp32 MFMA would
 // take 5.3 times the bf16 form's cycles.
+//
+// Infinities. Cut into pieces an infinity becomes inf and inf - inf, and the zero rows and columns that
+// fill up a matrix product (unused ranks, outputs of another row group) make NaNs of infinite H. Where a
+// matrix product's sum comes out infinite or NaN, it is therefore formed again in fp32 FMAs over what belongs
+// to it, which gives what the formula gives; unused ranks of H are stored as 0.
 #include "bt_internal.h"
 #include "convert.h"
 #include "wave.h"
@@ -210,6 +215,40 @@ __device__ inline int adapter_rank(const LoraArgs &a, int ad)
     return a.ranks ? max(0, min(a.ranks[ad], a.R)) : a.R;
 }
 
+// sum_k x[k] w[k] over k0 .. k1 - 1 in FMAs: for sums that are infinite or NaN on the matrix cores.
+template <typename W>
+__device__ inline float plain_dot(const float *x, const W *w, int k0, int k1)
+{
+    float s = 0.f;
+#pragma unroll 1
+    for (int k = k0; k < k1; ++k)
+        s = __builtin_fmaf(x[k], (float)w[k], s);
+    return s;
+}
+
+// Four sums (rows r .. r + 3 of group grp of adapter ad's A with token m over k0 .. k1 - 1) as they are
+// stored in H, but for the scale: unused ranks 0, and infinite or NaN ones formed again.
+template <typename W>
+__device__ inline f32x4 checked_sums(const LoraArgs &a, f32x4 s, int ad, int grp, int r, int rank, int64_t m, int k0,
+                                     int k1)
+{
+    // (four that overflow together cost a look that changes little)
+    if (__builtin_expect(not_finite((s[0] + s[1]) + (s[2] + s[3])), 0)) {
+        const float *x = a.X + m * a.K;
+        const W *w = static_cast<const W *>(a.A) + (((int64_t)ad * a.groups.n + grp) * a.R + r) * a.K;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j, w += a.K) {
+            float v = s[0];  // the four in turn
+            if (r + j >= rank)
+                v = 0.f;
+            else if (not_finite(v))
+                v = plain_dot(x, w, k0, k1);
+            s = f32x4{s[1], s[2], s[3], v};
+        }
+    }
+    return s;
+}
+
 // k_lora_shrink: 16 tokens against RT rank tiles of 16; eight waves take every eighth step of 32 k.
 template <typename W, int RT, bool VEC>
 __global__ __launch_bounds__(64 * kDeepWaves) void k_lora_shrink(LoraArgs a)
@@ -271,8 +310,9 @@ __global__ __launch_bounds__(64 * kDeepWaves) void k_lora_shrink(LoraArgs a)
 #pragma unroll
                 for (int w = 1; w < kDeepWaves; ++w)
                     s += part[w][i][l];
-                s *= a.scale[ad];
                 const int64_t m = m0 + (l & 15);
+                s = checked_sums<W>(a, s, ad, tile / tpg, (tile % tpg) * 16 + (l >> 4) * 4, rank, m, k0, k1);
+                s *= a.scale[ad];
                 float *dst = a.ws + (((int64_t)blockIdx.y * a.M + m) * a.groups.n + tile / tpg) * a.Rp +
                              (tile % tpg) * 16 + (l >> 4) * 4;
                 *reinterpret_cast<f32x4 *>(dst) = s;
@@ -296,6 +336,29 @@ constexpr int kExpandN = 64, kExpandT = kExpandN / 16;
 struct Slab {
     float row[kTile][kExpandN + 4];
 };
+
+// Adapter ad's part of output n of token m in FMAs: for those that are infinite or NaN on the matrix cores.
+template <typename W>
+__device__ inline float plain_output(const LoraArgs &a, int64_t m, int ad, int64_t n)
+{
+    int grp = 0;
+    while (n >= a.groups.end[grp])
+        ++grp;
+    const W *b = static_cast<const W *>(a.B) + ((int64_t)ad * a.N + n) * a.R;
+    const float *h = a.ws + (m * a.groups.n + grp) * a.Rp;
+    const int64_t step = a.M * a.groups.n * a.Rp;
+    const int rank = adapter_rank(a, ad);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int r = 0; r < rank; ++r) {
+        float x = 0.f;
+#pragma unroll 1
+        for (int s = 0; s < a.slices; ++s)
+            x += h[r + s * step];
+        sum = __builtin_fmaf(x, (float)b[r], sum);
+    }
+    return sum;
+}
 
 // The wave's 64 outputs from n0 on of the tokens in `stored`; `mine`: the adapter of token lane % 16.
 template <typename W, bool VEC>
@@ -390,6 +453,15 @@ __device__ __forceinline__ void expand_tile(const LoraArgs &a, int64_t m0, int64
 #pragma unroll
     for (int i = 0; i < kExpandT; ++i)
         *reinterpret_cast<f32x4 *>(&slab.row[t][16 * i + 4 * g]) = acc[i];
+    asm volatile("" ::: "memory");
+    const f32x4 all = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    if (__builtin_expect(not_finite((all[0] + all[1]) + (all[2] + all[3])), 0))
+#pragma unroll 1
+        for (int e = 0; e < 4 * kExpandT; ++e) {
+            const int c = 16 * (e / 4) + 4 * g + e % 4;
+            if (not_finite(slab.row[t][c]))
+                slab.row[t][c] = c < cols ? plain_output<W>(a, m0 + t, mine, n0 + c) : 0.f;
+        }
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < kExpandT; ++i)
@@ -496,6 +568,7 @@ __global__ __launch_bounds__(256, 3) void k_lora_shrink_few(LoraArgs a)
 #pragma unroll
             for (int q = 1; q < kWaves; ++q)
                 s += tile[q][lane];
+            s = checked_sums<W>(a, s, ad, grp, r0 + 4 * g, rank, m0 + t, k0, k1);
             *reinterpret_cast<f32x4 *>(a.ws + (((int64_t)blockIdx.y * a.M + m0 + t) * a.groups.n + grp) * a.Rp + r0 +
                                        4 * g) = s * scale;
         }
@@ -575,7 +648,7 @@ __global__ __launch_bounds__(256, 3) void k_lora_shrink_few(LoraArgs a)
 #pragma unroll
             for (int q = 1; q < kGroupTok; ++q)
                 m = i == q ? tok[q] : m;
-            a.ws[(((int64_t)blockIdx.y * a.M + m0 + m) * a.groups.n + grp) * a.Rp + r0 + r] = s * scale;
+            a.ws[(((int64_t)blockIdx.y * a.M + m0 + m) * a.groups.n + grp) * a.Rp + r0 + r] = r < rows ? s * scale : 0.f;
         }
         if (same)
             __syncthreads();

@@ -418,7 +418,8 @@ bt_status bt_kernel_plan(int32_t call, int64_t M, int64_t N, int64_t K, int32_t 
  *             aligned; contents on entry are ignored. Calls sharing one must not overlap.
  * Operands are multiplied without rounding them and summed in fp32 without atomics: the same call
  * gives the same bits. 1 <= R <= BT_LORA_MAX_RANK, 0 <= L < 2^31, M * N <= 2^35. An adapter's weights
- * never reach the tokens of another one, whatever they hold.
+ * never reach the tokens of another one, whatever they hold. Infinities and NaNs give what the formula
+ * gives, whichever form of the kernels takes the call.
  */
 #define BT_LORA_MAX_RANK 256
 size_t bt_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t ngroups);
