@@ -435,9 +435,10 @@ def _call(dev, fn, *args):
 
 
 # torch.cuda.current_stream(i).cuda_stream and torch.cuda.current_device() without the objects around
-# them: a decode step's calls are shorter than those take.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# them, where this torch has such (one built without a GPU has not, and serves the host-only queries): a
+# decode step's calls are shorter than those take.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _is(t, dtype, shape, device) -> bool:
