@@ -7,6 +7,7 @@ import torch
 
 import bit_ternary_weight_absmean_amd as bt
 from tests import block_ref
+from tests.test_block_attention_gpu import Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -152,3 +153,62 @@ def test_infinities_and_nans_that_a_row_sees_are_its_output(form, kind, out_type
     plain, plain_lse = run(zero(v), zero(pv))
     fine = torch.isfinite(ref)
     assert torch.equal(out[fine], plain[fine]) and torch.equal(lse, plain_lse)
+
+
+UNSEEN = {
+    "few rows": ([4, 3], [70, 3], 8, 2, 128, 0),
+    "few rows, slices": ([1, 2], [300, 4000], 8, 2, 64, 0),
+    "64-row tiles, slices": ([150], [1400], 8, 2, 128, 0),
+    "64-row tiles, uncut": ([400] * 12, [400] * 12, 8, 4, 80, 0),
+    "128-row tiles, uncut": ([700] * 4, [700] * 4, 32, 8, 128, 0),
+    "prefix, tiles and few rows": ([3] * 12, [20 + b for b in range(12)], 8, 2, 128, 900),
+    "prefix, tiles": ([150, 20], [150, 25], 6, 3, 80, 700),
+}
+
+
+@pytest.mark.parametrize("out_type", ["type", "fp32"])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("form", UNSEEN)
+def test_keys_and_values_that_are_nan_reach_only_rows_that_see_them(form, kind, out_type):
+    """The last key and value of every sequence, which its last query alone sees, are NaN: all other rows are
+    bit for bit what they are without."""
+    q_len, k_len, heads, kv, D, P = UNSEEN[form]
+    note(f"attention unseen {form} {kind} {out_type}")
+    c = Case(q_len, k_len, heads, kv, D, kind, prefix=P, seed=12)
+    out_dtype = torch.float32 if out_type == "fp32" else c.dt
+    want, want_lse = c.run(out_dtype=out_dtype)
+    last = torch.tensor([n - 1 for n in c.q_start[1:]], device=DEV)
+    for b, n in enumerate(k_len):
+        c.k[c.k_start[b] + n - 1] = math.nan
+        c.v[c.k_start[b] + n - 1] = math.nan
+    out, lse = c.run(out_dtype=out_dtype)
+    rest = torch.ones(out.shape[0], dtype=torch.bool, device=DEV)
+    rest[last] = False
+    assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
+    assert bool(out[last].isnan().all()) and bool(lse[last].isnan().all())
+
+
+INSTANCES = [
+    # q lengths, k lengths, heads, key heads, D, prefix: tiles of 128 rows go uncut in the first five, few rows
+    # stand behind a tiled prefix in the others
+    ([700] * 4, [700] * 4, 32, 8, 64, 0),
+    ([900, 30, 800, 1000], [900, 30, 800, 1000], 32, 32, 40, 0),
+    ([700] * 4, [700] * 4, 32, 8, 128, 0),
+    ([500] * 9, [500] * 9, 16, 16, 256, 0),
+    ([450] * 10, [450] * 10, 16, 16, 216, 0),
+    ([1] * 40, [(7 * b) % 60 for b in range(40)], 8, 2, 64, 1500),
+    ([2, 1] * 15, [(11 * b) % 50 for b in range(30)], 12, 4, 96, 700),
+    ([1] * 40, [(7 * b) % 60 for b in range(40)], 8, 2, 128, 3001),
+    ([1, 3] * 10, [(5 * b) % 90 for b in range(20)], 8, 4, 256, 800),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("q_len,k_len,heads,kv,D,P", INSTANCES)
+def test_every_instance_of_the_large_tiles(q_len, k_len, heads, kv, D, P, kind):
+    note(f"attention instances q={q_len[:4]} heads={heads}/{kv} D={D} prefix={P} {kind}")
+    c = Case(q_len, k_len, heads, kv, D, kind, prefix=P, seed=D + P)
+    assert P or bt.attention_workspace_bytes(sum(q_len), sum(k_len), len(q_len), heads, kv, D) == 0  # uncut
+    for out_dtype in (c.dt, torch.float32):
+        out, lse = c.run(out_dtype=out_dtype)
+        c.check(out, lse)
