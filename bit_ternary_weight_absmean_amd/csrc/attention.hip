@@ -23,7 +23,10 @@
 //
 // Rounding: scores, statistics and accumulators are fp32. Probabilities are rounded to the type of V
 // for the matrix cores, which is of the order of the output's own rounding where the output has that
-// type; for fp32 outputs they are carried as two such values (the rounded one and the rest). fp16
+// type; for fp32 outputs, and in the few-rows kernel always (the second product costs it nothing: 64 tokens
+// over slabs of 8192 keys 132.4 us with and without, 8 requests behind 1000 keys 18.4 against 18.2), they
+// are carried as two such values (the rounded one and the rest). For 16-bit outputs of tiles the rest would
+// cost a third (7B prompt of 8192 tokens, fp16: 549 us, with the rest and fp32 outputs 744). fp16
 // probabilities, and their rests, are rounded absolutely below 2^-14. All fp16 ones therefore carry a factor
 // 2^9 (so does l, and it cancels), and a maximum may rise by 2^6 only: the largest lies between 2^9 and
 // 2^15, and the absolute rounding is at most 2^-34 of it, a hundredth of what the fp32 accumulators round
@@ -849,10 +852,8 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 pf[2 * b + j] = pack2<E>(sc[b][2 * j], sc[b][2 * j + 1]);
-                if constexpr (WIDE) {
-                    const f32x2 back = unpack2<E>(pf[2 * b + j]);
-                    pr[2 * b + j] = pack2<E>(sc[b][2 * j] - back[0], sc[b][2 * j + 1] - back[1]);
-                }
+                const f32x2 back = unpack2<E>(pf[2 * b + j]);
+                pr[2 * b + j] = pack2<E>(sc[b][2 * j] - back[0], sc[b][2 * j + 1] - back[1]);
             }
         }
         l += lb;
@@ -863,8 +864,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, int block, char *buf
         for (int d = 0; d < ND; ++d) {
             const V8 v = __builtin_bit_cast(V8, v_frag(d));
             o[d] = Elem<E>::mma16(v, __builtin_bit_cast(V8, pf), o[d]);
-            if constexpr (WIDE)
-                o[d] = Elem<E>::mma16(v, __builtin_bit_cast(V8, pr), o[d]);
+            o[d] = Elem<E>::mma16(v, __builtin_bit_cast(V8, pr), o[d]);
         }
         asm volatile("" ::: "memory");
     };

@@ -480,8 +480,8 @@ bt_status bt_qk_norm_rope(const bt_heads_shape *shape, const void *qkv, const fl
  *                sequence's own keys; they are read once for all of the batch's queries.
  * type: BT_BF16 or BT_F16, of q, k, v and the prefix; out_type: the same or BT_F32. Scores,
  * statistics and sums are fp32; probabilities are rounded to `type` for the product with V (with
- * fp32 outputs they are carried to twice that precision), fp16 ones to no less than 2^-34 of the
- * row's largest (2^-23 and below: absolutely). Results do not depend on timing. Values
+ * fp32 outputs, and for sequences of a few rows, they are carried to twice that precision), fp16
+ * ones to no less than 2^-34 of the row's largest (2^-23 and below: absolutely). Results do not depend on timing. Values
  * of K and V that a query does not see do not reach it, infinities and NaNs included; infinities
  * and NaNs of V that it does see are its output, however small their probability.
  * head_dim: a multiple of 8 up to BT_ATTENTION_MAX_HEAD_DIM. Strides are in elements; q, k, v and

@@ -212,3 +212,41 @@ def test_every_instance_of_the_large_tiles(q_len, k_len, heads, kv, D, P, kind):
     for out_dtype in (c.dt, torch.float32):
         out, lse = c.run(out_dtype=out_dtype)
         c.check(out, lse)
+
+
+FEW = [
+    ([1], [777], 1024, 20, 5, 128, 0),
+    ([1] * 20, [(331 * b) % 3000 for b in range(20)], 3000, 20, 5, 128, 0),
+    ([4, 1, 2], [900, 300, 77], 900, 8, 2, 64, 0),
+    ([1, 1], [5000, 4000], 5000, 8, 1, 256, 0),
+    ([1, 1, 2], [90, 0, 60], 90, 4, 4, 96, 1500),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("q_len,k_len,slab,heads,kv,D,P", FEW)
+def test_few_rows_round_once(q_len, k_len, slab, heads, kv, D, P, kind):
+    """The 16-bit outputs of few rows are off by their own rounding and by what fp32 sums are: probabilities
+    are carried to twice the type's precision. Tolerance: half a step of the output; eps / 2 squared of
+    sum p |v| for the probabilities (fp16: at least 2^-34 of the largest for every key); an error e of a
+    score counts twice (the probability and the sum), e being D / 8 + 2 roundings of scale * sum |q k|, and
+    sums of n keys n / 16 + 4 roundings, both as for the other forms; joining slices 8 roundings."""
+    note(f"attention few rows rounding q={q_len[:4]} heads={heads}/{kv} D={D} prefix={P} {kind}")
+    c = Case(q_len, k_len, heads, kv, D, kind, slab=slab, prefix=P, seed=7 + D)
+    out, _ = c.run()
+    wide = lambda t: None if t is None else t.double()  # noqa: E731
+    args = (c.q_start, c.k_start, c.k_len, True)
+    ref, _ = block_ref.attention(c.q.double(), c.k.double(), c.v.double(), *args, prefix_k=wide(c.pk),
+                                 prefix_v=wide(c.pv))
+    mag, _ = block_ref.attention(c.q.double(), c.k.double(), c.v.double().abs(), *args, prefix_k=wide(c.pk),
+                                 prefix_v=None if c.pv is None else c.pv.double().abs())
+    eps = torch.finfo(c.dt).eps / 2
+    n = max(k_len) + P
+    kmax = max(float(t.double().norm(dim=-1).max()) for t in (c.k, c.pk) if t is not None)
+    e = (D / 8 + 2) * 2.0 ** -24 * D ** -0.5 * c.q.double().norm(dim=-1, keepdim=True) * kmax
+    tol = (2 * e + eps * eps + 2 * (n / 16 + 12) * 2.0 ** -24) * mag + eps * ref.abs() * (1 + 2.0 ** -7) + 1e-30
+    if kind == "fp16":
+        sums = [t.double().abs().sum(0).max() for t in (c.v, c.pv) if t is not None]
+        tol = tol + 2.0 ** -34 * float(sum(sums)) + 2.0 ** -25
+    d = (out.double() - ref).abs()
+    assert bool((d <= tol).all()), float((d / tol).max())
