@@ -565,7 +565,7 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor | None, inv_freq: to
     ``qkv`` [M, (heads + 2 kv_heads) * D], and the conversion of Q, K and V to the attention's type.
 
     ``inv_freq`` [rot_dim / 2] fp64 (None: no rotation) gives the rotated part of the heads. ``out`` =
-    (q [M, heads, D], k, v) of one type, rows and heads at any stride; k and v are [M, kv_heads, D], or
+    (q [M, heads, D], k, v) of one type, rows and heads at strides of whole fours; k and v are [M, kv_heads, D], or
     caches [any, kv_heads, D] with ``rows`` [M] int32 naming each token's row (outside: not written).
     Without ``out``, new tensors of ``dtype``. Returns (q, k, v)."""
     in_type = _type_of(qkv, "qkv", _TYPES)
@@ -646,9 +646,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.
               lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """bt_attention: softmax attention of packed sequences with grouped heads.
 
-    ``q`` [T, heads, D], ``k`` and ``v`` [rows, kv_heads, D] (bf16 or fp16, any row and head strides).
-    Sequence b has queries q_start[b] .. q_start[b + 1] and keys k_start[b] .. + k_len[b] (int32, on the
-    device); ``causal``: its last query sees all of them. With ``prefix_k`` / ``prefix_v`` [P, kv_heads,
+    ``q`` [T, heads, D], ``k`` and ``v`` [rows, kv_heads, D] (bf16 or fp16, row and head strides of
+    whole eights). Sequence b has queries q_start[b] .. q_start[b + 1] and keys k_start[b] .. + k_len[b]
+    (int32, on the device); ``causal``: its last query sees all of them. With ``prefix_k`` / ``prefix_v`` [P, kv_heads,
     D] every query also sees the whole prefix. ``scale`` defaults to D ** -0.5. ``out`` [T, heads, D] in
     q's type or fp32 (``out_dtype``); ``lse`` [T, heads] fp32 receives the log of the softmax's sum.
     Rows of no sequence are not written. Returns (out, lse)."""

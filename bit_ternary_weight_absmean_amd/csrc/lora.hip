@@ -326,10 +326,11 @@ __global__ __launch_bounds__(64 * kDeepWaves) void k_lora_shrink(LoraArgs a)
 // k_lora_expand: each wave on its own takes 16 tokens and 64 outputs. H and the weights go from
 // memory straight into the MFMA operands (no barrier), and Y0 is requested before either, so that a wave
 // waits twice: for its tokens' adapters, and for what depends on them. Y0 and Y move as 256-byte pieces of
-// four rows, past the caches (nothing reads them again here), the sums through LDS into that order: 2048
-// tokens of 2B gate+up, both kernels, 61.5 us (4.2 TB/s; a large copy reaches 4.9), against 67.9 us without
-// the cache hint, 71.6 us with the MFMA's own order (64-byte pieces of sixteen rows), 82 us with H read
-// again from every slice of K.
+// four rows, past the caches, the sums through LDS into that order: 2048 tokens of 2B gate+up, both kernels,
+// 61 us (4.2 TB/s; a large copy reaches 4.9), against 67.9 us through the caches, 71.6 us with the MFMA's own
+// order (64-byte pieces of sixteen rows), 82 us with H read again from every slice of K. Between the product
+// that wrote Y0 and a launch that reads Y, past / through the caches: 2048 tokens of 2B QKV with the product
+// and the head norms 70.5 / 66.8 us, 4096 of 7B QKV 330 / 337, 2048 of 2B gate+up with the product 125.5 / 127.
 constexpr int kStream = 2;  // buffer loads and stores: non-temporal
 constexpr int kExpandN = 64, kExpandT = kExpandN / 16;
 
@@ -772,9 +773,9 @@ struct LoraPlan {
 
 // The few-tokens form costs a workgroup per token, most of them idle where tokens come in runs; the other
 // form walks a tile's adapters one after the other. 256 tokens in random order over 64 adapters of 7B O,
-// few / many: 32 / 76 us; 1024: 103 / 150 us; in runs over 4 adapters of 2B QKV, 256 tokens: 21 / 12 us;
-// of 7B QKV (rank 64), 512: 66 / 40 us. Which one it will be is device data; adapters that tokens hardly
-// share are taken for the first.
+// few / many: 32 / 72 us; 512: 54 / 78; 1024 (sixteen tokens for each adapter): 91 / 108 in random order and
+// 33 / 18 in runs; in runs over 4 adapters of 2B QKV, 256 tokens: 20 / 12 us; of 7B QKV (rank 64), 512: 66 / 40
+// us. Which one it will be is device data; adapters that tokens hardly share (kFewPer) are taken for the first.
 LoraPlan lora_plan(int64_t M, int64_t K, int64_t R, int64_t groups, bool few)
 {
     LoraPlan p;
