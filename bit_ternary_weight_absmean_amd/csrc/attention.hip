@@ -353,14 +353,14 @@ __device__ inline void bad_values(const char *v, int64_t row_bytes, int from, in
 // product with V and the next block's scores on the matrix cores. Kept apart (the probabilities are
 // pinned at the end of the first phase), the matrix phase is one unbroken run of 32 MFMAs fed from LDS,
 // and the two waves of a SIMD, which belong to different workgroups, alternate: a 7B prompt of 8192
-// tokens takes 541 us (1.02 PFLOP/s; a large bf16 matrix product of the library reaches 1.38 on the
+// tokens takes 542-549 us (1.0 PFLOP/s; a large bf16 matrix product of the library reaches 1.38 on the
 // same card), against 592-620 us with scores, softmax and V's product in sequence. Eight waves of one
 // workgroup in two groups held half a block apart by barriers: 597-620 us; a raised wave priority in
 // the matrix phase: 549 us.
 //
 // HALVES == 2, for calls whose tiles of 128 rows would not fill the CUs: 64 rows, and the waves of a pair
 // take the two halves of every block's keys and are joined at the end. Twice the workgroups, each with half
-// the time per block (packed 2B prompts of 2048 tokens: 28.8 us with 128 rows, 26.2 with 64).
+// the time per block (packed 2B prompts of 2048 tokens: 28.8 us with 128 rows, 25.0-26.2 with 64).
 
 constexpr int kTileRows = 128, kSmallRows = 64, kTileKeys = 64;
 
@@ -699,7 +699,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
 // holds 16 bytes of key r), V through a private piece of LDS for the transposing read, and the next
 // block's loads are issued before this block is used, so that no barrier and no other wave is waited
 // for until the four partial results are joined at the end. 64 tokens over slabs of up to 8192 keys (2B
-// heads, 678 MB): 129-132 us with the joining, 5.2 TB/s.
+// heads, 678 MB): 132.5 us with the joining, 5.1 TB/s.
 
 constexpr int kFewRows = 16, kFewKeys = 32, kFewWaves = 4;
 
@@ -1214,7 +1214,9 @@ AttnPart plan_part(int64_t rows, int64_t seqs, int64_t keys, int64_t Hkv, bool a
         p.bm = kSmallRows;
     p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
     // Keys are cut so that about `want` workgroups share the work: eight per CU where the bytes of the
-    // keys are all that counts, and fewer for large tiles, whose outputs cost more to join.
+    // keys are all that counts, and fewer for large tiles, whose outputs cost more to join. 256 / 384 / 512 of
+    // those: 64 requests behind 16384 keys 71 / 67 / 74 us, 256 tokens over 8192 keys (2B) 52 / 46 / 55,
+    // eight drafts of 8 tokens over 4000 keys 25.6 / 25.2 / 31.8.
     const bool few = p.bm == kFewRows;
     const int64_t want = few ? 2048 : 384;
     const int64_t target = (want + Hkv - 1) / Hkv;
