@@ -344,6 +344,29 @@ __device__ inline void bad_values(const char *v, int64_t row_bytes, int from, in
     }
 }
 
+// The same, eight rows in flight (the last one again where there are no more: an infinity added twice is the
+// same infinity) and no more once all four are NaN: for tiles, whose lanes have sixteen fours of a long
+// prompt's values each. The few-rows kernel's short calls would pay for its size (8 requests behind 1000 keys
+// 18.4 -> 19.0 us).
+template <typename E>
+__device__ inline void many_bad_values(const char *v, int64_t row_bytes, int from, int to, float (&bad)[4])
+{
+    constexpr int kFlight = 8;
+    for (int key = from; key < to; key += kFlight) {
+        float x[kFlight][4];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u)
+            load4(reinterpret_cast<const E *>(v + min(key + u, to - 1) * row_bytes), x[u]);
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                bad[j] += not_finite(x[u][j]) ? x[u][j] : 0.f;
+        if (bad[0] != bad[0] && bad[1] != bad[1] && bad[2] != bad[2] && bad[3] != bad[3])
+            break;
+    }
+}
+
 // ------------------------------------------------------------------------- prompt kernel
 //
 // attn_tile: 32 rows per wave (32x32x16 MFMA) against a slice of the tile's keys, 64 at a time. K and
@@ -632,16 +655,17 @@ __device__ __forceinline__ void attn_tile(const AttnArgs &a, int block, char *kb
         for (int i = 0; i < 16; ++i)
             odd = odd || not_finite(o[d][i]);
     if (__builtin_expect((odd || poison) && live && l > 0.f && l < INFINITY, 0)) {
-        // finite sums lack the cleaned blocks only
-        const int from = odd ? lo : lo + max(0, gfull - lo) / kTileKeys * kTileKeys;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int e = 32 * d + 8 * b + 4 * h;
                 float bad[4] = {0.f, 0.f, 0.f, 0.f};
-                if (e < a.D)
-                    bad_values<E>(vp + 2 * e, vrow_bytes, from, min(hi, limit), bad);
+                // finite sums lack the cleaned blocks only (four that overflow together cost a look)
+                const bool all = not_finite((o[d][4 * b] + o[d][4 * b + 1]) + (o[d][4 * b + 2] + o[d][4 * b + 3]));
+                const int from = all ? lo : lo + max(0, gfull - lo) / kTileKeys * kTileKeys;
+                if (e < a.D && (all || poison))
+                    many_bad_values<E>(vp + 2 * e, vrow_bytes, from, min(hi, limit), bad);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     o[d][4 * b + i] = bad[i] == 0.f ? o[d][4 * b + i] : bad[i];
