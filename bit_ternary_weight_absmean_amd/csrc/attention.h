@@ -8,6 +8,7 @@
 namespace bt {
 
 struct AttnArgs {
+    static constexpr bool kPaged = false;
     const void *q, *k, *v;
     const int *q_start, *k_start, *k_len;
     void *out;
@@ -39,5 +40,25 @@ struct AttnPlan {
 AttnPlan attn_plan(int64_t T, int64_t S, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t P);
 hipError_t launch_attention(const AttnArgs &args, const AttnArgs &prefix, const AttnPlan &p, int type, int out_type,
                             hipStream_t s);
+
+// Attention over a 4-bit cache in pages (csrc/attention4.hip). Of AttnArgs it leaves out k, v, k_start and
+// their strides; S is what a row of the table can hold.
+struct Attn4Args : AttnArgs {
+    static constexpr bool kPaged = true;
+    const char *cache;
+    const int *table;
+    int64_t page_bytes, table_row;
+    int pages, page_shift;  // pages of 1 << page_shift tokens
+    int head_bytes;         // of a page
+    int groups;             // of 32 values in a row
+};
+
+struct Attn4Plan {
+    AttnPart main;
+    size_t bytes;
+};
+
+Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t most_keys);
+hipError_t launch_attention4(const Attn4Args &args, const Attn4Plan &p, int type, int out_type, hipStream_t s);
 
 }  // namespace bt
