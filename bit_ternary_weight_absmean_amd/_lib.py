@@ -43,6 +43,20 @@ SIGNATURES = {
     "bt_qk_norm_rope": (_i32, [_vp] * 11),
     "bt_attention_workspace_bytes": (_sz, [_i64] * 7),
     "bt_attention": (_i32, [_vp] * 13),
+    "bt_cache4_page_bytes": (_sz, [_i64] * 3),
+    "bt_cache4_write": (_i32, [_vp] * 6),
+    "bt_cache4_read": (_i32, [_vp] * 6),
+    "bt_attention4_workspace_bytes": (_sz, [_i64] * 7),
+    "bt_attention4": (_i32, [_vp] * 10),
+    "bt_pages_workspace_bytes": (_sz, [_i64] * 3),
+    "bt_pages_grow": (_i32, [_vp] * 12),
+    "bt_pages_fork": (_i32, [_vp] * 8),
+    "bt_pages_compact": (_i32, [_vp] * 7),
+    "bt_pages_copy": (_i32, [_vp] * 4 + [_i64, _vp]),
+    "bt_int8_weight_bytes": (_sz, [_i64, _i64]),
+    "bt_int8_pack": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp]),
+    "bt_int8_workspace_bytes": (_sz, [_i64] * 3),
+    "bt_int8_gemm": (_i32, [_vp] * 4 + [_i64] * 3 + [_vp, _vp, _i32, _vp, _vp, _vp]),
     "bt_status_str": (ctypes.c_char_p, [_i32]),
     "bt_last_error": (ctypes.c_char_p, []),
 }

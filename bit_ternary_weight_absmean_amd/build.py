@@ -27,7 +27,7 @@ CEILINGS_LIB = os.path.join(PKG, "libbt_ceilings.so")
 ARCH = "gfx950"
 
 SOURCES = ["abi.hip", "pack.hip", "quant.hip", "gemv.hip", "lut.hip", "bits.hip", "decode.hip", "gemm.hip",
-           "heads.hip", "lora.hip", "attention.hip"]
+           "heads.hip", "lora.hip", "attention.hip", "attention4.hip", "cache4.hip", "pages.hip", "int8.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -11,6 +11,8 @@
 #include "attention.h"
 #include "bt.h"
 #include "bt_internal.h"
+#include "cache4.h"
+#include "pages.h"
 
 // Scratch of bt_ternary_linear_static: one copy per GPU, held by the loaded library until
 // the process ends. Host code never passes `scratch` itself to a kernel (in host code the
@@ -137,6 +139,147 @@ bt_status check_attention(int64_t tokens, int64_t keys, int64_t seqs, int64_t he
     if ((plan.main.items + plan.pre.items) * kv_heads >= 1 << 24)
         return fail(BT_ERR_SHAPE, "%lld work items for one launch",
                     (long long)((plan.main.items + plan.pre.items) * kv_heads));
+    return BT_OK;
+}
+
+// The shape of a 4-bit cache; its page shift.
+bt_status check_cache4(int64_t pages, int64_t page_tokens, int64_t kv_heads, int64_t head_dim, int &shift)
+{
+    if (page_tokens < 16 || page_tokens > 1024 || (page_tokens & (page_tokens - 1)))
+        return fail(BT_ERR_SHAPE, "page_tokens = %lld is not a power of two in [16, 1024]", (long long)page_tokens);
+    if (head_dim < 8 || head_dim > BT_ATTENTION_MAX_HEAD_DIM || head_dim % 8)
+        return fail(BT_ERR_SHAPE, "head_dim = %lld is not a multiple of 8 in [8, %d]", (long long)head_dim,
+                    BT_ATTENTION_MAX_HEAD_DIM);
+    if (kv_heads < 1 || kv_heads > 65536 || kv_heads * bt::cache_groups(head_dim) > 65536)
+        return fail(BT_ERR_SHAPE, "kv_heads = %lld with head_dim = %lld: more than 65536 groups, or none",
+                    (long long)kv_heads, (long long)head_dim);
+    if (pages < 0 || pages > BT_ATTENTION_MAX_KEYS || pages * page_tokens > BT_ATTENTION_MAX_KEYS)
+        return fail(BT_ERR_SHAPE, "pages = %lld of %lld tokens: more than 2^30 tokens", (long long)pages,
+                    (long long)page_tokens);
+    shift = __builtin_ctzll((unsigned long long)page_tokens);
+    return BT_OK;
+}
+
+bt_status check_cache4_rows(const bt_cache4_rows *shape, const void *k, const void *v, const int32_t *rows,
+                            const void *cache, bt::CacheRows &a)
+{
+    if (!shape)
+        return fail(BT_ERR_NULL, "shape is NULL");
+    const bt_cache4_rows &s = *shape;
+    a = bt::CacheRows{};
+    if (bt_status e = check_cache4(s.pages, s.page_tokens, s.kv_heads, s.head_dim, a.page_shift))
+        return e;
+    if (s.tokens < 0 || s.tokens > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "tokens = %lld outside [0, 2^23]", (long long)s.tokens);
+    a.groups = bt::cache_groups(s.head_dim);
+    if (s.tokens * s.kv_heads * a.groups >= 1LL << 28)  // eight work-items each
+        return fail(BT_ERR_SHAPE, "%lld groups of values in one call: 2^28 or more",
+                    (long long)(s.tokens * s.kv_heads * a.groups));
+    if (s.type != BT_F32 && s.type != BT_BF16 && s.type != BT_F16)
+        return fail(BT_ERR_UNSUPPORTED, "type %lld", (long long)s.type);
+    if (s.tokens == 0)
+        return BT_OK;
+    if (!k || !v || !rows || (s.pages > 0 && !cache))
+        return fail(BT_ERR_NULL, "NULL k, v, rows or cache");
+    const int64_t strides[] = {s.k_row, s.k_head, s.v_row, s.v_head};
+    for (int64_t stride : strides)
+        if (stride < 0 || stride % 4)
+            return fail(BT_ERR_ALIGN, "strides of k and v must be multiples of 4");
+    const int align = s.type == BT_F32 ? 16 : 8;
+    if (!aligned(k, align) || !aligned(v, align) || !aligned(cache, 16) || !aligned(rows, 4))
+        return fail(BT_ERR_ALIGN, "k and v must be aligned to four elements, the cache to 16 bytes, rows to 4");
+    a.rows = rows;
+    a.page_bytes = s.kv_heads * bt::cache_head_bytes(s.page_tokens, s.head_dim);
+    a.k_row = s.k_row;
+    a.k_head = s.k_head;
+    a.v_row = s.v_row;
+    a.v_head = s.v_head;
+    a.places = s.pages * s.page_tokens;
+    a.M = (int)s.tokens;
+    a.Hkv = (int)s.kv_heads;
+    a.D = (int)s.head_dim;
+    return BT_OK;
+}
+
+// Shape checks of bt_attention4 that its workspace size shares.
+bt_status check_attention4(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                           int64_t max_pages, int64_t page_tokens, bt::Attn4Plan &plan)
+{
+    int shift;
+    if (bt_status e = check_cache4(0, page_tokens, kv_heads, head_dim, shift))
+        return e;
+    if (tokens < 0 || tokens > BT_MAX_DIM || seqs < 0 || seqs > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "tokens = %lld or seqs = %lld outside [0, 2^23]", (long long)tokens, (long long)seqs);
+    if (heads < 1 || heads > 65536 || heads % kv_heads)
+        return fail(BT_ERR_SHAPE, "heads = %lld, kv_heads = %lld: heads must be a multiple of kv_heads, at most 65536",
+                    (long long)heads, (long long)kv_heads);
+    if (tokens * heads > BT_ATTENTION_MAX_KEYS)
+        return fail(BT_ERR_SHAPE, "tokens * heads = %lld above 2^30", (long long)(tokens * heads));
+    if (max_pages < 0 || max_pages > BT_ATTENTION_MAX_KEYS || max_pages * page_tokens > BT_ATTENTION_MAX_KEYS)
+        return fail(BT_ERR_SHAPE, "max_pages = %lld: more than 2^30 tokens of a sequence", (long long)max_pages);
+    plan = bt::Attn4Plan{};
+    if (tokens == 0 || seqs == 0)
+        return BT_OK;
+    plan = bt::attn4_plan(tokens, seqs, heads, kv_heads, head_dim, max_pages * page_tokens);
+    if (plan.main.items * kv_heads >= 1 << 24)
+        return fail(BT_ERR_SHAPE, "%lld work items for one launch", (long long)(plan.main.items * kv_heads));
+    return BT_OK;
+}
+
+// The shape of a table of pages and, where `pool` counts, of what it lies over.
+bt_status check_pages(const bt_pages_shape *shape, bool pooled, bt::PagesArgs &a)
+{
+    if (!shape)
+        return fail(BT_ERR_NULL, "shape is NULL");
+    const bt_pages_shape &s = *shape;
+    a = bt::PagesArgs{};
+    if (s.page_tokens < 1 || s.page_tokens > 1024 || (s.page_tokens & (s.page_tokens - 1)))
+        return fail(BT_ERR_SHAPE, "page_tokens = %lld is not a power of two up to 1024", (long long)s.page_tokens);
+    const int64_t most = BT_ATTENTION_MAX_KEYS / s.page_tokens;
+    if (s.pages < 0 || s.pages > 1 << 24 || s.pages > most || s.max_pages < 0 || s.max_pages > most)
+        return fail(BT_ERR_SHAPE, "pages = %lld or max_pages = %lld: above 2^24 pages or 2^30 tokens", (long long)s.pages,
+                    (long long)s.max_pages);
+    if (s.seqs < 0 || s.seqs > BT_MAX_DIM || s.seqs * (s.max_pages + 1) >= 1LL << 31)
+        return fail(BT_ERR_SHAPE, "a table of %lld x %lld entries", (long long)s.seqs, (long long)s.max_pages);
+    if (s.tokens < 0 || s.tokens > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "tokens = %lld outside [0, 2^23]", (long long)s.tokens);
+    a.B = (int)s.seqs;
+    a.W = (int)s.max_pages;
+    a.P = (int)s.pages;
+    a.T = (int)s.tokens;
+    a.page_shift = __builtin_ctzll((unsigned long long)s.page_tokens);
+    if (!pooled || s.layers == 0)
+        return BT_OK;
+    if (s.layers < 0 || s.layers > 65536 || s.page_bytes < 16 || s.page_bytes > 1LL << 30 || s.page_bytes % 16)
+        return fail(BT_ERR_SHAPE, "a pool of %lld layers of pages of %lld bytes", (long long)s.layers,
+                    (long long)s.page_bytes);
+    if (s.layers > 1 && (s.layer_stride % 16 || s.layer_stride < s.pages * s.page_bytes))
+        return fail(BT_ERR_SHAPE, "layers %lld bytes apart: not a multiple of 16, or shorter than their pages",
+                    (long long)s.layer_stride);
+    a.layers = (int)s.layers;
+    a.layer_stride = s.layers > 1 ? s.layer_stride : 0;
+    a.page_bytes = s.page_bytes;
+    return BT_OK;
+}
+
+bt_status check_pages_arrays(const void *table, const void *length, const void *refs, const void *first,
+                             const void *list, const void *workspace)
+{
+    if (!table || !length || !refs || !first || !list || !workspace)
+        return fail(BT_ERR_NULL, "NULL table, length, refs, first, list or workspace");
+    if (!aligned(table, 4) || !aligned(length, 4) || !aligned(refs, 4) || !aligned(first, 4) || !aligned(list, 4))
+        return fail(BT_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
+    if (!aligned(workspace, 16))
+        return fail(BT_ERR_ALIGN, "workspace must be 16-byte aligned");
+    return BT_OK;
+}
+
+bt_status check_pool(const bt::PagesArgs &a, const void *pool)
+{
+    if (a.layers > 0 && a.P > 0 && !pool)
+        return fail(BT_ERR_NULL, "pool is NULL");
+    if (!aligned(pool, 16))
+        return fail(BT_ERR_ALIGN, "the pool must be 16-byte aligned");
     return BT_OK;
 }
 
@@ -842,6 +985,270 @@ bt_status bt_attention(const bt_attention_shape *shape, const void *q, const voi
     }
     return hip_status(bt::launch_attention(a, pre, plan, s.type, s.out_type, static_cast<hipStream_t>(stream)),
                       "bt_attention launch");
+}
+
+size_t bt_cache4_page_bytes(int64_t page_tokens, int64_t kv_heads, int64_t head_dim)
+{
+    int shift;
+    if (check_cache4(0, page_tokens, kv_heads, head_dim, shift))
+        return 0;
+    return (size_t)(kv_heads * bt::cache_head_bytes(page_tokens, head_dim));
+}
+
+bt_status bt_cache4_write(const bt_cache4_rows *shape, const void *k, const void *v, const int32_t *rows, void *cache,
+                          void *stream)
+{
+    bt::CacheRows a;
+    if (bt_status e = check_cache4_rows(shape, k, v, rows, cache, a))
+        return e;
+    if (a.M == 0 || a.places == 0)
+        return ok();
+    a.cache = static_cast<char *>(cache);
+    return hip_status(bt::launch_cache_write(a, k, v, (int)shape->type, static_cast<hipStream_t>(stream)),
+                      "bt_cache4_write launch");
+}
+
+bt_status bt_cache4_read(const bt_cache4_rows *shape, const void *cache, const int32_t *rows, void *k, void *v,
+                         void *stream)
+{
+    bt::CacheRows a;
+    if (bt_status e = check_cache4_rows(shape, k, v, rows, cache, a))
+        return e;
+    if (a.M == 0)
+        return ok();
+    a.cache = static_cast<char *>(const_cast<void *>(cache));
+    return hip_status(bt::launch_cache_read(a, k, v, (int)shape->type, static_cast<hipStream_t>(stream)),
+                      "bt_cache4_read launch");
+}
+
+size_t bt_attention4_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                     int64_t max_pages, int64_t page_tokens)
+{
+    bt::Attn4Plan plan;
+    if (check_attention4(tokens, seqs, heads, kv_heads, head_dim, max_pages, page_tokens, plan))
+        return 0;
+    return plan.bytes;
+}
+
+bt_status bt_attention4(const bt_attention4_shape *shape, const void *q, const void *cache, const int32_t *table,
+                        const int32_t *q_start, const int32_t *k_len, void *out, float *lse, void *workspace,
+                        void *stream)
+{
+    if (!shape)
+        return fail(BT_ERR_NULL, "shape is NULL");
+    const bt_attention4_shape &s = *shape;
+    bt::Attn4Plan plan;
+    bt::Attn4Args a{};
+    if (bt_status e = check_attention4(s.tokens, s.seqs, s.heads, s.kv_heads, s.head_dim, s.max_pages, s.page_tokens, plan))
+        return e;
+    if (bt_status e = check_cache4(s.pages, s.page_tokens, s.kv_heads, s.head_dim, a.page_shift))
+        return e;
+    if (!(s.scale > 0.0f) || !(s.scale < 1.0e30f))
+        return fail(BT_ERR_SHAPE, "scale must be finite and positive");
+    if ((s.type != BT_BF16 && s.type != BT_F16) || (s.out_type != s.type && s.out_type != BT_F32))
+        return fail(BT_ERR_UNSUPPORTED, "type %d with out_type %d", s.type, s.out_type);
+    if (s.tokens == 0 || s.seqs == 0)
+        return ok();
+    const bool keys = s.pages > 0 && s.max_pages > 0;
+    if (!q || !out || !q_start || !k_len || (keys && (!cache || !table)) || (plan.bytes > 0 && !workspace))
+        return fail(BT_ERR_NULL, "NULL q, cache, table, q_start, k_len, out or workspace");
+    if (s.q_row < 0 || s.q_row % 8 || s.q_head < 0 || s.q_head % 8)
+        return fail(BT_ERR_ALIGN, "strides of q must be multiples of 8");
+    if (!aligned(q, 16) || !aligned(cache, 16))
+        return fail(BT_ERR_ALIGN, "q and the cache must be 16-byte aligned");
+    if (s.out_row < 0 || s.out_head < 0 || s.out_row % 4 || s.out_head % 4 || !aligned(out, 4 * type_size(s.out_type)))
+        return fail(BT_ERR_ALIGN, "out and its strides must be aligned to four elements");
+    if (!aligned(table, 4) || !aligned(q_start, 4) || !aligned(k_len, 4) || !aligned(lse, 4))
+        return fail(BT_ERR_ALIGN, "table, q_start, k_len and lse must be 4-byte aligned");
+    if (keys && s.table_row < s.max_pages)
+        return fail(BT_ERR_SHAPE, "rows of the table %lld apart, but %lld long", (long long)s.table_row,
+                    (long long)s.max_pages);
+    if (plan.bytes > 0 && !aligned(workspace, 256))
+        return fail(BT_ERR_ALIGN, "workspace must be 256-byte aligned");
+    a.q = q;
+    a.q_start = q_start;
+    a.k_len = k_len;
+    a.out = out;
+    a.lse = lse;
+    a.ws_o = static_cast<float *>(workspace);
+    a.q_row = s.q_row;
+    a.q_head = s.q_head;
+    a.o_row = s.out_row;
+    a.o_head = s.out_head;
+    a.T = (int)s.tokens;
+    a.S = keys ? (int)(s.max_pages * s.page_tokens) : 0;
+    a.B = (int)s.seqs;
+    a.Hq = (int)s.heads;
+    a.Hkv = (int)s.kv_heads;
+    a.G = (int)(s.heads / s.kv_heads);
+    a.D = (int)s.head_dim;
+    a.scale_log2 = (float)(s.scale * M_LOG2E);
+    a.causal = s.causal != 0;
+    a.cache = static_cast<const char *>(cache);
+    a.table = table;
+    a.table_row = s.table_row;
+    a.pages = (int)s.pages;
+    a.head_bytes = (int)bt::cache_head_bytes(s.page_tokens, s.head_dim);
+    a.page_bytes = s.kv_heads * (int64_t)a.head_bytes;
+    a.groups = bt::cache_groups(s.head_dim);
+    return hip_status(bt::launch_attention4(a, plan, s.type, s.out_type, static_cast<hipStream_t>(stream)),
+                      "bt_attention4 launch");
+}
+
+size_t bt_pages_workspace_bytes(int64_t seqs, int64_t max_pages, int64_t pages)
+{
+    const bt_pages_shape shape = {seqs, max_pages, pages, 1, 0, 0, 0, 0};
+    bt::PagesArgs a;
+    if (check_pages(&shape, false, a))
+        return 0;
+    return bt::pages_workspace_bytes(seqs, max_pages, pages);
+}
+
+bt_status bt_pages_grow(const bt_pages_shape *shape, int32_t *table, int32_t *length, int32_t *refs, int32_t *first,
+                        const int32_t *q_start, void *pool, int32_t *rows, int32_t *positions, int32_t *granted,
+                        void *workspace, void *stream)
+{
+    bt::PagesArgs a;
+    if (bt_status e = check_pages(shape, true, a))
+        return e;
+    if (a.B == 0 && a.T == 0)
+        return ok();
+    if (bt_status e = check_pages_arrays(table, length, refs, first, q_start, workspace))
+        return e;
+    if (bt_status e = check_pool(a, pool))
+        return e;
+    if ((a.B > 0 && !granted) || (a.T > 0 && (!rows || !positions)))
+        return fail(BT_ERR_NULL, "NULL rows, positions or granted");
+    if (!aligned(rows, 4) || !aligned(positions, 4) || !aligned(granted, 4))
+        return fail(BT_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
+    a.table = table;
+    a.length = length;
+    a.refs = refs;
+    a.first = first;
+    a.q_start = q_start;
+    a.pool = static_cast<char *>(pool);
+    a.rows = rows;
+    a.positions = positions;
+    a.granted = granted;
+    a.ws = static_cast<int *>(workspace);
+    return hip_status(bt::launch_pages_grow(a, static_cast<hipStream_t>(stream)), "bt_pages_grow launch");
+}
+
+bt_status bt_pages_fork(const bt_pages_shape *shape, int32_t *table, int32_t *length, int32_t *refs, int32_t *first,
+                        const int32_t *parent, void *workspace, void *stream)
+{
+    bt::PagesArgs a;
+    if (bt_status e = check_pages(shape, false, a))
+        return e;
+    if (a.B == 0)
+        return ok();
+    if (bt_status e = check_pages_arrays(table, length, refs, first, parent, workspace))
+        return e;
+    a.table = table;
+    a.length = length;
+    a.refs = refs;
+    a.first = first;
+    a.parent = parent;
+    a.ws = static_cast<int *>(workspace);
+    return hip_status(bt::launch_pages_fork(a, static_cast<hipStream_t>(stream)), "bt_pages_fork launch");
+}
+
+bt_status bt_pages_compact(const bt_pages_shape *shape, int32_t *table, int32_t *refs, int32_t *first, void *pool,
+                           void *workspace, void *stream)
+{
+    bt::PagesArgs a;
+    if (bt_status e = check_pages(shape, true, a))
+        return e;
+    if (a.P == 0)
+        return ok();
+    if (bt_status e = check_pages_arrays(table, table, refs, first, table, workspace))
+        return e;
+    if (bt_status e = check_pool(a, pool))
+        return e;
+    a.table = table;
+    a.refs = refs;
+    a.first = first;
+    a.pool = static_cast<char *>(pool);
+    a.ws = static_cast<int *>(workspace);
+    return hip_status(bt::launch_pages_compact(a, static_cast<hipStream_t>(stream)), "bt_pages_compact launch");
+}
+
+bt_status bt_pages_copy(const bt_pages_shape *shape, void *pool, const int32_t *src, const int32_t *dst, int64_t n,
+                        void *stream)
+{
+    bt::PagesArgs a;
+    if (bt_status e = check_pages(shape, true, a))
+        return e;
+    if (n < 0 || n > 1 << 24)
+        return fail(BT_ERR_SHAPE, "n = %lld outside [0, 2^24]", (long long)n);
+    if (n == 0 || a.P == 0 || a.layers == 0)
+        return ok();
+    if (!src || !dst)
+        return fail(BT_ERR_NULL, "NULL src or dst");
+    if (!aligned(src, 4) || !aligned(dst, 4))
+        return fail(BT_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
+    if (bt_status e = check_pool(a, pool))
+        return e;
+    a.pool = static_cast<char *>(pool);
+    return hip_status(bt::launch_pages_copy(a, src, dst, n, static_cast<hipStream_t>(stream)), "bt_pages_copy launch");
+}
+
+size_t bt_int8_weight_bytes(int64_t N, int64_t K)
+{
+    return N <= 0 || K <= 0 || check_nk(N, K) ? 0 : bt::int8_weight_bytes(N, K);
+}
+
+size_t bt_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || M > BT_MAX_DIM || N <= 0 || K <= 0 || check_nk(N, K) || M * N > BT_MAX_MN)
+        return 0;
+    return bt::int8_workspace_bytes(M, N, K);
+}
+
+bt_status bt_int8_pack(const int8_t *W, int64_t ldw, int64_t N, int64_t K, void *Wp, void *stream)
+{
+    if (bt_status e = check_nk(N, K))
+        return e;
+    if (ldw < K)
+        return fail(BT_ERR_SHAPE, "rows %lld bytes apart, but %lld long", (long long)ldw, (long long)K);
+    if (N == 0 || K == 0)
+        return ok();
+    if (!W || !Wp)
+        return fail(BT_ERR_NULL, "W or Wp is NULL");
+    if (!aligned(Wp, 16))
+        return fail(BT_ERR_ALIGN, "Wp must be 16-byte aligned");
+    return hip_status(bt::launch_int8_pack(W, ldw, N, K, Wp, static_cast<hipStream_t>(stream)), "bt_int8_pack launch");
+}
+
+bt_status bt_int8_gemm(const void *Wp, const float *w_scale, const int8_t *Xq, const float *x_scale, int64_t M,
+                       int64_t N, int64_t K, const float *bias, void *Y, int32_t y_type, int32_t *acc,
+                       void *workspace, void *stream)
+{
+    if (M < 0 || M > BT_MAX_DIM)
+        return fail(BT_ERR_SHAPE, "M = %lld outside [0, 2^23]", (long long)M);
+    if (bt_status e = check_nk(N, K))
+        return e;
+    if (M * N > BT_MAX_MN)
+        return fail(BT_ERR_SHAPE, "M * N = %lld above 2^36", (long long)(M * N));
+    if (!known_type(y_type))
+        return fail(BT_ERR_UNSUPPORTED, "y_type %d", y_type);
+    if (M == 0 || N == 0)
+        return ok();
+    if (!Y && !acc)
+        return fail(BT_ERR_NULL, "Y and acc are both NULL");
+    const size_t need = K > 0 ? bt::int8_workspace_bytes(M, N, K) : 0;
+    if (!w_scale || !x_scale || (K > 0 && (!Wp || !Xq)) || (need && !workspace))
+        return fail(BT_ERR_NULL, "NULL input pointer or workspace");
+    if (!aligned(Wp, 16) || !aligned(Xq, 16))
+        return fail(BT_ERR_ALIGN, "Wp and Xq must be 16-byte aligned");
+    if (!aligned(w_scale, 4) || !aligned(x_scale, 4) || !aligned(bias, 4) || !aligned(acc, 4) ||
+        !aligned(Y, type_size(y_type)))
+        return fail(BT_ERR_ALIGN, "scales, bias and outputs must be aligned to their element");
+    if (need && !aligned(workspace, 256))
+        return fail(BT_ERR_ALIGN, "workspace must be 256-byte aligned");
+    return hip_status(bt::launch_int8(Wp, w_scale, Xq, x_scale, M, N, K, bias, Y, y_type, acc, workspace,
+                                      static_cast<hipStream_t>(stream)),
+                      "bt_int8_gemm launch");
 }
 
 const char *bt_status_str(bt_status s)

@@ -1,0 +1,508 @@
+// Attention over a cache held in 4 bits, in pages (bt_attention4): single tokens, drafts of a few tokens and
+// prompts, whole or continued, whose keys and values lie in the cache (csrc/cache4.h).
+//
+//   s[r, j] = scale * q_r . K_j over the keys j that row r sees;  out_r = sum_j softmax(s)_j V_j;
+//   lse_r = ln sum_j exp(s[r, j])      (no key seen: out 0, lse -inf)
+//
+// One pass over the keys with a running maximum and sum per row, rows of (token, head of the group), transposed
+// products, items, slices and their joining as in csrc/attention.hip.
+//
+// Types. A code with its scale is exactly a bf16, one conversion for two of them, so both products run on bf16
+// operands: K is exact, a bf16 query is exact, an fp16 query is two bf16 (its 11 bits are 8 and 3) and two products.
+// Probabilities are carried as a bf16 and its rest (16 bits), and a second rest for fp32 outputs (24 bits).
+//
+// Order of the values. A product's order of summation is free as long as both operands have it. Lane (r, g) of an S^T
+// operand takes a key's group g, 16 bytes and one scale in one load each, as its part of the four steps of
+// 128 values; the query operands are loaded to match.
+//
+// NaN. A group of K that holds a NaN makes the scores of its key NaN, which counts in rows that see it only (unseen
+// scores are replaced). A group of V that holds one goes into the product as zeros, and rows that see its key get NaN
+// in the group's values directly. Finite groups are finite in bf16, so there are no infinities to meet.
+#include "attention_items.h"
+#include "cache4.h"
+
+namespace bt {
+namespace {
+
+using V8 = bf16x8;
+
+// A wave's view of a sequence's row of the table: 64 entries of it in the lanes.
+struct PageWindow {
+    const int *row;
+    int used;   // entries that hold keys
+    int first, mine;
+};
+
+__device__ inline PageWindow page_window(const Attn4Args &a, const Seq &s)
+{
+    PageWindow w;
+    w.row = a.table + (int64_t)s.k0 * a.table_row;
+    w.used = (int)(((int64_t)s.nk + (1 << a.page_shift) - 1) >> a.page_shift);
+    w.first = -64;
+    w.mine = -1;
+    return w;
+}
+
+// Sixteen keys of one page from `key` (uniform): a buffer over their head's part of the page, of no bytes where there
+// is no such page, and the tile's number in it.
+struct Tile4 {
+    __amdgpu_buffer_rsrc_t from;
+    int tile;
+    bool there;
+};
+
+__device__ inline Tile4 find_tile(const Attn4Args &a, PageWindow &w, int head, int key)
+{
+    const int p = key >> a.page_shift;
+    int page = -1;
+    if (p < w.used) {
+        if ((uint32_t)(p - w.first) >= 64u) {
+            const int at = p + (int)(threadIdx.x & 63);
+            w.first = p;
+            w.mine = at < w.used ? w.row[at] : -1;
+        }
+        page = __builtin_amdgcn_readlane(w.mine, p - w.first);
+    }
+    Tile4 t;
+    t.there = page >= 0 && page < a.pages;
+    t.tile = (key & ((1 << a.page_shift) - 1)) / kCacheTile;
+    const char *base = a.cache + (t.there ? page * a.page_bytes : 0) + (int64_t)head * a.head_bytes;
+    t.from = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), (short)0, t.there ? a.head_bytes : 0,
+                                               kBufferWord3);
+    return t;
+}
+
+// What lane (r, g) holds of sixteen keys: key r's codes of DP / 4 values (from 32 g on; of 16 from 16 g on for
+// DP == 64; for DP == 256 also from 128 + 32 g on), and their scale bytes.
+template <int DP>
+struct Codes4 {
+    static constexpr int NB = DP > 128 ? 2 : 1, W = DP == 64 ? 2 : 4;  // pieces, words of a piece
+    uint32_t k[NB][W], v[NB][W], ks[NB], vs[NB];
+};
+
+template <int DP>
+struct Places4 {
+    uint32_t code[Codes4<DP>::NB], scale[Codes4<DP>::NB];  // in the tile
+};
+
+template <int DP>
+__device__ inline Places4<DP> lane_places(const Attn4Args &a)
+{
+    const int r = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    Places4<DP> p;
+#pragma unroll
+    for (int n = 0; n < Codes4<DP>::NB; ++n) {
+        const int group = DP == 64 ? g >> 1 : g + 4 * n;
+        const bool in = group < a.groups;
+        p.code[n] = in ? (uint32_t)((group * kCacheTile + r) * 16 + (DP == 64 ? 8 * (g & 1) : 0)) : kOutside;
+        p.scale[n] = in ? (uint32_t)(group * kCacheTile + r) : kOutside;
+    }
+    return p;
+}
+
+// One piece of codes of a tile, K's or V's.
+template <int W>
+__device__ inline void load_codes(const __amdgpu_buffer_rsrc_t &from, uint32_t at, uint32_t (&x)[W])
+{
+    if constexpr (W == 4) {
+        const u32x4 y = __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = y[j];
+    } else {
+        const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, 0);
+        x[0] = y[0];
+        x[1] = y[1];
+    }
+}
+
+template <int DP>
+__device__ inline void load_keys(const Attn4Args &a, const Places4<DP> &p, const Tile4 &t, Codes4<DP> &x)
+{
+    const uint32_t plane = (uint32_t)a.groups << a.page_shift, at = (uint32_t)(t.tile * a.groups * kCacheTile);
+#pragma unroll
+    for (int n = 0; n < Codes4<DP>::NB; ++n) {
+        load_codes(t.from, p.code[n] + 16 * at, x.k[n]);
+        x.ks[n] = __builtin_amdgcn_raw_buffer_load_b8(t.from, p.scale[n] + 32 * plane + at, 0, 0);
+    }
+}
+
+template <int DP>
+__device__ inline void load_values(const Attn4Args &a, const Places4<DP> &p, const Tile4 &t, Codes4<DP> &x)
+{
+    const uint32_t plane = (uint32_t)a.groups << a.page_shift, at = (uint32_t)(t.tile * a.groups * kCacheTile);
+#pragma unroll
+    for (int n = 0; n < Codes4<DP>::NB; ++n) {
+        load_codes(t.from, p.code[n] + 16 * (plane + at), x.v[n]);
+        x.vs[n] = __builtin_amdgcn_raw_buffer_load_b8(t.from, p.scale[n] + 33 * plane + at, 0, 0);
+    }
+}
+
+// First value of step st of lane group g in the order of the S^T operands (see Codes4).
+template <int DP>
+__device__ inline int step_value(int g, int st)
+{
+    return DP == 64 ? 16 * g + 8 * st : 128 * (st / 4) + 32 * g + 8 * (st % 4);
+}
+
+// Eight query values as bf16, or as bf16 and their rests.
+template <typename E>
+__device__ inline void split_query(u32x4 x, V8 &hi, V8 &lo)
+{
+    if constexpr (sizeof(E) == 2 && Elem<E>::kRaised == 0.0f) {  // bf16
+        hi = __builtin_bit_cast(V8, x);
+        lo = hi;
+    } else {
+        const typename Elem<E>::v8 h = __builtin_bit_cast(typename Elem<E>::v8, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            hi[j] = (bf16_t)(float)h[j];
+            lo[j] = (bf16_t)((float)h[j] - (float)hi[j]);
+        }
+    }
+}
+
+template <typename E>
+constexpr bool kSplitQuery = sizeof(typename Elem<E>::v8) == 16 && Elem<E>::kRaised != 0.0f;
+
+// The keys r < n of sixteen, as bits.
+__device__ inline uint32_t first_bits(int n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
+
+// -------------------------------------------------------------------- few-rows kernel
+//
+// attn4_few: 16 rows (a decode step's heads of one group, a short draft) against a slice of their keys; bound by
+// the cache's bytes. Each of four waves takes every fourth block of 32 keys on its own. K's codes become S^T operands
+// in their registers; V's go as bf16 through a private piece of LDS for the transposing read. The next block's
+// loads are issued before this block is used; the four partial results are joined at the end.
+
+constexpr int kFewRows = 16, kFewKeys = 32, kFewWaves = 4;
+
+template <typename E, int DP, bool WIDE>
+__device__ __forceinline__ void attn4_few(const Attn4Args &a, int block, char *buf,
+                                          float (&stat)[kFewWaves][3][kFewRows])
+{
+    constexpr int NS = DP / 32, ND = DP / 16;
+    constexpr int kVBytes = kFewKeys * DP * 2;
+    using Codes = Codes4<DP>;
+    static_assert(kVBytes >= kFewRows * DP * 4, "the waves' partial outputs reuse the V blocks");
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int id = block / a.Hkv, head = block % a.Hkv;
+    Item it;
+    if (!find_item(a, kFewRows, id, false, it))
+        return;
+    const Seq s = it.s;
+    const int rows = s.nq * a.G;
+    const int row = it.tile * kFewRows + col;
+    const int token = row / a.G, qh = head * a.G + row % a.G;
+    const bool live = row < rows;
+    const int limit = live ? row_limit(a, s, token) : 0;
+    const int first = it.tile * kFewRows, last = min(rows, first + kFewRows) - 1;
+    const int lo = (int)min((int64_t)it.piece * it.unit * kUnit, (int64_t)s.nk);
+    const int hi = min((int)min((int64_t)(it.piece + 1) * it.unit * kUnit, (int64_t)s.nk), row_limit(a, s, last / a.G));
+    const int wfull = row_limit(a, s, first / a.G);
+
+    V8 qf[NS], ql[NS];
+    {
+        const char *p = static_cast<const char *>(a.q) + 2 * ((int64_t)(s.q0 + token) * a.q_row + (int64_t)qh * a.q_head);
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            u32x4 x = {0, 0, 0, 0};
+            const int d = step_value<DP>(g, st);
+            if (live && d < a.D)
+                x = *reinterpret_cast<const u32x4 *>(p + 2 * d);
+            split_query<E>(x, qf[st], ql[st]);
+        }
+    }
+    const Places4<DP> places = lane_places<DP>(a);
+    PageWindow window = page_window(a, s);
+    struct Block {
+        Codes t[2];
+        bool there[2];
+    };
+    auto fetch = [&](int key, Block &x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const Tile4 t = find_tile(a, window, head, key + 16 * b);
+            x.there[b] = t.there;
+            load_keys<DP>(a, places, t, x.t[b]);
+            load_values<DP>(a, places, t, x.t[b]);
+        }
+    };
+
+    f32x4 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+        o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    const float c2 = a.scale_log2;
+    char *vb = buf + wave * kVBytes;
+    const int tr_row = 4 * g + (lane & 15) / 4, tr_col = (lane & 3) * 8;
+    auto v_frag = [&](int dt) {
+        u32x4 x;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+            const int r = 16 * jj + tr_row;
+            const int byte = dt * 32 + tr_col;
+            const char *p = vb + r * (DP * 2) + (((byte >> 4) ^ swizzle<DP>(r)) << 4) + (byte & 15);
+            const u32x2 half = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+            x[2 * jj] = half[0];
+            x[2 * jj + 1] = half[1];
+        }
+        return __builtin_bit_cast(V8, x);
+    };
+    auto step = [&](int key, Block &x) __attribute__((always_inline)) {
+        f32x4 sc[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            sc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < NS; ++st) {
+                const int n = st / Codes::W;
+                const V8 k = cache_values(x.t[b].k[n][st % Codes::W], cache_scale(x.t[b].ks[n]));
+                sc[b] = Elem<bf16_t>::mma16(k, qf[st], sc[b]);
+                if constexpr (kSplitQuery<E>)
+                    sc[b] = Elem<bf16_t>::mma16(k, ql[st], sc[b]);
+            }
+        }
+        // register i of block b: key + 16 b + 4 g + i
+        if (key + kFewKeys > wfull || !x.there[0] || !x.there[1]) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (key + 16 * b + 4 * g + i >= limit || !x.there[b])
+                        sc[b][i] = -INFINITY;
+        }
+        // V to LDS. Keys past the sequence's end hold anything: zeros. Groups with NaNs: zeros, and remembered.
+        uint64_t nan[2][Codes::NB], any = 0;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const bool past = key + 16 * b + col >= s.nk;
+            const int r = 16 * b + col;
+#pragma unroll
+            for (int n = 0; n < Codes::NB; ++n) {
+                const bool bad = x.t[b].vs[n] > kCacheNaN;
+                nan[b][n] = __ballot(bad && !past);
+                any |= nan[b][n];
+                const bool none = past || bad;
+                const float f = cache_scale(none ? 0u : x.t[b].vs[n]);
+#pragma unroll
+                for (int w = 0; w < Codes::W; ++w) {
+                    const int c = Codes::W * (g + 4 * n) + w;
+                    const V8 y = cache_values(none ? 0u : x.t[b].v[n][w], f);
+                    *reinterpret_cast<u32x4 *>(vb + r * (DP * 2) + ((c ^ swizzle<DP>(r)) << 4)) = __builtin_bit_cast(u32x4, y);
+                }
+            }
+        }
+        float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                         fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+        mx = across_quarters(mx, [](float x, float y) { return fmaxf(x, y); });
+        if (__any((mx - m) * c2 > Elem<bf16_t>::kRise || (m == -INFINITY && mx > -INFINITY))) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.f : exp2_fast((m - mn) * c2);
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                o[d] *= f;
+            m = mn;
+        }
+        const float ref = m == -INFINITY ? 0.f : m * c2;
+        constexpr int PARTS = WIDE ? 3 : 2;
+        u32x4 pf[PARTS];
+        float lb = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sc[b][i] = exp2_fast(__builtin_fmaf(sc[b][i], c2, -ref));
+                lb += sc[b][i];
+            }
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    pf[p][2 * b + j] = pack2<bf16_t>(sc[b][2 * j], sc[b][2 * j + 1]);
+                    const f32x2 back = unpack2<bf16_t>(pf[p][2 * b + j]);
+                    sc[b][2 * j] -= back[0];
+                    sc[b][2 * j + 1] -= back[1];
+                }
+        }
+        l += lb;
+        // This wave's LDS writes before its reads: LDS operations of a wave complete in order, so
+        // only the compiler has to keep them so.
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            const V8 v = v_frag(d);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+                o[d] = Elem<bf16_t>::mma16(v, __builtin_bit_cast(V8, pf[p]), o[d]);
+        }
+        asm volatile("" ::: "memory");
+        if (__builtin_expect(any != 0, 0)) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                // 16 values of group d / 2, in piece n of the lanes of quarter q
+                const int n = DP > 128 ? d / 8 : 0, q = DP == 64 ? d & 2 : d / 2 % 4;
+                uint32_t seen = 0;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (x.there[b])
+                        seen |= (uint32_t)(nan[b][n] >> (16 * q)) & first_bits(limit - key - 16 * b);
+                if (seen)
+                    o[d] = f32x4{NAN, NAN, NAN, NAN};
+            }
+        }
+    };
+
+    constexpr int kStride = kFewWaves * kFewKeys;
+    const int k0 = lo + wave * kFewKeys;
+    if (k0 < hi) {
+        Block x, y;
+        fetch(k0, x);
+        for (int key = k0; key < hi; key += 2 * kStride) {
+            fetch(key + kStride, y);
+            step(key, x);
+            if (key + kStride >= hi)
+                break;
+            fetch(key + 2 * kStride, x);
+            step(key + kStride, y);
+        }
+    }
+    // join the four waves: common maximum, then the sums
+    l = across_quarters(l, [](float x, float y) { return x + y; });
+    if (g == 0) {
+        stat[wave][0][col] = m;
+        stat[wave][1][col] = l;
+    }
+    __syncthreads();
+    float mall = stat[0][0][col];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w)
+        mall = fmaxf(mall, stat[w][0][col]);
+    float lall = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+        const float mw = stat[w][0][col];
+        lall += mw == -INFINITY ? stat[w][1][col] : stat[w][1][col] * exp2_fast((mw - mall) * c2);  // 0, or NaN scores
+    }
+    const float inv = lall > 0.f ? 1.f / lall : (lall == 0.f ? 0.f : lall);
+    const float f = m == -INFINITY ? inv : exp2_fast((m - mall) * c2) * inv;
+    const float lse = lall == 0.f ? -INFINITY : mall * c2 * kLn2 + logf(lall);
+    // wave's O^T to LDS as [row][D]: 4 values of row col per register group
+    float *mine = reinterpret_cast<float *>(vb);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        const f32x4 x = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o[d] * f;
+        *reinterpret_cast<f32x4 *>(mine + col * DP + ((4 * d + g) ^ (col & 7)) * 4) = x;
+    }
+    __syncthreads();
+    const bool part = it.pieces > 1;
+    for (int e = threadIdx.x; e < kFewRows * (DP / 4); e += 256) {
+        const int r = e / (DP / 4), c = e % (DP / 4);
+        const int rr = it.tile * kFewRows + r;
+        if (rr >= rows || c * 4 >= a.D)
+            continue;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w)
+            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(buf + w * kVBytes) + r * DP +
+                                                    (c ^ (r & 7)) * 4);
+        const float x[4] = {sum[0], sum[1], sum[2], sum[3]};
+        if (part) {
+            store4(a.ws_o + ((int64_t)block * kFewRows + r) * a.D + 4 * c, x);
+        } else {
+            const int64_t at = (int64_t)(s.q0 + rr / a.G) * a.o_row + (int64_t)(head * a.G + rr % a.G) * a.o_head + 4 * c;
+            if constexpr (WIDE)
+                store4(static_cast<float *>(a.out) + at, x);
+            else
+                store4(static_cast<E *>(a.out) + at, x);
+        }
+    }
+    if (wave == 0 && g == 0 && live) {
+        if (part)
+            a.ws_l[(int64_t)block * kFewRows + col] = lse;
+        else if (a.lse)
+            a.lse[(int64_t)(s.q0 + token) * a.Hq + qh] = lse;
+    }
+}
+
+template <typename E, int DP, bool WIDE>
+__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn4_few(Attn4Args a)
+{
+    __shared__ __attribute__((aligned(1024))) char buf[kFewWaves * kFewKeys * DP * 2];
+    __shared__ float stat[kFewWaves][3][kFewRows];
+    attn4_few<E, DP, WIDE>(a, blockIdx.x, buf, stat);
+}
+
+// --------------------------------------------------------------------------------- plans
+
+template <typename E, int DP, bool WIDE>
+hipError_t run_kind4(const Attn4Args &a, const Attn4Plan &p, hipStream_t s)
+{
+    const unsigned grid = (unsigned)(p.main.items * a.Hkv);
+    k_attn4_few<E, DP, WIDE><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename E, bool WIDE>
+hipError_t run_dim4(const Attn4Args &a, const Attn4Plan &p, hipStream_t s)
+{
+    if (a.D <= 64)
+        return run_kind4<E, 64, WIDE>(a, p, s);
+    if (a.D <= 128)
+        return run_kind4<E, 128, WIDE>(a, p, s);
+    return run_kind4<E, 256, WIDE>(a, p, s);
+}
+
+template <typename TO>
+hipError_t run_combine4(const Attn4Args &a, const Attn4Plan &p, hipStream_t s)
+{
+    const dim3 grid((unsigned)(p.main.tiles * a.Hkv), (unsigned)((p.main.bm + kJoinGroups - 1) / kJoinGroups));
+    k_attn_combine<TO><<<grid, 32 * kJoinGroups, 0, s>>>(a, Attn4Args{}, p.main.bm, p.main.bm);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t most_keys)
+{
+    Attn4Plan plan{};
+    AttnPart &p = plan.main;
+    const int64_t rows = T * (Hq / Hkv), seqs = B < T ? B : T;
+    p.bm = kFewRows;
+    p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
+    p.target = most_keys <= 512 ? 0 : (2048 + Hkv - 1) / Hkv;
+    p.min_units = 4;
+    const int64_t most = ((most_keys + kUnit - 1) / kUnit + p.min_units - 1) / p.min_units;
+    p.items = p.tiles + (p.target ? p.target + 8 : 0);
+    if (p.target && p.tiles * (most > 1 ? most : 1) < p.items)
+        p.items = p.tiles * (most > 1 ? most : 1);
+    const int64_t slots = p.target ? p.items * Hkv * p.bm : 0;
+    p.l_off = round_up(slots * D * 4, 256);
+    plan.bytes = (size_t)(p.l_off + round_up(slots * 4, 256));
+    return plan;
+}
+
+hipError_t launch_attention4(const Attn4Args &args, const Attn4Plan &p, int type, int out_type, hipStream_t s)
+{
+    Attn4Args a = args;
+    char *ws = reinterpret_cast<char *>(args.ws_o);
+    a.target = (int)p.main.target;
+    a.items = (int)p.main.items;
+    a.min_units = p.main.min_units;
+    a.ws_o = reinterpret_cast<float *>(ws);
+    a.ws_l = reinterpret_cast<float *>(ws + p.main.l_off);
+    const bool wide = out_type == kF32;
+    hipError_t e = type == kBF16 ? (wide ? run_dim4<bf16_t, true>(a, p, s) : run_dim4<bf16_t, false>(a, p, s))
+                                 : (wide ? run_dim4<f16_t, true>(a, p, s) : run_dim4<f16_t, false>(a, p, s));
+    if (e != hipSuccess || !p.main.target)
+        return e;
+    return wide            ? run_combine4<float>(a, p, s)
+           : type == kBF16 ? run_combine4<bf16_t>(a, p, s)
+                           : run_combine4<f16_t>(a, p, s);
+}
+
+}  // namespace bt

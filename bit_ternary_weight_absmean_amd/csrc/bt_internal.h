@@ -118,6 +118,14 @@ hipError_t launch_lora(const void *A, const void *B, int w_type, const float *sc
                        int64_t R, const RowGroups &groups, const int32_t *adapter, const float *X, const float *Y0,
                        int64_t M, int64_t N, int64_t K, float *Y, void *workspace, hipStream_t s);
 
+// Products of int8 tokens and packed int8 weights.
+size_t int8_weight_bytes(int64_t N, int64_t K);
+size_t int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_pack(const int8_t *W, int64_t ld, int64_t N, int64_t K, void *Wp, hipStream_t s);
+hipError_t launch_int8(const void *Wp, const float *w_scale, const int8_t *X, const float *x_scale, int64_t M,
+                       int64_t N, int64_t K, const float *bias, void *Y, int y_type, int32_t *acc, void *workspace,
+                       hipStream_t s);
+
 // Names of the kernel instances the launchers pick for a call (host-only, snprintf
 // semantics; 16-byte aligned activation rows assumed), for bt_kernel_plan.
 int plan_quant_act(int64_t M, int64_t K, char *buf, size_t len);

@@ -510,6 +510,160 @@ bt_status bt_attention(const bt_attention_shape *shape, const void *q, const voi
                        const void *prefix_k, const void *prefix_v, void *out, float *lse,
                        void *workspace, void *stream);
 
+/*
+ * The 4-bit cache: keys and values of tokens in pages. A page is page_tokens places (a power of two, 16 to 1024);
+ * place `row` of a cache of `pages` pages is place row % page_tokens of page row / page_tokens. 32 values of one
+ * token and key head (a group; the last one of a head is filled up with zeros) share a scale:
+ *   e = the smallest integer with max|x| <= 7 * 2^e, at least -127 and at most 125; scale byte e + 127;
+ *   code = the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0 to 7; + 8: negative) to x / 2^e, of two equally near
+ *   ones that with the even number; 6 beyond. A group with an infinity or NaN has scale byte 255.
+ *   Scale bytes above 252 read as NaN (no write of finite values makes one).
+ * Layout, with G = ceil(head_dim / 32): head h's part of a page starts at byte h * page_tokens * G * 34 and holds
+ * K codes (16 * page_tokens * G bytes), V codes (the same), K scales (page_tokens * G bytes), V scales. The chunk of
+ * place t and group g is number ((t / 16) * G + g) * 16 + t % 16, 16 bytes of codes (value d of the group in byte
+ * d / 2, the lower four bits first) and one byte of scales. So a page takes kv_heads * page_tokens * G * 34 bytes.
+ * kv_heads * G <= 65536, head_dim a multiple of 8 up to BT_ATTENTION_MAX_HEAD_DIM, pages * page_tokens <= 2^30.
+ */
+size_t bt_cache4_page_bytes(int64_t page_tokens, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * bt_cache4_write -- tokens' keys and values into places of the cache; bt_cache4_read -- the values of places.
+ *   cache     pages * bt_cache4_page_bytes(...) bytes, 16-byte aligned.
+ *   rows      [tokens] int32 on the device: the place of each token. Tokens with a place outside the cache write
+ *             nothing, and read zeros. Two tokens of one write must not name the same place (what it then holds is
+ *             unspecified); other places stay as they are.
+ *   k, v      value d of head h of token m at m * x_row + h * x_head + d (strides in elements) of `type` (BT_F32,
+ *             BT_BF16 or BT_F16). Arrays and strides are aligned to four elements. As outputs of the read they must not
+ *             overlap each other. Every finite value of the cache is exactly a bf16.
+ */
+typedef struct {
+    int64_t pages, page_tokens, kv_heads, head_dim, tokens;
+    int64_t k_row, k_head, v_row, v_head;
+    int64_t type;
+} bt_cache4_rows;
+bt_status bt_cache4_write(const bt_cache4_rows *shape, const void *k, const void *v, const int32_t *rows, void *cache,
+                          void *stream);
+bt_status bt_cache4_read(const bt_cache4_rows *shape, const void *cache, const int32_t *rows, void *k, void *v,
+                         void *stream);
+
+/*
+ * bt_attention4 -- bt_attention over a 4-bit cache: sequence b's queries are rows q_start[b] .. q_start[b+1] - 1 of q
+ * (they must not overlap; rows of no sequence are not written), its keys the first k_len[b] tokens in the pages
+ * table[b * table_row + 0, 1, ...] (k_len is cut to max_pages * page_tokens). causal, out and lse as there.
+ *   table     [seqs, max_pages] int32 on the device, rows table_row elements apart. Entries behind a sequence's last
+ *             key are not read. The keys of an entry outside [0, pages) count as not seen.
+ * type: BT_BF16 or BT_F16, of q; out_type: the same or BT_F32. Keys and values are exact in the products, scores,
+ * statistics and sums fp32; probabilities are carried in 16 bits (in 8, the precision of a bf16, for more than 16
+ * rows of a sequence and key head with bf16 outputs). Results do not depend on timing. What a query does not see
+ * does not reach it, NaNs included; a NaN group of V that it sees is NaN in its output's values of that group, one of K
+ * makes the whole row NaN.
+ * q: 16-byte aligned with strides multiples of 8; out: aligned to four elements. tokens <= BT_MAX_DIM; tokens *
+ * heads and max_pages * page_tokens at most BT_ATTENTION_MAX_KEYS; scale finite and positive.
+ *   workspace bt_attention4_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim, max_pages, page_tokens) bytes of
+ *             device scratch, 256-byte aligned, or NULL when that is 0; contents on entry are ignored. Calls
+ *             sharing one must not overlap.
+ */
+typedef struct {
+    int64_t tokens, seqs, max_pages, table_row;
+    int64_t pages, page_tokens, heads, kv_heads, head_dim;
+    int32_t type, out_type, causal;
+    float scale;
+    int64_t q_row, q_head, out_row, out_head;
+} bt_attention4_shape;
+size_t bt_attention4_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                     int64_t max_pages, int64_t page_tokens);
+bt_status bt_attention4(const bt_attention4_shape *shape, const void *q, const void *cache, const int32_t *table,
+                        const int32_t *q_start, const int32_t *k_len, void *out, float *lse, void *workspace,
+                        void *stream);
+
+/*
+ * The pages of a cache: which sequence holds which, all of it on the device.
+ *   table     [seqs, max_pages] int32: the pages of each sequence in order, ceil(length / page_tokens) of them; -1
+ *             behind.   length [seqs] int32, in tokens.
+ *   refs      [pages] int32: how many entries of the table hold the page; 0: it is free.
+ *   first     [1] int32: no page below it is free. 0 is always right (and has to be set when refs is changed by
+ *             other means); the calls keep it up to date.
+ *   pool      `layers` arrays of `pages` pages of page_bytes, layer_stride bytes apart (0 layers: nothing is copied
+ *             and pool may be NULL). 16-byte aligned; page_bytes and layer_stride multiples of 16.
+ * A sequence's pages have to be inside [0, pages); entries that are not are left alone. page_tokens is a power of two
+ * up to 1024, pages * page_tokens and max_pages * page_tokens are at most 2^30, pages <= 2^24, seqs * (max_pages + 1)
+ * < 2^31, page_bytes <= 2^30. Everything is deterministic.
+ *   workspace bt_pages_workspace_bytes(seqs, max_pages, pages) bytes of device scratch, 16-byte aligned; contents on
+ *             entry are ignored. Calls sharing one must not overlap, and calls on one table are to be in one order.
+ */
+typedef struct {
+    int64_t seqs, max_pages, pages, page_tokens;
+    int64_t layers, layer_stride, page_bytes; /* of the pool */
+    int64_t tokens;                           /* bt_pages_grow: rows of its outputs */
+} bt_pages_shape;
+size_t bt_pages_workspace_bytes(int64_t seqs, int64_t max_pages, int64_t pages);
+
+/*
+ * bt_pages_grow -- room for new tokens: sequence b gains n = q_start[b+1] - q_start[b] of them (q_start [seqs + 1]
+ * int32, not falling, inside [0, tokens]). It needs pages for length + n tokens, and one more where its last page is
+ * partly filled and held more than once: it then gets a copy of that page of its own (in all layers).
+ * Free pages go, lowest index first, to the sequences in order; within one, its copy comes first. A sequence whose
+ * pages are not there any more, or that max_pages has no room for, is refused: it stays as it is. The pages asked for
+ * by a refused sequence stay free, but those behind it that need pages are refused with it.
+ *   rows      [tokens] int32 out: the place of each new token (page * page_tokens + place in the page) for the writes
+ *             of its keys and values; -1 in a refused sequence, and for tokens of none.
+ *   positions [tokens] int32 out: the token's number in its sequence, from 0 (-1 for tokens of none).
+ *   granted   [seqs] int32 out: n, or 0.
+ */
+bt_status bt_pages_grow(const bt_pages_shape *shape, int32_t *table, int32_t *length, int32_t *refs, int32_t *first,
+                        const int32_t *q_start, void *pool, int32_t *rows, int32_t *positions, int32_t *granted,
+                        void *workspace, void *stream);
+
+/*
+ * bt_pages_fork -- all sequences at once become what sequence parent[b] (int32 [seqs], on the device) was: the same
+ * pages, held once more. parent[b] == b keeps b as it is; outside [0, seqs): b holds nothing any more. Pages that no
+ * sequence holds are free. Nothing is copied until a sequence grows.
+ */
+bt_status bt_pages_fork(const bt_pages_shape *shape, int32_t *table, int32_t *length, int32_t *refs, int32_t *first,
+                        const int32_t *parent, void *workspace, void *stream);
+
+/*
+ * bt_pages_compact -- brings the L pages that are in use to the places 0 .. L - 1: the k-th one at or past L goes to
+ * the k-th free place below L. Pool, table and refs follow. What the places past L hold is left as it is.
+ */
+bt_status bt_pages_compact(const bt_pages_shape *shape, int32_t *table, int32_t *refs, int32_t *first, void *pool,
+                           void *workspace, void *stream);
+
+/*
+ * bt_pages_copy -- page dst[i] becomes a copy of page src[i] in all layers, i < n (int32 on the device; pairs with a
+ * number outside [0, pages) are left out). No page may be in dst twice, or in both lists.
+ */
+bt_status bt_pages_copy(const bt_pages_shape *shape, void *pool, const int32_t *src, const int32_t *dst, int64_t n,
+                        void *stream);
+
+/*
+ * bt_int8_gemm -- the product of int8 tokens (bt_quant_act's, or any) and int8 weights with a scale for each token
+ * and each output channel, for the projections that are not ternary:
+ *   acc[m,n] = sum_k W[n,k] X[m,k] (int32, exact);
+ *   Y[m,n] = fp32(acc) * (x_scale[m] * w_scale[n]) + bias[n] in fp32, rounded to y_type.
+ *   Wp        bt_int8_weight_bytes(N, K) bytes from bt_int8_pack, 16-byte aligned.
+ *   w_scale   [N] fp32, x_scale [M] fp32, bias [N] fp32 or NULL.
+ *   Xq        [M, bt_act_row_bytes(K)] int8, 16-byte aligned; bytes past K of a row may hold anything.
+ *   Y         [M, N] of y_type (BT_F32, BT_BF16 or BT_F16), acc [M, N] int32; either may be NULL, not both. Aligned to
+ *             their element.
+ *   workspace bt_int8_workspace_bytes(M, N, K) bytes of device scratch, 256-byte aligned, or NULL when that is 0;
+ *             contents on entry are ignored. Calls sharing one must not overlap.
+ * Codes may be -128 to 127; acc is exact while K * max|X| * max|W| < 2^31 (always, with one side in +-127). K == 0
+ * gives acc 0.
+ */
+size_t bt_int8_weight_bytes(int64_t N, int64_t K);
+size_t bt_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bt_status bt_int8_gemm(const void *Wp, const float *w_scale, const int8_t *Xq, const float *x_scale, int64_t M,
+                       int64_t N, int64_t K, const float *bias, void *Y, int32_t y_type, int32_t *acc,
+                       void *workspace, void *stream);
+
+/*
+ * bt_int8_pack -- weights' codes W [N, K] int8 (rows ldw bytes apart) into Wp, once. Layout: rows and k are filled up
+ * with zeros to whole blocks of 16 rows x 64 k, 1 KB each; block (n / 16, k / 64) is number (n / 16) * ceil(K / 64) +
+ * k / 64, and byte 16 * (n % 16 + 16 * (k % 64 / 16)) + k % 16 of it holds (n, k).
+ */
+bt_status bt_int8_pack(const int8_t *W, int64_t ldw, int64_t N, int64_t K, void *Wp, void *stream);
+
 /* Static text for a status code. */
 const char *bt_status_str(bt_status s);
 
