@@ -3,12 +3,20 @@
 //
 // Weights are packed once (bt_int8_pack) into blocks of 16 rows x 64 k, 1 KB each, byte 16 * (r + 16 g) + e of a
 // block holding row r, k = 16 g + e: the operand of v_mfma_i32_16x16x64_i8 as its 64 lanes take it, so that a wave
-// reads a block as one contiguous KB.
+// reads a block as one contiguous KB, from memory and from LDS. Rows of the product are weight rows, columns tokens:
+// a lane then holds four outputs of one token that lie side by side.
+//
+// Up to 64 tokens go to k_int8_few, which streams the weights past the matrix cores without LDS; more to k_int8_tile.
+#include <type_traits>
+
 #include "bt_internal.h"
 #include "convert.h"
 
 namespace bt {
 namespace {
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
 
 __global__ __launch_bounds__(256) void k_int8_pack(const int8_t *W, int64_t ld, int64_t N, int64_t K, int64_t pieces,
                                                    int64_t KC, char *Wp)
@@ -26,12 +34,6 @@ __global__ __launch_bounds__(256) void k_int8_pack(const int8_t *W, int64_t ld, 
     *reinterpret_cast<uint4 *>(Wp + id * 16) = *reinterpret_cast<const uint4 *>(x);
 }
 
-template <typename T>
-__device__ inline void store1(T *p, float v)
-{
-    *p = (T)v;
-}
-
 struct Int8Args {
     const char *Wp;
     const float *w_scale, *x_scale, *bias;
@@ -39,39 +41,354 @@ struct Int8Args {
     void *Y;
     int *acc;
     int64_t M, N, ldx;
-    int KC;
+    int KC, NB;       // 64-k blocks of a row, 16-row blocks
+    int wide;         // outputs of four neighbours can be stored at once
+    int tiles_m, tiles_n;
 };
 
+// Four outputs of token m from column n on.
 template <typename TY>
-__global__ __launch_bounds__(64) void k_int8_simple(Int8Args a)
+__device__ inline void store_outputs(const Int8Args &a, int64_t m, int64_t n, v4i c, float xs, const float (&ws)[4],
+                                     const float (&bias)[4])
 {
-    const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
-    const int64_t nb = blockIdx.x, mb = blockIdx.y;
-    const char *w = a.Wp + nb * a.KC * 1024 + lane * 16;
-    const int64_t m = mb * 16 + r;
-    const int8_t *x = a.X + (m < a.M ? m : 0) * a.ldx + 16 * g;
-    v4i c = {0, 0, 0, 0};
-    for (int k = 0; k < a.KC; ++k) {
-        const v4i wa = *reinterpret_cast<const v4i *>(w + (int64_t)k * 1024);
-        const v4i xb = *reinterpret_cast<const v4i *>(x + (int64_t)k * 64);
-        c = __builtin_amdgcn_mfma_i32_16x16x64_i8(wa, xb, c, 0, 0, 0);
-    }
-    if (m >= a.M)
-        return;
+    float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t n = nb * 16 + 4 * g + i;
-        if (n >= a.N)
-            break;
+        y[i] = (float)c[i] * (xs * ws[i]);
+        if (a.bias)
+            y[i] = y[i] + bias[i];
+    }
+    const int64_t at = m * a.N + n;
+    if (a.wide && n + 4 <= a.N) {
         if (a.acc)
-            a.acc[m * a.N + n] = c[i];
-        if (a.Y) {
-            float y = (float)c[i] * (a.x_scale[m] * a.w_scale[n]);
-            if (a.bias)
-                y = y + a.bias[n];
-            store1(static_cast<TY *>(a.Y) + m * a.N + n, y);
+            *reinterpret_cast<v4i *>(a.acc + at) = c;
+        if (a.Y)
+            store4(static_cast<TY *>(a.Y) + at, y);
+        return;
+    }
+    for (int i = 0; i < 4 && n + i < a.N; ++i) {
+        if (a.acc)
+            a.acc[at + i] = c[i];
+        if (a.Y)
+            static_cast<TY *>(a.Y)[at + i] = (TY)y[i];
+    }
+}
+
+__device__ inline void load_scales(const Int8Args &a, int64_t n, float (&ws)[4], float (&bias)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t at = min(n + i, a.N - 1);
+        ws[i] = a.w_scale[at];
+        bias[i] = a.bias ? a.bias[at] : 0.f;
+    }
+}
+
+// ------------------------------------------------------------------------------ few tokens
+//
+// k_int8_few: 16 RT weight rows against 16 MT tokens by eight waves, which take every eighth 64-k block each (side by
+// side, so that the workgroup streams whole rows of blocks) and are joined through LDS. Operands go from memory
+// straight into registers, kDepth blocks ahead. Bound by the weights' bytes.
+
+constexpr int kFewWaves8 = 8;
+
+template <typename TY, int RT, int MT>
+__global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
+{
+    constexpr int kDepth = RT * MT >= 8 ? 2 : 4;
+    __shared__ v4i part[kFewWaves8][RT * MT][64];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int rb0 = blockIdx.x * RT;
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+
+    const char *w[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+        w[i] = a.Wp + (int64_t)min(rb0 + i, a.NB - 1) * a.KC * 1024 + lane * 16;
+    const int8_t *x[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+        x[j] = a.X + min(m0 + 16 * j + r, a.M - 1) * a.ldx + 16 * g;
+
+    v4i c[RT][MT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            c[i][j] = v4i{0, 0, 0, 0};
+    const int n = (a.KC - wave + kFewWaves8 - 1) / kFewWaves8;  // blocks of this wave (none: <= 0)
+    v4i wf[kDepth][RT], xf[kDepth][MT];
+    auto fetch = [&](int d, int k) __attribute__((always_inline)) {
+        const int64_t at = wave + (int64_t)min(k, n - 1) * kFewWaves8;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            wf[d][i] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w[i] + at * 1024));
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            xf[d][j] = *reinterpret_cast<const v4i *>(x[j] + at * 64);
+    };
+    auto multiply = [&](int d) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                c[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[d][i], xf[d][j], c[i][j], 0, 0, 0);
+    };
+    if (n > 0) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            fetch(d, d);
+        int k = 0;
+        for (; k + kDepth <= n; k += kDepth)
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                multiply(d);
+                fetch(d, k + kDepth + d);
+            }
+#pragma unroll
+        for (int d = 0; d < kDepth - 1; ++d)
+            if (k + d < n)
+                multiply(d);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            part[wave][i * MT + j][lane] = c[i][j];
+    __syncthreads();
+    // four outputs of a token each; threads side by side along the row
+    for (int q = threadIdx.x; q < RT * MT * 64; q += 64 * kFewWaves8) {
+        const int t = q / (4 * RT), rest = q % (4 * RT), i = rest / 4, quad = rest % 4;
+        const int64_t m = m0 + t, row = (int64_t)(rb0 + i) * 16 + 4 * quad;
+        if (m >= a.M || row >= a.N)
+            continue;
+        v4i sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int v = 0; v < kFewWaves8; ++v)
+            sum += part[v][i * MT + t / 16][16 * quad + t % 16];
+        float ws[4], bias[4];
+        load_scales(a, row, ws, bias);
+        store_outputs<TY>(a, m, row, sum, a.x_scale[m], ws, bias);
+    }
+}
+
+// ------------------------------------------------------------------------------- many tokens
+//
+// k_int8_tile: BM tokens x BN weight rows by WM x WN waves; 64 k a step through a ring of four LDS stages filled by
+// direct loads. A stage holds the weights' blocks as they are and the tokens as rows of 64 bytes, whose 16-byte piece p
+// lies at place p ^ (row / 4): sixteen rows' pieces then lie in sixteen different places of a 256-byte line, and four
+// lanes of a load read 64 neighbouring bytes.
+//
+// A step is two halves of the wave's tokens. While the first one's MFMAs run, the second's operands are read; then one
+// barrier publishes the next stage and frees this one for the load four steps ahead; while the second half's MFMAs run,
+// the next step's weights and first tokens are read.
+
+constexpr int kStages = 4;
+
+// At most VM of the wave's direct loads are on their way, its LDS reads are done; then the other waves' too.
+template <int VM>
+__device__ inline void meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(VM) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <typename TY, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
+{
+    constexpr int WAVES = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave
+    constexpr int XB = BM / 16, WB = BN / 16;                            // 1 KB blocks of a stage
+    constexpr int LX = XB / WAVES, LW = WB / WAVES;                      // of them, by a wave
+    constexpr int HALF = TM / 2;
+    constexpr int kBytes = (XB + WB) * 1024;
+    static_assert(XB % WAVES == 0 && WB % WAVES == 0 && TM % 2 == 0, "blocks split evenly over waves");
+    __shared__ __attribute__((aligned(1024))) char lds0[kBytes], lds1[kBytes], lds2[kBytes], lds3[kBytes];
+    auto stage = [&](auto sc) -> char * {
+        constexpr int S = decltype(sc)::value % kStages;
+        if constexpr (S == 0)
+            return lds0;
+        else if constexpr (S == 1)
+            return lds1;
+        else if constexpr (S == 2)
+            return lds2;
+        else
+            return lds3;
+    };
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int wm = wave % WM, wn = wave / WM;
+
+    // Workgroup b runs on XCD b % 8: every XCD takes a contiguous run of a tile order that goes through groups of
+    // kGroup token tiles column by column, so that what runs on it at a time shares its operands in its L2.
+    constexpr int kGroup = 8, kXcd = 8;
+    const int total = a.tiles_m * a.tiles_n, run = (total + kXcd - 1) / kXcd;
+    const int t = blockIdx.x % kXcd * run + blockIdx.x / kXcd;
+    if (blockIdx.x / kXcd >= run || t >= total)
+        return;
+    const int gid = t / (kGroup * a.tiles_n), in = t - gid * kGroup * a.tiles_n;
+    const int rows = min(kGroup, a.tiles_m - gid * kGroup);
+    const int64_t m0 = (int64_t)(gid * kGroup + in % rows) * BM;
+    const int tn = in / rows, rb0 = tn * WB;
+
+    // this wave's direct loads; rows past the last read the last
+    const int8_t *xp[LX];
+    const char *wp[LW];
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+        const int row = lane >> 2, p = (lane & 3) ^ (row >> 2);
+        xp[i] = a.X + min(m0 + (wave * LX + i) * 16 + row, a.M - 1) * a.ldx + 16 * p;
+    }
+#pragma unroll
+    for (int i = 0; i < LW; ++i)
+        wp[i] = a.Wp + (int64_t)min(rb0 + wave * LW + i, a.NB - 1) * a.KC * 1024 + lane * 16;
+    const int last = a.KC - 1;
+    auto issue = [&](int k, char *dst) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            __builtin_amdgcn_global_load_lds((global_void *)(xp[i] + (int64_t)k * 64),
+                                             (lds_void *)(dst + (wave * LX + i) * 1024), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < LW; ++i)
+            __builtin_amdgcn_global_load_lds((global_void *)(wp[i] + (int64_t)k * 1024),
+                                             (lds_void *)(dst + (XB + wave * LW + i) * 1024), 16, 0, 0);
+    };
+    const int x_off = wm * TM * 1024 + r * 64 + ((g ^ (r >> 2)) << 4);
+    const int w_off = (XB + wn * TN) * 1024 + lane * 16;
+    v4i acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+            acc[i][j] = v4i{0, 0, 0, 0};
+    v4i wf[2][TN], xf[2][HALF];
+    auto read_w = [&](const char *s, v4i (&f)[TN]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+            f[i] = *reinterpret_cast<const v4i *>(s + w_off + i * 1024);
+    };
+    auto read_x = [&](const char *s, int half, v4i (&f)[HALF]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < HALF; ++j)
+            f[j] = *reinterpret_cast<const v4i *>(s + x_off + (half * HALF + j) * 1024);
+    };
+    auto multiply = [&](const v4i (&w)[TN], const v4i (&x)[HALF], int half) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < HALF; ++j)
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                acc[i][half * HALF + j] =
+                    __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], x[j], acc[i][half * HALF + j], 0, 0, 0);
+    };
+    auto step = [&](auto sc, int k) __attribute__((always_inline)) {
+        constexpr int S = decltype(sc)::value;
+        char *now = stage(sc);
+        const char *next = stage(std::integral_constant<int, S + 1>{});
+        read_x(now, 1, xf[1]);
+        multiply(wf[S % 2], xf[0], 0);
+        // the next stage has landed (two more may be on their way), this one's operands are read
+        meet<(kStages - 2) * (LX + LW)>();
+        issue(min(k + kStages, last), now);  // past the end: the last one again, not used
+        read_w(next, wf[(S + 1) % 2]);
+        read_x(next, 0, xf[0]);
+        multiply(wf[S % 2], xf[1], 1);
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    issue(0, lds0);
+    issue(min(1, last), lds1);
+    issue(min(2, last), lds2);
+    issue(min(3, last), lds3);
+    meet<(kStages - 1) * (LX + LW)>();
+    read_w(lds0, wf[0]);
+    read_x(lds0, 0, xf[0]);
+    for (int k = 0;; k += kStages) {
+        step(I0{}, k);
+        if (k + 1 > last)
+            break;
+        step(I1{}, k + 1);
+        if (k + 2 > last)
+            break;
+        step(I2{}, k + 2);
+        if (k + 3 > last)
+            break;
+        step(I3{}, k + 3);
+        if (k + 4 > last)
+            break;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load is on its way to LDS when the workgroup ends
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+        const int64_t n = (int64_t)(rb0 + wn * TN + i) * 16 + 4 * g;
+        if (n >= a.N)
+            continue;
+        float ws[4], bias[4];
+        load_scales(a, n, ws, bias);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const int64_t m = m0 + (wm * TM + j) * 16 + r;
+            if (m < a.M)
+                store_outputs<TY>(a, m, n, acc[i][j], a.x_scale[m], ws, bias);
         }
     }
+}
+
+// K == 0: acc is 0.
+template <typename TY>
+__global__ __launch_bounds__(256) void k_int8_zero(Int8Args a)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= a.M * a.N)
+        return;
+    const float y = a.bias ? a.bias[id % a.N] : 0.f;
+    if (a.acc)
+        a.acc[id] = 0;
+    if (a.Y)
+        static_cast<TY *>(a.Y)[id] = (TY)y;
+}
+
+template <typename TY, int RT, int MT>
+hipError_t run_few(const Int8Args &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.NB + RT - 1) / RT), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+    k_int8_few<TY, RT, MT><<<grid, 64 * kFewWaves8, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename TY, int BM, int BN, int WM, int WN>
+hipError_t run_tile(Int8Args a, hipStream_t s)
+{
+    a.tiles_m = (int)((a.M + BM - 1) / BM);
+    a.tiles_n = (int)((a.N + BN - 1) / BN);
+    const int64_t run = ((int64_t)a.tiles_m * a.tiles_n + 7) / 8;
+    k_int8_tile<TY, BM, BN, WM, WN><<<(unsigned)(8 * run), 64 * WM * WN, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename TY>
+hipError_t run_int8(const Int8Args &a, hipStream_t s)
+{
+    if (a.KC == 0) {
+        k_int8_zero<TY><<<(unsigned)((a.M * a.N + 255) / 256), 256, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    if (a.M <= 64) {
+        const bool rows4 = a.NB >= 4 * 512, rows2 = a.NB >= 2 * 256;
+        if (a.M <= 16)
+            return rows4 ? run_few<TY, 4, 1>(a, s) : rows2 ? run_few<TY, 2, 1>(a, s) : run_few<TY, 1, 1>(a, s);
+        if (a.M <= 32)
+            return rows2 ? run_few<TY, 2, 2>(a, s) : run_few<TY, 1, 2>(a, s);
+        if (a.M <= 48)
+            return rows2 ? run_few<TY, 2, 3>(a, s) : run_few<TY, 1, 3>(a, s);
+        return rows2 ? run_few<TY, 2, 4>(a, s) : run_few<TY, 1, 4>(a, s);
+    }
+    const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+    if (big >= 192)
+        return run_tile<TY, 256, 256, 2, 4>(a, s);
+    return run_tile<TY, 128, 128, 2, 2>(a, s);
 }
 
 }  // namespace
@@ -91,16 +408,22 @@ size_t int8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 hipError_t launch_int8(const void *Wp, const float *w_scale, const int8_t *X, const float *x_scale, int64_t M,
                        int64_t N, int64_t K, const float *bias, void *Y, int y_type, int32_t *acc, void *, hipStream_t s)
 {
-    const Int8Args a = {static_cast<const char *>(Wp), w_scale, x_scale, bias, X, Y, acc, M, N, round_up(K, 256),
-                        (int)((K + 63) / 64)};
-    const dim3 grid((unsigned)((N + 15) / 16), (unsigned)((M + 15) / 16));
-    if (y_type == kF32)
-        k_int8_simple<float><<<grid, 64, 0, s>>>(a);
-    else if (y_type == kBF16)
-        k_int8_simple<bf16_t><<<grid, 64, 0, s>>>(a);
-    else
-        k_int8_simple<f16_t><<<grid, 64, 0, s>>>(a);
-    return hipGetLastError();
+    Int8Args a{};
+    a.Wp = static_cast<const char *>(Wp);
+    a.w_scale = w_scale;
+    a.x_scale = x_scale;
+    a.bias = bias;
+    a.X = X;
+    a.Y = Y;
+    a.acc = acc;
+    a.M = M;
+    a.N = N;
+    a.ldx = round_up(K, 256);
+    a.KC = (int)((K + 63) / 64);
+    a.NB = (int)((N + 15) / 16);
+    const uintptr_t four = y_type == kF32 ? 15 : 7;
+    a.wide = N % 4 == 0 && !(reinterpret_cast<uintptr_t>(Y) & four) && !(reinterpret_cast<uintptr_t>(acc) & 15);
+    return y_type == kF32 ? run_int8<float>(a, s) : y_type == kBF16 ? run_int8<bf16_t>(a, s) : run_int8<f16_t>(a, s);
 }
 
 }  // namespace bt
