@@ -187,12 +187,31 @@ __global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
 constexpr int kStages = 4;
 
 // At most VM of the wave's direct loads are on their way, its LDS reads are done; then the other waves' too.
+// (The wait is the builtin, which the compiler counts as its own: an asm one it does not see, and adds others.)
 template <int VM>
 __device__ inline void meet()
 {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(VM) : "memory");
-    __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((VM & 0xF) | (VM >> 4) << 14 | 0x7 << 4);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// The order of a half step: READS reads of LDS and LOADS direct loads spread over MMAS matrix instructions.
+template <int READS, int LOADS, int MMAS>
+__device__ __forceinline__ void interleave()
+{
+    constexpr int left = READS > LOADS ? READS : LOADS, each = left > 1 ? MMAS / left : MMAS;
+    if constexpr (left > 0) {
+        if constexpr (READS > 0)
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if constexpr (LOADS > 0)
+            __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x8, each, 0);
+        interleave<(READS > 0 ? READS - 1 : 0), (LOADS > 0 ? LOADS - 1 : 0), MMAS - each>();
+    }
 }
 
 template <typename TY, int BM, int BN, int WM, int WN>
@@ -287,12 +306,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
         const char *next = stage(std::integral_constant<int, S + 1>{});
         read_x(now, 1, xf[1]);
         multiply(wf[S % 2], xf[0], 0);
+        interleave<HALF, 0, TN * HALF>();
         // the next stage has landed (two more may be on their way), this one's operands are read
         meet<(kStages - 2) * (LX + LW)>();
         issue(min(k + kStages, last), now);  // past the end: the last one again, not used
         read_w(next, wf[(S + 1) % 2]);
         read_x(next, 0, xf[0]);
         multiply(wf[S % 2], xf[1], 1);
+        interleave<TN + HALF, LX + LW, TN * HALF>();
+        __builtin_amdgcn_sched_barrier(0);
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
@@ -305,20 +327,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
     meet<(kStages - 1) * (LX + LW)>();
     read_w(lds0, wf[0]);
     read_x(lds0, 0, xf[0]);
-    for (int k = 0;; k += kStages) {
+    int k = 0;
+    for (; k + kStages <= a.KC; k += kStages) {
         step(I0{}, k);
-        if (k + 1 > last)
-            break;
         step(I1{}, k + 1);
-        if (k + 2 > last)
-            break;
         step(I2{}, k + 2);
-        if (k + 3 > last)
-            break;
         step(I3{}, k + 3);
-        if (k + 4 > last)
-            break;
     }
+    if (k <= last)
+        step(I0{}, k);
+    if (k + 1 <= last)
+        step(I1{}, k + 1);
+    if (k + 2 <= last)
+        step(I2{}, k + 2);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load is on its way to LDS when the workgroup ends
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
