@@ -177,8 +177,7 @@ __global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
 //
 // k_int8_tile: BM tokens x BN weight rows by WM x WN waves; 64 k a step through a ring of four LDS stages filled by
 // direct loads. A stage holds the weights' blocks as they are and the tokens as rows of 64 bytes, whose 16-byte piece p
-// lies at place p ^ (row / 4): sixteen rows' pieces then lie in sixteen different places of a 256-byte line, and four
-// lanes of a load read 64 neighbouring bytes.
+// lies at place p ^ piece_place(row); four lanes of a load read 64 neighbouring bytes.
 //
 // A step is two halves of the wave's tokens. While the first one's MFMAs run, the second's operands are read; then one
 // barrier publishes the next stage and frees this one for the load four steps ahead; while the second half's MFMAs run,
@@ -198,6 +197,12 @@ __device__ inline void meet()
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
 }
+
+// A read of 16 bytes by 64 lanes goes in groups of sixteen, lanes 0-3, 12-15, 20-27 and their like: with r = lane % 16
+// and g = lane / 16, quarters 0 and 3 of r at one g, 1 and 2 at its neighbour. With these four numbers, g ^ number is
+// different in all four, and the group's pieces lie in different places of a 256-byte line. (With the quarter's own
+// number: 40% of the LDS cycles were conflicts.)
+__device__ inline int piece_place(int row) { return (row >> 1 & 2) ^ (row >> 3 & 1) * 3; }
 
 // The order of a half step: READS reads of LDS and LOADS direct loads spread over MMAS matrix instructions.
 template <int READS, int LOADS, int MMAS>
@@ -256,7 +261,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
     const char *wp[LW];
 #pragma unroll
     for (int i = 0; i < LX; ++i) {
-        const int row = lane >> 2, p = (lane & 3) ^ (row >> 2);
+        const int row = lane >> 2, p = (lane & 3) ^ piece_place(row);
         xp[i] = a.X + min(m0 + (wave * LX + i) * 16 + row, a.M - 1) * a.ldx + 16 * p;
     }
 #pragma unroll
@@ -273,7 +278,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
             __builtin_amdgcn_global_load_lds((global_void *)(wp[i] + (int64_t)k * 1024),
                                              (lds_void *)(dst + (XB + wave * LW + i) * 1024), 16, 0, 0);
     };
-    const int x_off = wm * TM * 1024 + r * 64 + ((g ^ (r >> 2)) << 4);
+    const int x_off = wm * TM * 1024 + r * 64 + ((g ^ piece_place(r)) << 4);
     const int w_off = (XB + wn * TN) * 1024 + lane * 16;
     v4i acc[TN][TM];
 #pragma unroll
