@@ -42,14 +42,15 @@ struct Int8Args {
     int *acc;
     int64_t M, N, ldx;
     int KC, NB;       // 64-k blocks of a row, 16-row blocks
-    int wide;         // outputs of four neighbours can be stored at once
+    int wide;         // four outputs side by side can be stored at once
+    int pieces;       // rows of Y are whole 16-byte pieces, 16-byte aligned
     int tiles_m, tiles_n;
 };
 
 // Four outputs of token m from column n on.
 template <typename TY>
 __device__ inline void store_outputs(const Int8Args &a, int64_t m, int64_t n, v4i c, float xs, const float (&ws)[4],
-                                     const float (&bias)[4])
+                                     const float (&bias)[4], bool with_y)
 {
     float y[4];
 #pragma unroll
@@ -62,14 +63,14 @@ __device__ inline void store_outputs(const Int8Args &a, int64_t m, int64_t n, v4
     if (a.wide && n + 4 <= a.N) {
         if (a.acc)
             *reinterpret_cast<v4i *>(a.acc + at) = c;
-        if (a.Y)
+        if (a.Y && with_y)
             store4(static_cast<TY *>(a.Y) + at, y);
         return;
     }
     for (int i = 0; i < 4 && n + i < a.N; ++i) {
         if (a.acc)
             a.acc[at + i] = c[i];
-        if (a.Y)
+        if (a.Y && with_y)
             static_cast<TY *>(a.Y)[at + i] = (TY)y[i];
     }
 }
@@ -169,7 +170,7 @@ __global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
             sum += part[v][i * MT + t / 16][16 * quad + t % 16];
         float ws[4], bias[4];
         load_scales(a, row, ws, bias);
-        store_outputs<TY>(a, m, row, sum, a.x_scale[m], ws, bias);
+        store_outputs<TY>(a, m, row, sum, a.x_scale[m], ws, bias, true);
     }
 }
 
@@ -204,18 +205,18 @@ __device__ inline void meet()
 // number: 40% of the LDS cycles were conflicts.)
 __device__ inline int piece_place(int row) { return (row >> 1 & 2) ^ (row >> 3 & 1) * 3; }
 
-// The order of a half step: READS reads of LDS and LOADS direct loads spread over MMAS matrix instructions.
+// The order of a half step: READS reads of LDS, then LOADS direct loads, each behind one of the first of its MMAS matrix
+// instructions, so that the reads are back when the next half needs them.
 template <int READS, int LOADS, int MMAS>
 __device__ __forceinline__ void interleave()
 {
-    constexpr int left = READS > LOADS ? READS : LOADS, each = left > 1 ? MMAS / left : MMAS;
-    if constexpr (left > 0) {
+    if constexpr (MMAS > 0) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
         if constexpr (READS > 0)
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        if constexpr (LOADS > 0)
+        else if constexpr (LOADS > 0)
             __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x8, each, 0);
-        interleave<(READS > 0 ? READS - 1 : 0), (LOADS > 0 ? LOADS - 1 : 0), MMAS - each>();
+        interleave<(READS > 0 ? READS - 1 : 0), (READS > 0 || LOADS == 0 ? LOADS : LOADS - 1), MMAS - 1>();
     }
 }
 
@@ -229,6 +230,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
     constexpr int kBytes = (XB + WB) * 1024;
     static_assert(XB % WAVES == 0 && WB % WAVES == 0 && TM % 2 == 0, "blocks split evenly over waves");
     __shared__ __attribute__((aligned(1024))) char lds0[kBytes], lds1[kBytes], lds2[kBytes], lds3[kBytes];
+    __shared__ __attribute__((aligned(16))) float s_w[BN], s_bias[BN], s_x[BM];
     auto stage = [&](auto sc) -> char * {
         constexpr int S = decltype(sc)::value % kStages;
         if constexpr (S == 0)
@@ -255,6 +257,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
     const int rows = min(kGroup, a.tiles_m - gid * kGroup);
     const int64_t m0 = (int64_t)(gid * kGroup + in % rows) * BM;
     const int tn = in / rows, rb0 = tn * WB;
+
+    // scales, for the end
+    for (int i = threadIdx.x; i < BN; i += 64 * WAVES) {
+        const int64_t n = min((int64_t)rb0 * 16 + i, a.N - 1);
+        s_w[i] = a.w_scale[n];
+        s_bias[i] = a.bias ? a.bias[n] : 0.f;
+    }
+    for (int i = threadIdx.x; i < BM; i += 64 * WAVES)
+        s_x[i] = a.x_scale[min(m0 + i, a.M - 1)];
 
     // this wave's direct loads; rows past the last read the last
     const int8_t *xp[LX];
@@ -345,19 +356,69 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
         step(I1{}, k + 1);
     if (k + 2 <= last)
         step(I2{}, k + 2);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load is on its way to LDS when the workgroup ends
+    meet<0>();  // no load is on its way to LDS, all reads are done: the stages are free
+
+    // Outputs. A lane has four of a token side by side, and storing those writes 32 bytes of 16 rows at a time (7 rounds of
+    // tiles of a 4096 x 28672 product: 190 us). Rows of whole 16-byte pieces go through the wave's part of the stages
+    // instead, and leave as 128 or 256 bytes of a row.
+    const int64_t mw = m0 + wm * TM * 16, nw = (int64_t)(rb0 + wn * TN) * 16;
+    const bool pieces = a.Y && a.pieces;
+    if (pieces) {
+        constexpr int ROW = 16 * TN * (int)sizeof(TY), PIECES = ROW / 16;  // bytes and pieces of a wave's row
+        constexpr int PART = 16384, TOKENS = PART / ROW < 16 * TM ? PART / ROW : 16 * TM;
+        static_assert(PART * WAVES == kStages * kBytes && kBytes % PART == 0, "a part each");
+        static_assert(TOKENS % 16 == 0 && 16 * TM % TOKENS == 0, "whole tiles at a time");
+        const int at = wave * PART / kBytes;
+        char *mine = (at == 0 ? lds0 : at == 1 ? lds1 : at == 2 ? lds2 : lds3) + wave * PART % kBytes;
+#pragma unroll
+        for (int j0 = 0; j0 < TM; j0 += TOKENS / 16) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                const float4 ws = *reinterpret_cast<const float4 *>(s_w + (wn * TN + i) * 16 + 4 * g);
+                const float4 bias = *reinterpret_cast<const float4 *>(s_bias + (wn * TN + i) * 16 + 4 * g);
+#pragma unroll
+                for (int j = 0; j < TOKENS / 16; ++j) {
+                    const v4i c = acc[i][j0 + j];
+                    const float xs = s_x[(wm * TM + j0 + j) * 16 + r];
+                    float y[4] = {(float)c[0] * (xs * ws.x), (float)c[1] * (xs * ws.y), (float)c[2] * (xs * ws.z),
+                                  (float)c[3] * (xs * ws.w)};
+                    if (a.bias) {
+                        y[0] = y[0] + bias.x;
+                        y[1] = y[1] + bias.y;
+                        y[2] = y[2] + bias.z;
+                        y[3] = y[3] + bias.w;
+                    }
+                    const int byte = (16 * i + 4 * g) * (int)sizeof(TY), row = 16 * j + r;
+                    store4(reinterpret_cast<TY *>(mine + row * ROW + ((byte >> 4 ^ (row & (PIECES - 1))) << 4) + (byte & 15)), y);
+                }
+            }
+            // LDS operations of a wave complete in order: only the compiler has to keep them so
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int q = 0; q < TOKENS * PIECES / 64; ++q) {
+                const int row = (q * 64 + lane) / PIECES, piece = lane % PIECES;
+                const uint4 y = *reinterpret_cast<const uint4 *>(mine + row * ROW + ((piece ^ (row & (PIECES - 1))) << 4));
+                const int64_t m = mw + 16 * j0 + row, n = nw + piece * (16 / (int)sizeof(TY));
+                if (m < a.M && n < a.N)
+                    *reinterpret_cast<uint4 *>(static_cast<TY *>(a.Y) + m * a.N + n) = y;
+            }
+            asm volatile("" ::: "memory");
+        }
+    }
+    if (pieces && !a.acc)
+        return;
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
-        const int64_t n = (int64_t)(rb0 + wn * TN + i) * 16 + 4 * g;
+        const int64_t n = nw + 16 * i + 4 * g;
         if (n >= a.N)
             continue;
         float ws[4], bias[4];
         load_scales(a, n, ws, bias);
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-            const int64_t m = m0 + (wm * TM + j) * 16 + r;
+            const int64_t m = mw + 16 * j + r;
             if (m < a.M)
-                store_outputs<TY>(a, m, n, acc[i][j], a.x_scale[m], ws, bias);
+                store_outputs<TY>(a, m, n, acc[i][j], a.x_scale[m], ws, bias, !pieces);
         }
     }
 }
@@ -449,6 +510,7 @@ hipError_t launch_int8(const void *Wp, const float *w_scale, const int8_t *X, co
     a.NB = (int)((N + 15) / 16);
     const uintptr_t four = y_type == kF32 ? 15 : 7;
     a.wide = N % 4 == 0 && !(reinterpret_cast<uintptr_t>(Y) & four) && !(reinterpret_cast<uintptr_t>(acc) & 15);
+    a.pieces = N * (y_type == kF32 ? 4 : 2) % 16 == 0 && !(reinterpret_cast<uintptr_t>(Y) & 15);
     return y_type == kF32 ? run_int8<float>(a, s) : y_type == kBF16 ? run_int8<bf16_t>(a, s) : run_int8<f16_t>(a, s);
 }
 
