@@ -85,19 +85,54 @@ __device__ inline void load_scales(const Int8Args &a, int64_t n, float (&ws)[4],
     }
 }
 
+// At most VM of the wave's direct loads are on their way, its LDS reads are done.
+// (The wait is the builtin, which the compiler counts as its own: an asm one it does not see, and adds others.)
+template <int VM>
+__device__ inline void landed()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((VM & 0xF) | (VM >> 4) << 14 | 0x7 << 4);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// A read of 16 bytes by 64 lanes goes in groups of sixteen, lanes 0-3, 12-15, 20-27 and their like: with r = lane % 16
+// and g = lane / 16, quarters 0 and 3 of r at one g, 1 and 2 at its neighbour. A block of sixteen tokens x 64 k lies in
+// LDS as rows of 64 bytes, whose 16-byte piece p is at place p ^ piece_place(row): g ^ piece_place is different in the four
+// quarters of a group, so that its pieces lie in different places of a 256-byte line. (With the quarter's own
+// number: 40% of the LDS cycles were conflicts.)
+__device__ inline int piece_place(int row) { return (row >> 1 & 2) ^ (row >> 3 & 1) * 3; }
+
 // ------------------------------------------------------------------------------ few tokens
 //
-// k_int8_few: 16 RT weight rows against 16 MT tokens by eight waves, which take every eighth 64-k block each (side by
-// side, so that the workgroup streams whole rows of blocks) and are joined through LDS. Operands go from memory
-// straight into registers, kDepth blocks ahead. Bound by the weights' bytes.
+// k_int8_few: 16 RT weight rows against 16 MT tokens by W waves, which take every W-th 64-k block each (side by side, so
+// that the workgroup streams whole rows of blocks) and are joined through LDS. Weights go from memory straight into
+// registers, RING blocks ahead. So do tokens where weights are what there is to read (RING == 2, DIRECT: more
+// workgroups fit a CU); in few workgroups they take a direct way into a piece of LDS of the wave's own, since a lane's
+// 16 bytes of 16 rows cost the load path more than 64 bytes side by side do.
 
-constexpr int kFewWaves8 = 8;
-
-template <typename TY, int RT, int MT>
-__global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
+template <typename TY, int RT, int MT, int RING, int W, bool DIRECT>
+__global__ __launch_bounds__(64 * W) void k_int8_few(Int8Args a)
 {
-    constexpr int kDepth = RT * MT >= 8 ? 2 : 4;
-    __shared__ v4i part[kFewWaves8][RT * MT][64];
+    static_assert(DIRECT || RING == 4, "four stages in LDS");
+    constexpr int kStagesUsed = DIRECT ? 1 : 4;
+    constexpr int kEach = DIRECT ? RT * MT : MT > RT * MT / 4 ? MT : RT * MT / 4;  // KB of a wave in a stage
+    constexpr int kPart = kEach * 1024;
+    static_assert(kEach * kStagesUsed >= RT * MT, "room for the waves' results");
+    __shared__ __attribute__((aligned(1024))) char ring0[W * kPart], ring1[DIRECT ? 16 : W * kPart],
+        ring2[DIRECT ? 16 : W * kPart], ring3[DIRECT ? 16 : W * kPart];
+    auto stage = [&](auto sc) -> char * {
+        constexpr int S = decltype(sc)::value;
+        if constexpr (S == 0)
+            return ring0;
+        else if constexpr (S == 1)
+            return ring1;
+        else if constexpr (S == 2)
+            return ring2;
+        else
+            return ring3;
+    };
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int rb0 = blockIdx.x * RT;
@@ -109,8 +144,11 @@ __global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
         w[i] = a.Wp + (int64_t)min(rb0 + i, a.NB - 1) * a.KC * 1024 + lane * 16;
     const int8_t *x[MT];
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-        x[j] = a.X + min(m0 + 16 * j + r, a.M - 1) * a.ldx + 16 * g;
+    for (int j = 0; j < MT; ++j) {
+        const int row = DIRECT ? r : lane >> 2, p = DIRECT ? g : (lane & 3) ^ piece_place(row);
+        x[j] = a.X + min(m0 + 16 * j + row, a.M - 1) * a.ldx + 16 * p;
+    }
+    const int x_off = wave * kPart + r * 64 + ((g ^ piece_place(r)) << 4);
 
     v4i c[RT][MT];
 #pragma unroll
@@ -118,56 +156,102 @@ __global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
 #pragma unroll
         for (int j = 0; j < MT; ++j)
             c[i][j] = v4i{0, 0, 0, 0};
-    const int n = (a.KC - wave + kFewWaves8 - 1) / kFewWaves8;  // blocks of this wave (none: <= 0)
-    v4i wf[kDepth][RT], xf[kDepth][MT];
-    auto fetch = [&](int d, int k) __attribute__((always_inline)) {
-        const int64_t at = wave + (int64_t)min(k, n - 1) * kFewWaves8;
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-            wf[d][i] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w[i] + at * 1024));
+    const int n = (a.KC - wave + W - 1) / W;  // blocks of this wave (none: <= 0)
+    v4i wf[RING][RT], xf[DIRECT ? RING : 1][MT];
+    auto fetch = [&](auto sc, int k) __attribute__((always_inline)) {
+        constexpr int S = decltype(sc)::value;
+        const int64_t at = wave + (int64_t)min(k, n - 1) * W;  // past the end: the last one again, not used
 #pragma unroll
         for (int j = 0; j < MT; ++j)
-            xf[d][j] = *reinterpret_cast<const v4i *>(x[j] + at * 64);
+            if constexpr (DIRECT)
+                xf[S][j] = *reinterpret_cast<const v4i *>(x[j] + at * 64);
+            else
+                __builtin_amdgcn_global_load_lds((global_void *)(x[j] + at * 64),
+                                                 (lds_void *)(stage(sc) + wave * kPart + j * 1024), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            wf[S][i] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w[i] + at * 1024));
     };
-    auto multiply = [&](int d) __attribute__((always_inline)) {
+    auto multiply = [&](const v4i (&wv)[RT], const v4i (&xv)[MT]) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j)
-                c[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[d][i], xf[d][j], c[i][j], 0, 0, 0);
+                c[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i], xv[j], c[i][j], 0, 0, 0);
     };
+    // MORE: loads of three further steps are on their way, and this one's places are filled again
+    auto step = [&](auto sc, int k, auto more) __attribute__((always_inline)) {
+        constexpr int S = decltype(sc)::value;
+        constexpr bool MORE = decltype(more)::value;
+        if constexpr (DIRECT) {
+            multiply(wf[S], xf[S]);
+        } else {
+            landed<MORE ? (RING - 1) * (RT + MT) : 0>();
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                xf[0][j] = *reinterpret_cast<const v4i *>(stage(sc) + x_off + j * 1024);
+            multiply(wf[S], xf[0]);
+            if constexpr (MORE)
+                landed<(RING - 1) * (RT + MT)>();  // the reads, before the stage is filled again
+        }
+        if constexpr (MORE)
+            fetch(sc, k + RING);
+    };
+    using More = std::true_type;
+    using NoMore = std::false_type;
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
     if (n > 0) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d)
-            fetch(d, d);
+        fetch(I0{}, 0);
+        fetch(I1{}, 1);
+        if constexpr (RING > 2) {
+            fetch(I2{}, 2);
+            fetch(I3{}, 3);
+        }
         int k = 0;
-        for (; k + kDepth <= n; k += kDepth)
-#pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                multiply(d);
-                fetch(d, k + kDepth + d);
+        for (; k + RING <= n; k += RING) {
+            step(I0{}, k, More{});
+            step(I1{}, k + 1, More{});
+            if constexpr (RING > 2) {
+                step(I2{}, k + 2, More{});
+                step(I3{}, k + 3, More{});
             }
-#pragma unroll
-        for (int d = 0; d < kDepth - 1; ++d)
-            if (k + d < n)
-                multiply(d);
+        }
+        if (k < n)
+            step(I0{}, k, NoMore{});
+        if constexpr (RING > 2) {
+            if (k + 1 < n)
+                step(I1{}, k + 1, NoMore{});
+            if (k + 2 < n)
+                step(I2{}, k + 2, NoMore{});
+        }
+        landed<0>();
     }
+    __syncthreads();  // no load is on its way to LDS
+    // the results take the stages' room: kEach tiles of a wave in each
+    auto place = [&](int v, int t) -> v4i * {
+        const int s = t / kEach;
+        char *p = s == 0 ? ring0 : s == 1 ? ring1 : s == 2 ? ring2 : ring3;
+        return reinterpret_cast<v4i *>(p + v * kPart + t % kEach * 1024);
+    };
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < MT; ++j)
-            part[wave][i * MT + j][lane] = c[i][j];
+            place(wave, i * MT + j)[lane] = c[i][j];
     __syncthreads();
     // four outputs of a token each; threads side by side along the row
-    for (int q = threadIdx.x; q < RT * MT * 64; q += 64 * kFewWaves8) {
+    for (int q = threadIdx.x; q < RT * MT * 64; q += 64 * W) {
         const int t = q / (4 * RT), rest = q % (4 * RT), i = rest / 4, quad = rest % 4;
         const int64_t m = m0 + t, row = (int64_t)(rb0 + i) * 16 + 4 * quad;
         if (m >= a.M || row >= a.N)
             continue;
         v4i sum = {0, 0, 0, 0};
 #pragma unroll
-        for (int v = 0; v < kFewWaves8; ++v)
-            sum += part[v][i * MT + t / 16][16 * quad + t % 16];
+        for (int v = 0; v < W; ++v)
+            sum += place(v, i * MT + t / 16)[16 * quad + t % 16];
         float ws[4], bias[4];
         load_scales(a, row, ws, bias);
         store_outputs<TY>(a, m, row, sum, a.x_scale[m], ws, bias, true);
@@ -184,26 +268,16 @@ __global__ __launch_bounds__(64 * kFewWaves8) void k_int8_few(Int8Args a)
 // barrier publishes the next stage and frees this one for the load four steps ahead; while the second half's MFMAs run,
 // the next step's weights and first tokens are read.
 
-constexpr int kStages = 4;
 
-// At most VM of the wave's direct loads are on their way, its LDS reads are done; then the other waves' too.
-// (The wait is the builtin, which the compiler counts as its own: an asm one it does not see, and adds others.)
+// The same for all waves of the workgroup.
 template <int VM>
 __device__ inline void meet()
 {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((VM & 0xF) | (VM >> 4) << 14 | 0x7 << 4);
+    landed<VM>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
 }
-
-// A read of 16 bytes by 64 lanes goes in groups of sixteen, lanes 0-3, 12-15, 20-27 and their like: with r = lane % 16
-// and g = lane / 16, quarters 0 and 3 of r at one g, 1 and 2 at its neighbour. With these four numbers, g ^ number is
-// different in all four, and the group's pieces lie in different places of a 256-byte line. (With the quarter's own
-// number: 40% of the LDS cycles were conflicts.)
-__device__ inline int piece_place(int row) { return (row >> 1 & 2) ^ (row >> 3 & 1) * 3; }
 
 // The order of a half step: READS reads of LDS, then LOADS direct loads, each behind one of the first of its MMAS matrix
 // instructions, so that the reads are back when the next half needs them.
@@ -219,6 +293,8 @@ __device__ __forceinline__ void interleave()
         interleave<(READS > 0 ? READS - 1 : 0), (READS > 0 || LOADS == 0 ? LOADS : LOADS - 1), MMAS - 1>();
     }
 }
+
+constexpr int kStages = 4;
 
 template <typename TY, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
@@ -437,11 +513,11 @@ __global__ __launch_bounds__(256) void k_int8_zero(Int8Args a)
         static_cast<TY *>(a.Y)[id] = (TY)y;
 }
 
-template <typename TY, int RT, int MT>
+template <typename TY, int RT, int MT, int RING, int W, bool DIRECT>
 hipError_t run_few(const Int8Args &a, hipStream_t s)
 {
     const dim3 grid((unsigned)((a.NB + RT - 1) / RT), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-    k_int8_few<TY, RT, MT><<<grid, 64 * kFewWaves8, 0, s>>>(a);
+    k_int8_few<TY, RT, MT, RING, W, DIRECT><<<grid, 64 * W, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -455,6 +531,20 @@ hipError_t run_tile(Int8Args a, hipStream_t s)
     return hipGetLastError();
 }
 
+// Few workgroups, tokens through LDS: the smallest tile of which no more than one a CU is needed.
+int few_tile(int64_t M, int64_t NB)
+{
+    constexpr int order[] = {12, 13, 14, 22, 23, 24, 42, 43, 44};  // 10 RT + MT
+    int best = 0;
+    for (int c : order) {
+        const int rt = c / 10, mt = c % 10, area = best / 10 * (best % 10);
+        const int64_t groups = (NB + rt - 1) / rt * ((M + 16 * mt - 1) / (16 * mt));
+        if (groups <= 256 && (best == 0 || rt * mt < area))
+            best = c;
+    }
+    return best;
+}
+
 template <typename TY>
 hipError_t run_int8(const Int8Args &a, hipStream_t s)
 {
@@ -462,18 +552,29 @@ hipError_t run_int8(const Int8Args &a, hipStream_t s)
         k_int8_zero<TY><<<(unsigned)((a.M * a.N + 255) / 256), 256, 0, s>>>(a);
         return hipGetLastError();
     }
-    if (a.M <= 64) {
-        const bool rows4 = a.NB >= 4 * 512, rows2 = a.NB >= 2 * 256;
-        if (a.M <= 16)
-            return rows4 ? run_few<TY, 4, 1>(a, s) : rows2 ? run_few<TY, 2, 1>(a, s) : run_few<TY, 1, 1>(a, s);
-        if (a.M <= 32)
-            return rows2 ? run_few<TY, 2, 2>(a, s) : run_few<TY, 1, 2>(a, s);
-        if (a.M <= 48)
-            return rows2 ? run_few<TY, 2, 3>(a, s) : run_few<TY, 1, 3>(a, s);
-        return rows2 ? run_few<TY, 2, 4>(a, s) : run_few<TY, 1, 4>(a, s);
+    if (a.M <= 16)
+        return a.NB >= 1600  ? run_few<TY, 4, 1, 2, 8, true>(a, s)
+               : a.NB >= 512 ? run_few<TY, 2, 1, 2, 8, true>(a, s)
+                             : run_few<TY, 1, 1, 4, 8, true>(a, s);
+    if (a.M <= 64 && a.NB >= 800)
+        return a.M <= 32   ? run_few<TY, 4, 2, 2, 8, true>(a, s)
+               : a.M <= 48 ? (a.NB >= 1200 ? run_few<TY, 4, 3, 2, 4, true>(a, s) : run_few<TY, 4, 3, 2, 8, true>(a, s))
+               : a.NB >= 1200 ? run_few<TY, 4, 4, 2, 4, true>(a, s)
+                              : run_few<TY, 4, 4, 2, 8, true>(a, s);
+    switch (few_tile(a.M, a.NB)) {
+    case 12: return run_few<TY, 1, 2, 4, 8, false>(a, s);
+    case 13: return run_few<TY, 1, 3, 4, 8, false>(a, s);
+    case 14: return run_few<TY, 1, 4, 4, 8, false>(a, s);
+    case 22: return run_few<TY, 2, 2, 4, 8, false>(a, s);
+    case 23: return run_few<TY, 2, 3, 4, 8, false>(a, s);
+    case 24: return run_few<TY, 2, 4, 4, 8, false>(a, s);
+    case 42: return run_few<TY, 4, 2, 4, 8, false>(a, s);
+    case 43: return run_few<TY, 4, 3, 4, 8, false>(a, s);
+    case 44: return run_few<TY, 4, 4, 4, 8, false>(a, s);
+    default: break;
     }
-    const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-    if (big >= 192)
+    // one workgroup of large tiles fills a CU: from three quarters of the CUs on they win
+    if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= 192)
         return run_tile<TY, 256, 256, 2, 4>(a, s);
     return run_tile<TY, 128, 128, 2, 2>(a, s);
 }
