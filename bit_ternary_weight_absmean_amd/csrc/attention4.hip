@@ -168,6 +168,363 @@ constexpr bool kSplitQuery = sizeof(typename Elem<E>::v8) == 16 && Elem<E>::kRai
 // The keys r < n of sixteen, as bits.
 __device__ inline uint32_t first_bits(int n) { return n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
 
+// ------------------------------------------------------------------------- prompt kernel
+//
+// attn4_tile: 32 rows per wave (32x32x16 MFMA) against a slice of the tile's keys, 64 at a time, as attn_tile of
+// csrc/attention.hip has it: a vector phase from scores to probabilities, then a matrix phase of this block's product with
+// V and the next block's scores; two buffers of K and of V in LDS, K one block ahead. A block's codes are loaded
+// into registers (each wave 16 of its keys) while the one before them is used, and go to LDS as bf16, once for
+// all of the tile's rows, beside that one's matrix phase.
+//
+// HALVES == 2, for calls whose tiles of 128 rows would not fill the CUs: 64 rows, and the waves of a pair take the two
+// halves of every block's keys and are joined at the end.
+
+constexpr int kTileRows = 128, kSmallRows = 64, kTileKeys = 64;
+
+// Of the blocks in LDS: which 16-key tiles name no page (those of four blocks on end: K's are written two ahead of their
+// use), and which keys have NaN groups (V's).
+template <int DP>
+struct BlockNotes {
+    uint32_t gone[4][4];
+    unsigned short nan[2][DP / 32][4];
+};
+
+template <typename E, int DP, bool WIDE, int HALVES>
+__device__ __forceinline__ void attn4_tile(const Attn4Args &a, int block, char *kbuf0, char *kbuf1, char *vbuf0,
+                                           char *vbuf1, BlockNotes<DP> *notes)
+{
+    constexpr int ROWS = kTileRows / HALVES, KB = 2 / HALVES;  // rows of the tile, 32-key parts per wave
+    constexpr int NS = DP / 16, ND = DP / 32;                  // MFMA steps over D, 32-wide tiles of D
+    constexpr int PARTS = WIDE ? 3 : kSplitQuery<E> ? 2 : 1;   // of a probability
+    using Codes = Codes4<DP>;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int col = lane & 31, h = lane >> 5, r16 = lane & 15, g = lane >> 4;
+    const int rg = HALVES == 2 ? wave & 1 : wave;        // the wave's 32 rows
+    const int part0 = HALVES == 2 ? wave >> 1 : 0;       // its first 32-key part of a block
+    const int id = block / a.Hkv, head = block % a.Hkv;
+    Item it;
+    if (!find_item(a, ROWS, id, false, it))
+        return;
+    const Seq s = it.s;
+
+    // this lane's row
+    const int rows = s.nq * a.G;
+    const int row = it.tile * ROWS + 32 * rg + col;
+    const int token = row / a.G, qh = head * a.G + row % a.G;
+    const bool live = row < rows;
+    const int limit = live ? row_limit(a, s, token) : 0;
+    // the keys of the tile, and those that every live row of the wave sees
+    const int last = min(rows, (it.tile + 1) * ROWS) - 1;
+    const int lo = (int)min((int64_t)it.piece * it.unit * kUnit, (int64_t)s.nk);
+    const int hi = min((int)min((int64_t)(it.piece + 1) * it.unit * kUnit, (int64_t)s.nk), row_limit(a, s, last / a.G));
+    const int first = it.tile * ROWS + 32 * rg;
+    const int wfull = first < rows ? row_limit(a, s, first / a.G) : 0;
+    const int wmost = first < rows ? row_limit(a, s, min(rows - 1, first + 31) / a.G) : 0;
+
+    // Q^T operands: lane (col, h) holds values 16 st + 8 h .. + 7 of its row
+    V8 qf[NS], ql[NS];
+    {
+        const char *p = static_cast<const char *>(a.q) + 2 * ((int64_t)(s.q0 + token) * a.q_row + (int64_t)qh * a.q_head);
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            u32x4 x = {0, 0, 0, 0};
+            if (live && 16 * st + 8 * h < a.D)
+                x = *reinterpret_cast<const u32x4 *>(p + 2 * (16 * st + 8 * h));
+            split_query<E>(x, qf[st], ql[st]);
+        }
+    }
+    const Places4<DP> places = lane_places<DP>(a);
+    PageWindow kwindow = page_window(a, s), vwindow = kwindow;
+    // the codes of this wave's 16 keys of a block of K and one of V, on their way
+    Codes x;
+    bool there = false;
+    auto load_k = [&](int key) __attribute__((always_inline)) {
+        if (key >= hi)
+            return;
+        const Tile4 t = find_tile(a, kwindow, head, key + 16 * wave);
+        there = t.there;
+        load_keys<DP>(a, places, t, x);
+    };
+    auto load_v = [&](int key) __attribute__((always_inline)) {
+        if (key >= hi)
+            return;
+        load_values<DP>(a, places, find_tile(a, vwindow, head, key + 16 * wave), x);
+    };
+    // Their values to LDS as [key][D]: lane (r, g) has key r of the wave's tile, 32 values from chunk 4 g (16 from 2 g).
+    auto store_k = [&](int key, char *kb) __attribute__((always_inline)) {
+        if (key >= hi)
+            return;
+        const int r = 16 * wave + r16;
+#pragma unroll
+        for (int n = 0; n < Codes::NB; ++n)
+#pragma unroll
+            for (int w = 0; w < Codes::W; ++w) {
+                const int c = Codes::W * (g + 4 * n) + w;
+                *reinterpret_cast<u32x4 *>(kb + r * (DP * 2) + ((c ^ swizzle<DP>(r)) << 4)) =
+                    __builtin_bit_cast(u32x4, cache_values(x.k[n][w], cache_scale(x.ks[n])));
+            }
+        if (lane == 0)
+            notes->gone[key / kTileKeys & 3][wave] = !there;
+    };
+    // V: keys past the sequence's end hold anything: zeros; groups with NaNs: zeros, and noted
+    auto store_v = [&](int key, char *vb) __attribute__((always_inline)) {
+        if (key >= hi)
+            return;
+        const int r = 16 * wave + r16;
+        const bool past = key + r >= s.nk;
+#pragma unroll
+        for (int n = 0; n < Codes::NB; ++n) {
+            const bool bad = x.vs[n] > kCacheNaN, none = past || bad;
+            const uint64_t nan = __ballot(bad && !past);
+            const float f = cache_scale(none ? 0u : x.vs[n]);
+#pragma unroll
+            for (int w = 0; w < Codes::W; ++w) {
+                const int c = Codes::W * (g + 4 * n) + w;
+                *reinterpret_cast<u32x4 *>(vb + r * (DP * 2) + ((c ^ swizzle<DP>(r)) << 4)) =
+                    __builtin_bit_cast(u32x4, cache_values(none ? 0u : x.v[n][w], f));
+            }
+            if (r16 == 0)
+                notes->nan[key / kTileKeys & 1][DP == 64 ? g >> 1 : g + 4 * n][wave] = (unsigned short)(nan >> (16 * g));
+        }
+    };
+
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[d][i] = 0.f;
+    float m = -INFINITY, l = 0.f;  // l: this lane's keys only until the end
+    const float c2 = a.scale_log2;
+
+    // S^T of a block; register i of half b: key + 32 b + 8 (i / 4) + 4 h + i % 4
+    f32x16 sc[KB];
+    const int kbase = col * (DP * 2) + ((h ^ swizzle<DP>(col)) << 4);
+    auto scores = [&](const char *kb) __attribute__((always_inline)) {
+        kb += part0 * 32 * DP * 2;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sc[b][i] = 0.f;
+#pragma unroll
+            for (int st = 0; st < NS; ++st) {
+                const V8 k = __builtin_bit_cast(V8, *reinterpret_cast<const u32x4 *>(kb + (kbase ^ (st << 5)) + b * 32 * DP * 2));
+                sc[b] = Elem<bf16_t>::mma32(k, qf[st], sc[b]);
+                if constexpr (kSplitQuery<E>)
+                    sc[b] = Elem<bf16_t>::mma32(k, ql[st], sc[b]);
+            }
+        }
+    };
+    // The vector phase: probabilities of the block, as P^T operands (slot j of step t is register
+    // 8 (t % 2) + j of half t / 2).
+    u32x4 pf[PARTS][2 * KB];
+    auto soften = [&](int key) __attribute__((always_inline)) {
+        const u32x4 gone = *reinterpret_cast<const u32x4 *>(notes->gone[key / kTileKeys & 3]);
+        if (uniform(gone[0] | gone[1] | gone[2] | gone[3]) || key + kTileKeys > wfull) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (key + 32 * (part0 + b) + 8 * (i / 4) + 4 * h + i % 4 >= limit || (part0 ? gone[2 + i / 8] : gone[2 * b + i / 8]))
+                        sc[b][i] = -INFINITY;
+        }
+        float mx = sc[0][0];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                mx = fmaxf(mx, sc[b][i]);
+        mx = fmaxf(mx, other_half(mx));
+        if (__any((mx - m) * c2 > Elem<bf16_t>::kRise || (m == -INFINITY && mx > -INFINITY))) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.f : exp2_fast((m - mn) * c2);
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] *= f;
+            m = mn;
+        }
+        const float ref = m == -INFINITY ? 0.f : m * c2;
+        float lb = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2 * KB; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float p[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    p[e] = exp2_fast(__builtin_fmaf(sc[t / 2][8 * (t % 2) + 2 * j + e], c2, -ref));
+                    lb += p[e];
+                }
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) {
+                    pf[q][t][j] = pack2<bf16_t>(p[0], p[1]);
+                    const f32x2 back = unpack2<bf16_t>(pf[q][t][j]);
+                    p[0] -= back[0];
+                    p[1] -= back[1];
+                }
+            }
+        l += lb;
+        // done here, not where they are used
+        asm volatile("" : "+v"(l));
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+            for (int t = 0; t < 2 * KB; ++t)
+                asm volatile("" : "+v"(pf[q][t]));
+    };
+    // The matrix phase. V^T operands: lane i of 16 reads 8 bytes of row i / 4 of its 4 x 16 block of V. Row
+    // 16 t + 8 j + tr_row is swizzled by that of tr_row, with bit 1 flipped by j.
+    const int tr_row = 4 * h + (lane & 15) / 4, tr_col = (lane >> 4 & 1) * 32 + (lane & 3) * 8;  // bytes
+    const int vbase = tr_row * (DP * 2) + (((tr_col >> 4) ^ swizzle<DP>(tr_row)) << 4) + (tr_col & 15);
+    auto weigh = [&](int key, const char *vb) __attribute__((always_inline)) {
+        vb += part0 * 32 * DP * 2;
+        uint64_t any = 0;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            any |= *reinterpret_cast<const uint64_t *>(notes->nan[key / kTileKeys & 1][d]);
+#pragma unroll
+            for (int t = 0; t < 2 * KB; ++t) {
+                u32x4 y;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const char *p = vb + (vbase ^ (d << 6) ^ (j << 5)) + (16 * t + 8 * j) * DP * 2;
+                    const u32x2 half =
+                        __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+                    y[2 * j] = half[0];
+                    y[2 * j + 1] = half[1];
+                }
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+                    o[d] = Elem<bf16_t>::mma32(__builtin_bit_cast(V8, y), __builtin_bit_cast(V8, pf[q][t]), o[d]);
+            }
+        }
+        if (__builtin_expect(uniform((uint32_t)(any | any >> 32)), 0)) {
+            const int n = limit - key;
+            const uint64_t sees = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                if (*reinterpret_cast<const uint64_t *>(notes->nan[key / kTileKeys & 1][d]) & sees)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[d][i] = NAN;
+        }
+    };
+
+    // End of a block: this wave's LDS operations are done; then all waves'.
+    auto sync = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (lo < hi) {
+        load_k(lo);
+        load_v(lo);
+        store_k(lo, kbuf0);
+        load_k(lo + kTileKeys);
+        sync();
+        scores(kbuf0);
+        store_v(lo, vbuf0);
+        store_k(lo + kTileKeys, kbuf1);
+        load_k(lo + 2 * kTileKeys);
+        load_v(lo + kTileKeys);
+        sync();
+        // K runs one block ahead of V; the last block's matrix phase forms scores from whatever the
+        // other buffer holds, and they are not used.
+        auto one = [&](int key, char *vb, char *kb, char *vnext, char *knext) __attribute__((always_inline)) {
+            if (key < wmost)
+                soften(key);
+            store_k(key + 2 * kTileKeys, knext);
+            store_v(key + kTileKeys, vnext);
+            load_k(key + 3 * kTileKeys);
+            load_v(key + 2 * kTileKeys);
+            if (key < wmost) {
+                scores(kb);
+                weigh(key, vb);
+            }
+            sync();
+        };
+        for (int key = lo; key < hi; key += 2 * kTileKeys) {
+            one(key, vbuf0, kbuf1, vbuf1, kbuf0);
+            if (key + kTileKeys < hi)
+                one(key + kTileKeys, vbuf1, kbuf0, vbuf0, kbuf1);
+        }
+    }
+    l += other_half(l);
+    __syncthreads();
+    if constexpr (HALVES == 2) {
+        // the second half's sums to the first half's waves
+        float *sums = reinterpret_cast<float *>(rg ? kbuf1 : kbuf0), *stat = reinterpret_cast<float *>(vbuf0) + 64 * rg;
+        if (part0) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sums[(d * 16 + i) * 64 + lane] = o[d][i];
+            stat[col] = m;
+            stat[32 + col] = l;
+        }
+        __syncthreads();
+        if (part0)
+            return;
+        const float m1 = stat[col], mn = fmaxf(m, m1);
+        const float f0 = m == mn ? 1.f : exp2_fast((m - mn) * c2), f1 = m1 == mn ? 1.f : exp2_fast((m1 - mn) * c2);
+        l = l * f0 + stat[32 + col] * f1;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[d][i] = o[d][i] * f0 + sums[(d * 16 + i) * 64 + lane] * f1;
+        m = mn;
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
+    const float lse = l == 0.f ? -INFINITY : m * c2 * kLn2 + logf(l);
+    if (!live)
+        return;
+    const bool part = it.pieces > 1;
+    if (part) {
+        const int64_t slot = block;
+        const int r = 32 * rg + col;
+        float *dst = a.ws_o + (slot * ROWS + r) * a.D;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int e = 32 * d + 8 * b + 4 * h;
+                if (e < a.D) {
+                    const float x[4] = {o[d][4 * b] * inv, o[d][4 * b + 1] * inv, o[d][4 * b + 2] * inv,
+                                        o[d][4 * b + 3] * inv};
+                    store4(dst + e, x);
+                }
+            }
+        if (h == 0)
+            a.ws_l[slot * ROWS + r] = lse;
+        return;
+    }
+    const int64_t at = (int64_t)(s.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int e = 32 * d + 8 * b + 4 * h;
+            if (e < a.D) {
+                const float x[4] = {o[d][4 * b] * inv, o[d][4 * b + 1] * inv, o[d][4 * b + 2] * inv,
+                                    o[d][4 * b + 3] * inv};
+                if constexpr (WIDE)
+                    store4(static_cast<float *>(a.out) + at + e, x);
+                else
+                    store4(static_cast<E *>(a.out) + at + e, x);
+            }
+        }
+    if (a.lse && h == 0)
+        a.lse[(int64_t)(s.q0 + token) * a.Hq + qh] = lse;
+}
+
 // -------------------------------------------------------------------- few-rows kernel
 //
 // attn4_few: 16 rows (a decode step's heads of one group, a short draft) against a slice of their keys; bound by
@@ -437,13 +794,27 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn4_few(Attn4Args a
     attn4_few<E, DP, WIDE>(a, blockIdx.x, buf, stat);
 }
 
+template <typename E, int DP, bool WIDE, int HALVES>
+__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn4_tile(Attn4Args a)
+{
+    constexpr int bytes = kTileKeys * DP * 2;
+    __shared__ __attribute__((aligned(1024))) char kbuf0[bytes], kbuf1[bytes], vbuf0[bytes], vbuf1[bytes];
+    __shared__ __attribute__((aligned(16))) BlockNotes<DP> notes;
+    attn4_tile<E, DP, WIDE, HALVES>(a, blockIdx.x, kbuf0, kbuf1, vbuf0, vbuf1, &notes);
+}
+
 // --------------------------------------------------------------------------------- plans
 
 template <typename E, int DP, bool WIDE>
 hipError_t run_kind4(const Attn4Args &a, const Attn4Plan &p, hipStream_t s)
 {
     const unsigned grid = (unsigned)(p.main.items * a.Hkv);
-    k_attn4_few<E, DP, WIDE><<<grid, 256, 0, s>>>(a);
+    if (p.main.bm == kFewRows)
+        k_attn4_few<E, DP, WIDE><<<grid, 256, 0, s>>>(a);
+    else if (p.main.bm == kSmallRows)
+        k_attn4_tile<E, DP, WIDE, 2><<<grid, 256, 0, s>>>(a);
+    else
+        k_attn4_tile<E, DP, WIDE, 1><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -472,9 +843,15 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
     Attn4Plan plan{};
     AttnPart &p = plan.main;
     const int64_t rows = T * (Hq / Hkv), seqs = B < T ? B : T;
-    p.bm = kFewRows;
+    // mean rows of a sequence: up to 16, one small tile each
+    p.bm = rows <= kFewRows * seqs ? kFewRows : kTileRows;
+    if (p.bm == kTileRows && (rows / kTileRows + seqs) * Hkv < 512)
+        p.bm = kSmallRows;
     p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
-    p.target = most_keys <= 512 ? 0 : (2048 + Hkv - 1) / Hkv;
+    const int64_t target = ((p.bm == kFewRows ? 2048 : 384) + Hkv - 1) / Hkv;
+    p.target = p.bm == kFewRows || 3 * p.tiles < target ? target : 0;
+    if (most_keys <= 512)
+        p.target = 0;
     p.min_units = 4;
     const int64_t most = ((most_keys + kUnit - 1) / kUnit + p.min_units - 1) / p.min_units;
     p.items = p.tiles + (p.target ? p.target + 8 : 0);

@@ -2,8 +2,9 @@
 in 64 bits on the cache's own values.
 
 Tolerance of the attention. Keys and values are exact (a code with its scale is a bf16), and so are the queries.
- - Probabilities are carried in two bf16 parts, each the nearest: 2^-9 of the one before, so 2^-18 in all; in three,
-   2^-27, for fp32 outputs; in one, 2^-9, for bf16 outputs of more than 16 rows of a sequence and key head.
+ - Probabilities are carried in two bf16 parts, each the nearest: a bf16 has 8 significant bits, so the rest is at most
+   half a step, 2^-8 of a value in [1, 2) and so of any value, and 2^-16 is left after two parts; after three, for
+   fp32 outputs, 2^-24; after one, for bf16 outputs of more than 16 rows of a sequence and key head, 2^-8.
    Parts below bf16's smallest are below 2^-126 of the largest.
  - Scores: fp32 sums of products of bf16 (two parts of an fp16 query: exact, twice the terms), off by at most
    2 * (D / 8 + 2) * 2^-24 * scale * sum |q k| (instructions add 16 products or more at once), and the roundings of the
@@ -193,7 +194,7 @@ class Case:
         return ref
 
 
-def tolerance(q, k, keys, mag, ref, rlse, out_type, scale=None, one_part=True):
+def tolerance(q, k, keys, mag, ref, rlse, out_type, scale=None):
     """(of out, of lse); see the head of the file."""
     D = q.shape[-1]
     s = D ** -0.5 if scale is None else scale
@@ -201,7 +202,7 @@ def tolerance(q, k, keys, mag, ref, rlse, out_type, scale=None, one_part=True):
     qk = s * q.double().norm(dim=-1, keepdim=True) * kmax  # bounds scale * sum |q k|
     e = 2 * (D / 8 + 2) * 2.0 ** -24 * qk
     rest = (keys / 16 + 4) * 2.0 ** -24
-    parts = {torch.float32: 2.0 ** -27, torch.float16: 2.0 ** -18}.get(out_type, 2.0 ** -9)
+    parts = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -16}.get(out_type, 2.0 ** -8)
     tol = (2 * e + parts + 2 * rest) * mag + torch.finfo(out_type).eps / 2 * ref.abs() * (1 + 2.0 ** -8) + 1e-30
     if out_type == torch.float16:
         tol = tol + 2.0 ** -25
