@@ -51,10 +51,14 @@ struct Attn4Args : AttnArgs {
     int pages, page_shift;  // pages of 1 << page_shift tokens
     int head_bytes;         // of a page
     int groups;             // of 32 values in a row
+    char *notes;            // of the tiles, in the workspace
+    int tiles;              // of which there is room for
 };
+constexpr int kNoteBytes = 32;
 
 struct Attn4Plan {
     AttnPart main;
+    int64_t notes_off;  // in the workspace
     size_t bytes;
 };
 

@@ -26,6 +26,109 @@ namespace {
 
 using V8 = bf16x8;
 
+// -------------------------------------------------------------------------- work items
+//
+// Items are those of csrc/attention_items.h. Where up to four sequences fall to a lane, their lengths are loaded
+// side by side and kept, instead of one wave's worth after the other, twice (300 decoding sequences: XXX).
+// The tile's number among all sequences' goes with the item: its first slice notes for the joining where the tile's
+// results lie, and the first item of all how many tiles there are.
+
+struct Item4 : Item {
+    int number;  // of the tile
+};
+
+// What the joining needs of a tile: its first slot and slices, and its sequence's queries.
+struct TileNote {
+    int slot, pieces, tile, q0, nq, pad[3];
+};
+static_assert(sizeof(TileNote) == kNoteBytes, "room in the workspace");
+
+template <int C>
+__device__ inline bool find_among(const Attn4Args &a, int bm, int id, Item4 &it)
+{
+    const int lane = threadIdx.x & 63;
+    Seq s[C];
+    float work = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        s[c] = Seq{0, 0, 0, 0};
+        if (64 * c + lane < a.B)
+            s[c] = load_seq(a, 64 * c + lane);
+    }
+    it.unit = 1 << 30;
+    if (a.target) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            work += (float)row_tiles(a, s[c], bm) * (float)key_units(s[c]);
+        work = __uint_as_float(wave_reduce_bits(__float_as_uint(work), [](uint32_t x, uint32_t y) {
+            return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+        }));
+        it.unit = uniform(max(a.min_units, (int)fminf(ceilf(work / (float)a.target), 1e9f)));
+    }
+    int tiles_before = 0, items_before = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int tiles = row_tiles(a, s[c], bm), items = tiles * pieces_of(s[c], it.unit);
+        const int ti = wave_scan(tiles), ii = wave_scan(items);
+        const uint64_t past = __ballot(items_before + ii > id);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            it.s.q0 = __builtin_amdgcn_readlane(s[c].q0, l);
+            it.s.nq = __builtin_amdgcn_readlane(s[c].nq, l);
+            it.s.k0 = __builtin_amdgcn_readlane(s[c].k0, l);
+            it.s.nk = __builtin_amdgcn_readlane(s[c].nk, l);
+            it.base = items_before + __builtin_amdgcn_readlane(ii - items, l);
+            it.pieces = uniform(pieces_of(it.s, it.unit));
+            // later tiles of a prompt see more keys: they come first
+            it.tile = row_tiles(a, it.s, bm) - 1 - (id - it.base) / it.pieces;
+            it.piece = (id - it.base) % it.pieces;
+            it.number = tiles_before + __builtin_amdgcn_readlane(ti - tiles, l) + it.tile;
+            return true;
+        }
+        tiles_before += __builtin_amdgcn_readlane(ti, 63);
+        items_before += __builtin_amdgcn_readlane(ii, 63);
+    }
+    return false;
+}
+
+__device__ inline bool find_item4(const Attn4Args &a, int bm, int id, Item4 &it)
+{
+    if (a.B <= 64)
+        return find_among<1>(a, bm, id, it);
+    if (a.B <= 256)
+        return find_among<4>(a, bm, id, it);
+    if (a.B <= 1024)
+        return find_among<16>(a, bm, id, it);
+    if (!find_item(a, bm, id, false, it))
+        return false;
+    int before = 0;
+    for (int b = threadIdx.x & 63; b < it.s.k0; b += 64)
+        before += row_tiles(a, load_seq(a, b), bm);
+    it.number = wave_sum_i32(before) + it.tile;
+    return true;
+}
+
+// Item `id` of key head `head`, and what the joining is told of it; false: there are fewer.
+__device__ inline bool take_item(const Attn4Args &a, int bm, int id, int head, Item4 &it)
+{
+    TileNote *notes = reinterpret_cast<TileNote *>(a.notes);  // the first one: the number of tiles
+    const bool found = find_item4(a, bm, id, it);
+    if (a.target && head == 0 && threadIdx.x < 64) {
+        if (id == 0) {
+            int tiles = 0;
+            for (int b = threadIdx.x; b < a.B; b += 64)
+                tiles += row_tiles(a, load_seq(a, b), bm);
+            tiles = wave_sum_i32(tiles);
+            if (threadIdx.x == 0)
+                notes[0].pieces = tiles;
+        }
+        // (sequences that overlap may have more tiles than there is room for: those are not joined)
+        if (found && it.piece == 0 && it.number < a.tiles && threadIdx.x == 0)
+            notes[1 + it.number] = TileNote{first_item(a, it, bm), it.pieces, it.tile, it.s.q0, it.s.nq, {0, 0, 0}};
+    }
+    return found;
+}
+
 // A wave's view of a sequence's row of the table: 64 entries of it in the lanes.
 struct PageWindow {
     const int *row;
@@ -202,8 +305,8 @@ __device__ __forceinline__ void attn4_tile(const Attn4Args &a, int block, char *
     const int rg = HALVES == 2 ? wave & 1 : wave;        // the wave's 32 rows
     const int part0 = HALVES == 2 ? wave >> 1 : 0;       // its first 32-key part of a block
     const int id = block / a.Hkv, head = block % a.Hkv;
-    Item it;
-    if (!find_item(a, ROWS, id, false, it))
+    Item4 it;
+    if (!take_item(a, ROWS, id, head, it))
         return;
     const Seq s = it.s;
 
@@ -546,8 +649,8 @@ __device__ __forceinline__ void attn4_few(const Attn4Args &a, int block, char *b
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int id = block / a.Hkv, head = block % a.Hkv;
-    Item it;
-    if (!find_item(a, kFewRows, id, false, it))
+    Item4 it;
+    if (!take_item(a, kFewRows, id, head, it))
         return;
     const Seq s = it.s;
     const int rows = s.nq * a.G;
@@ -803,6 +906,122 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn4_tile(Attn4Args 
     attn4_tile<E, DP, WIDE, HALVES>(a, blockIdx.x, kbuf0, kbuf1, vbuf0, vbuf1, &notes);
 }
 
+// ------------------------------------------------------------------------------- joining
+//
+// k_attn4_join: a row's slices joined by their lse, out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max), as
+// k_attn_combine of csrc/attention.hip does, from the notes that the items left.
+
+constexpr int kJoinGroups = 8;  // and the largest number of rows of a workgroup
+
+template <typename TO>
+__global__ __launch_bounds__(32 * kJoinGroups) void k_attn4_join(Attn4Args a, int bm)
+{
+    __shared__ f32x4 sums[kJoinGroups][2][32];
+    __shared__ float stat[kJoinGroups][2];
+    const int l32 = threadIdx.x & 31, group = threadIdx.x >> 5;
+    const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+    const TileNote *notes = reinterpret_cast<const TileNote *>(a.notes);
+    if (id >= notes[0].pieces)
+        return;
+    const TileNote tile = notes[1 + id];
+    const int pieces = tile.pieces, slot = tile.slot;
+    if (pieces == 1 || slot + pieces > a.items)
+        return;  // written by its one item; or tiles of sequences that overlap, without room
+    const int rows = tile.nq * a.G;
+    const int r0 = blockIdx.y * kJoinGroups;
+    const int here = min(min(bm - r0, kJoinGroups), rows - tile.tile * bm - r0);  // rows of this workgroup
+    if (here <= 0)
+        return;
+    const int ways = 32 - __builtin_clz(2 * here - 1) - 1;  // log2 of here rounded up to a power of two
+    const int gp = kJoinGroups >> ways;                              // groups of a row
+    const int r = r0 + (group & ((1 << ways) - 1)), part = group >> ways;
+    const int row = tile.tile * bm + r;
+    const bool live = r < r0 + here;
+    const int n = pieces;
+    float m = -INFINITY, total = 0.f;
+    f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+    const int c0 = 4 * l32 < a.D ? 4 * l32 : 0, c1 = 128 + 4 * l32 < a.D ? 128 + 4 * l32 : 0;
+    if (live)
+        for (int i = part; i < n; i += 4 * gp) {
+            float v[4];
+            f32x4 x0[4], x1[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = min(i + u * gp, n - 1);
+                const int64_t at = ((int64_t)(slot + j) * a.Hkv + head) * bm + r;
+                const float *o = a.ws_o + at * a.D;
+                v[u] = a.ws_l[at];
+                x0[u] = *reinterpret_cast<const f32x4 *>(o + c0);
+                if (a.D > 128)
+                    x1[u] = *reinterpret_cast<const f32x4 *>(o + c1);
+            }
+            float mx = m;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (i + u * gp >= n) {  // the last slice again: not taken (0 * inf would be NaN)
+                    v[u] = -INFINITY;
+                    x0[u] = x1[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+                mx = fmaxf(mx, v[u]);
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx, f = expf(m - ref);
+            total *= f;
+            s0 *= f;
+            s1 *= f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float w = expf(v[u] - ref);
+                total += w;
+                s0 += x0[u] * w;
+                if (a.D > 128)
+                    s1 += x1[u] * w;
+            }
+            m = mx;
+        }
+    if (gp > 1) {
+        sums[group][0][l32] = s0;
+        sums[group][1][l32] = s1;
+        if (l32 == 0) {
+            stat[group][0] = m;
+            stat[group][1] = total;
+        }
+        __syncthreads();
+        if (part)
+            return;
+        float mx = m;
+        for (int q = 1; q < gp; ++q)
+            mx = fmaxf(mx, stat[group + (q << ways)][0]);
+        const float ref = mx == -INFINITY ? 0.f : mx, f = expf(m - ref);
+        total *= f;
+        s0 *= f;
+        s1 *= f;
+        for (int q = 1; q < gp; ++q) {
+            const int g = group + (q << ways);
+            const float w = expf(stat[g][0] - ref);
+            total += stat[g][1] * w;
+            s0 += sums[g][0][l32] * w;
+            s1 += sums[g][1][l32] * w;
+        }
+        m = mx;
+    }
+    if (!live)
+        return;
+    const int token = row / a.G, qh = head * a.G + row % a.G;
+    const int64_t at = (int64_t)(tile.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    TO *dst = static_cast<TO *>(a.out) + at;
+    if (4 * l32 < a.D) {
+        const float y[4] = {s0[0] * inv, s0[1] * inv, s0[2] * inv, s0[3] * inv};
+        store4(dst + 4 * l32, y);
+    }
+    if (128 + 4 * l32 < a.D) {
+        const float y[4] = {s1[0] * inv, s1[1] * inv, s1[2] * inv, s1[3] * inv};
+        store4(dst + 128 + 4 * l32, y);
+    }
+    if (a.lse && l32 == 0)
+        a.lse[(int64_t)(tile.q0 + token) * a.Hq + qh] = total == 0.f ? -INFINITY : m + logf(total);
+}
+
 // --------------------------------------------------------------------------------- plans
 
 template <typename E, int DP, bool WIDE>
@@ -829,10 +1048,10 @@ hipError_t run_dim4(const Attn4Args &a, const Attn4Plan &p, hipStream_t s)
 }
 
 template <typename TO>
-hipError_t run_combine4(const Attn4Args &a, const Attn4Plan &p, hipStream_t s)
+hipError_t run_join4(const Attn4Args &a, const Attn4Plan &p, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.main.tiles * a.Hkv), (unsigned)((p.main.bm + kJoinGroups - 1) / kJoinGroups));
-    k_attn_combine<TO><<<grid, 32 * kJoinGroups, 0, s>>>(a, Attn4Args{}, p.main.bm, p.main.bm);
+    k_attn4_join<TO><<<grid, 32 * kJoinGroups, 0, s>>>(a, p.main.bm);
     return hipGetLastError();
 }
 
@@ -859,7 +1078,8 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
         p.items = p.tiles * (most > 1 ? most : 1);
     const int64_t slots = p.target ? p.items * Hkv * p.bm : 0;
     p.l_off = round_up(slots * D * 4, 256);
-    plan.bytes = (size_t)(p.l_off + round_up(slots * 4, 256));
+    plan.notes_off = p.l_off + round_up(slots * 4, 256);
+    plan.bytes = (size_t)(plan.notes_off + (p.target ? round_up((1 + p.tiles) * kNoteBytes, 256) : 0));
     return plan;
 }
 
@@ -872,14 +1092,16 @@ hipError_t launch_attention4(const Attn4Args &args, const Attn4Plan &p, int type
     a.min_units = p.main.min_units;
     a.ws_o = reinterpret_cast<float *>(ws);
     a.ws_l = reinterpret_cast<float *>(ws + p.main.l_off);
+    a.notes = ws + p.notes_off;
+    a.tiles = (int)p.main.tiles;
     const bool wide = out_type == kF32;
     hipError_t e = type == kBF16 ? (wide ? run_dim4<bf16_t, true>(a, p, s) : run_dim4<bf16_t, false>(a, p, s))
                                  : (wide ? run_dim4<f16_t, true>(a, p, s) : run_dim4<f16_t, false>(a, p, s));
     if (e != hipSuccess || !p.main.target)
         return e;
-    return wide            ? run_combine4<float>(a, p, s)
-           : type == kBF16 ? run_combine4<bf16_t>(a, p, s)
-                           : run_combine4<f16_t>(a, p, s);
+    return wide            ? run_join4<float>(a, p, s)
+           : type == kBF16 ? run_join4<bf16_t>(a, p, s)
+                           : run_join4<f16_t>(a, p, s);
 }
 
 }  // namespace bt

@@ -1,5 +1,5 @@
-// What the attention kernels share: element types, the work items that every workgroup derives from the
-// sequences' lengths, and the joining of the items' results.
+// What the attention kernels share: element types, and the work items that every workgroup derives from the
+// sequences' lengths.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -274,162 +274,6 @@ template <int DP>
 __device__ inline int swizzle(int row)
 {
     return DP >= 128 ? ((row & 3) << 2 | (row >> 2 & 3)) : ((row >> 1 & 1) << 2 | (row >> 2 & 3));
-}
-
-// ------------------------------------------------------------------------------- joining
-//
-// k_attn_combine: a row's slices, and with a shared prefix the prefix's slices of the same row,
-// joined by their lse: out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max). 32 lanes read a
-// row; the groups of a workgroup are spread over its rows, so that the slices of few rows are read
-// side by side (four in flight in each group) and joined through LDS. Latency is all there is to it:
-// 16 groups cost 0.6-0.9 us more in small calls, 32 groups 1-3 us, fewer workgroups fitting a CU.
-
-constexpr int kJoinGroups = 8;  // and the largest number of rows of a workgroup
-
-template <typename TO, typename Args>
-__global__ __launch_bounds__(32 * kJoinGroups) void k_attn_combine(Args a, Args pre, int bm, int pre_bm)
-{
-    __shared__ f32x4 sums[kJoinGroups][2][32];
-    __shared__ float stat[kJoinGroups][2];
-    const int l32 = threadIdx.x & 31, group = threadIdx.x >> 5;
-    const int id = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
-    Item it;
-    if (!find_item(a, bm, id, true, it))
-        return;
-    const bool shared = pre.shared;
-    if (!shared && it.pieces == 1)
-        return;  // written by its one item
-    const int rows = it.s.nq * a.G;
-    const int slot = first_item(a, it, bm);
-    if (slot + it.pieces > a.items)
-        return;  // more tiles than sequences that do not overlap can have: not computed
-    const int r0 = blockIdx.y * kJoinGroups;
-    const int here = min(min(bm - r0, kJoinGroups), rows - it.tile * bm - r0);  // rows of this workgroup
-    if (here <= 0)
-        return;
-    const int ways = 32 - __builtin_clz(2 * here - 1) - 1;  // log2 of here rounded up to a power of two
-    const int gp = kJoinGroups >> ways;                              // groups of a row
-    const int r = r0 + (group & ((1 << ways) - 1)), part = group >> ways;
-    const int row = it.tile * bm + r;
-    const bool live = r < r0 + here;
-    // the prefix's items of this row
-    int pslot = 0, pn = 0, prow = 0;
-    if (shared) {
-        Item p;
-        find_item(pre, pre_bm, 0, true, p);
-        const int all = min(it.s.q0 * pre.G + row, pre.T * pre.G - 1);  // T * heads <= 2^30
-        p.tile = all / pre_bm;
-        prow = all % pre_bm;
-        pslot = first_item(pre, p, pre_bm);
-        pn = p.pieces;
-    }
-    const int n = it.pieces + pn;
-    float m = -INFINITY, total = 0.f;
-    f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
-    const int c0 = 4 * l32 < a.D ? 4 * l32 : 0, c1 = 128 + 4 * l32 < a.D ? 128 + 4 * l32 : 0;
-    if (live)
-        for (int i = part; i < n; i += 4 * gp) {
-            float v[4];
-            f32x4 x0[4], x1[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int j = min(i + u * gp, n - 1);
-                const bool own = j < it.pieces;
-                const int64_t at = own ? ((int64_t)(slot + j) * a.Hkv + head) * bm + r
-                                       : ((int64_t)(pslot + j - it.pieces) * a.Hkv + head) * pre_bm + prow;
-                const float *o = (own ? a.ws_o : pre.ws_o) + at * a.D;
-                v[u] = (own ? a.ws_l : pre.ws_l)[at];
-                x0[u] = *reinterpret_cast<const f32x4 *>(o + c0);
-                if (a.D > 128)
-                    x1[u] = *reinterpret_cast<const f32x4 *>(o + c1);
-            }
-            float mx = m;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (i + u * gp >= n) {  // the last slice again: not taken (0 * inf would be NaN)
-                    v[u] = -INFINITY;
-                    x0[u] = x1[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-                mx = fmaxf(mx, v[u]);
-            }
-            const float ref = mx == -INFINITY ? 0.f : mx, f = expf(m - ref);
-            total *= f;
-            s0 *= f;
-            s1 *= f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float w = expf(v[u] - ref);
-                total += w;
-                s0 += x0[u] * w;
-                if (a.D > 128)
-                    s1 += x1[u] * w;
-            }
-            m = mx;
-        }
-    if (gp > 1) {
-        sums[group][0][l32] = s0;
-        sums[group][1][l32] = s1;
-        if (l32 == 0) {
-            stat[group][0] = m;
-            stat[group][1] = total;
-        }
-        __syncthreads();
-        if (part)
-            return;
-        float mx = m;
-        for (int q = 1; q < gp; ++q)
-            mx = fmaxf(mx, stat[group + (q << ways)][0]);
-        const float ref = mx == -INFINITY ? 0.f : mx, f = expf(m - ref);
-        total *= f;
-        s0 *= f;
-        s1 *= f;
-        for (int q = 1; q < gp; ++q) {
-            const int g = group + (q << ways);
-            const float w = expf(stat[g][0] - ref);
-            total += stat[g][1] * w;
-            s0 += sums[g][0][l32] * w;
-            s1 += sums[g][1][l32] * w;
-        }
-        m = mx;
-    }
-    if (!live)
-        return;
-    const f32x4 both = s0 + s1;
-    const bool odd = not_finite((both[0] + both[1]) + (both[2] + both[3]));
-    if (__builtin_expect(odd && total > 0.f && total < INFINITY, 0)) {
-        // a weight of 0 is too small for fp32, not none: what is infinite or NaN in a slice stays
-        f32x4 b0 = {0.f, 0.f, 0.f, 0.f}, b1 = b0;
-        for (int j = 0; j < n; ++j) {
-            const bool own = j < it.pieces;
-            const int64_t at = own ? ((int64_t)(slot + j) * a.Hkv + head) * bm + r
-                                   : ((int64_t)(pslot + j - it.pieces) * a.Hkv + head) * pre_bm + prow;
-            const float *o = (own ? a.ws_o : pre.ws_o) + at * a.D;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                b0[i] += not_finite(o[c0 + i]) ? o[c0 + i] : 0.f;
-                b1[i] += a.D > 128 && not_finite(o[c1 + i]) ? o[c1 + i] : 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s0[i] = b0[i] == 0.f ? s0[i] : b0[i];
-            s1[i] = b1[i] == 0.f ? s1[i] : b1[i];
-        }
-    }
-    const int token = row / a.G, qh = head * a.G + row % a.G;
-    const int64_t at = (int64_t)(it.s.q0 + token) * a.o_row + (int64_t)qh * a.o_head;
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    TO *dst = static_cast<TO *>(a.out) + at;
-    if (4 * l32 < a.D) {
-        const float y[4] = {s0[0] * inv, s0[1] * inv, s0[2] * inv, s0[3] * inv};
-        store4(dst + 4 * l32, y);
-    }
-    if (128 + 4 * l32 < a.D) {
-        const float y[4] = {s1[0] * inv, s1[1] * inv, s1[2] * inv, s1[3] * inv};
-        store4(dst + 128 + 4 * l32, y);
-    }
-    if (a.lse && l32 == 0)
-        a.lse[(int64_t)(it.s.q0 + token) * a.Hq + qh] = total == 0.f ? -INFINITY : m + logf(total);
 }
 
 }  // namespace
