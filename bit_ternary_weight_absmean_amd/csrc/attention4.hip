@@ -37,6 +37,11 @@ struct Item4 : Item {
     int number;  // of the tile
 };
 
+// The fewest units of a slice by the longest sequence's: no more than about 48 slices of a tile, which the joining
+// reads one behind the other (one token over 30000 keys in 118 slices: 29.5 us, in 59: 21.8), and four units where there
+// are enough (8000 keys, two: 16.7 us, four: 13.4; 777 keys, two: 9.8, four: 10.7).
+__device__ inline int slice_floor(int longest) { return max(longest / 48, min(4, longest / 6)); }
+
 // What the joining needs of a tile: its first slot and slices, and its sequence's queries.
 struct TileNote {
     int slot, pieces, tile, q0, nq, pad[3];
@@ -63,7 +68,12 @@ __device__ inline bool find_among(const Attn4Args &a, int bm, int id, Item4 &it)
         work = __uint_as_float(wave_reduce_bits(__float_as_uint(work), [](uint32_t x, uint32_t y) {
             return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
         }));
-        it.unit = uniform(max(a.min_units, (int)fminf(ceilf(work / (float)a.target), 1e9f)));
+        int longest = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            longest = max(longest, key_units(s[c]));
+        longest = (int)wave_reduce_bits((uint32_t)longest, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+        it.unit = uniform(max(max(a.min_units, slice_floor(longest)), (int)fminf(ceilf(work / (float)a.target), 1e9f)));
     }
     int tiles_before = 0, items_before = 0;
 #pragma unroll
@@ -1061,17 +1071,23 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
 {
     Attn4Plan plan{};
     AttnPart &p = plan.main;
-    const int64_t rows = T * (Hq / Hkv), seqs = B < T ? B : T;
-    // mean rows of a sequence: up to 16, one small tile each
-    p.bm = rows <= kFewRows * seqs ? kFewRows : kTileRows;
-    if (p.bm == kTileRows && (rows / kTileRows + seqs) * Hkv < 512)
-        p.bm = kSmallRows;
+    const int64_t rows = T * (Hq / Hkv), seqs = B < T ? B : T;  // the sequences that have rows
+    // Rows of a tile, by the mean rows of a sequence: up to 16, one small tile each; up to 64, one of 64. Longer ones take
+    // tiles of 128, or of 64 where those would not fill the CUs and there are no long caches to cut instead (capacity of
+    // twice the call's tokens or more; 7B prompts of 813 tokens behind 4096 keys: 79 us cut, 118 uncut with 64 rows; packed
+    // 2B prompts of 2048 tokens 45 and 36).
+    const bool few = rows <= kFewRows * seqs;
+    const int64_t tiles128 = rows / kTileRows + seqs;
+    const bool fills = tiles128 * Hkv >= 512, cached = most_keys > 2 * T;
+    p.bm = few ? kFewRows : rows <= kSmallRows * seqs || !(fills || cached) ? kSmallRows : kTileRows;
     p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
-    const int64_t target = ((p.bm == kFewRows ? 2048 : 384) + Hkv - 1) / Hkv;
-    p.target = p.bm == kFewRows || 3 * p.tiles < target ? target : 0;
-    if (most_keys <= 512)
-        p.target = 0;
-    p.min_units = 4;
+    // Keys are cut into slices where the tiles alone leave CUs idle: so that about four workgroups of few rows or two
+    // of many share a CU. 64 tokens over slabs of up to 8192 keys, 2B heads: 104 us uncut, 55 cut; 300 tokens over 300 to
+    // 1200 keys, eight key heads: 66 uncut, 76 cut.
+    const int64_t target = ((few ? 1024 : 512) + Hkv - 1) / Hkv;
+    const bool cut = few ? p.tiles * Hkv < 768 : p.bm == kSmallRows ? cached : !fills;
+    p.target = cut && most_keys > 512 ? target : 0;
+    p.min_units = few ? 2 : 4;
     const int64_t most = ((most_keys + kUnit - 1) / kUnit + p.min_units - 1) / p.min_units;
     p.items = p.tiles + (p.target ? p.target + 8 : 0);
     if (p.target && p.tiles * (most > 1 ? most : 1) < p.items)
