@@ -70,18 +70,15 @@ __device__ inline void copy_piece(const PagesArgs &a, int64_t src, int64_t dst, 
     char *to = a.pool + layer * a.layer_stride + dst * a.page_bytes;
     const int64_t lo = (int64_t)piece * kCopyBytes, hi = min(lo + kCopyBytes, a.page_bytes);
     constexpr int U = kCopyBytes / 16 / 256;
-    uint4 x[U];
+    v4i x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)  // past the end: the last piece again, not stored
+        x[u] = *reinterpret_cast<const v4i *>(from + min(lo + (u * 256 + (int)threadIdx.x) * 16, hi - 16));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t at = lo + (u * 256 + threadIdx.x) * 16;
         if (at < hi)
-            x[u] = *reinterpret_cast<const uint4 *>(from + at);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t at = lo + (u * 256 + threadIdx.x) * 16;
-        if (at < hi)
-            *reinterpret_cast<uint4 *>(to + at) = x[u];
+            *reinterpret_cast<v4i *>(to + at) = x[u];
     }
 }
 
@@ -107,6 +104,12 @@ unsigned copy_grid(const PagesArgs &a, int64_t count)
 
 // ---------------------------------------------------------------------------------- grow
 //
+// One workgroup hands out the pages: what every sequence needs, the free pages in order, who gets them. Up to 1024
+// sequences it keeps all of it in registers and LDS and writes the tables, the counts and the tokens' places itself
+// (each reading of memory behind another costs about 0.7 us here: first lengths, then the last pages' numbers and the
+// counts from `first` on, then the last pages' counts); the second launch copies pages. For more sequences, or more
+// than 2048 tokens, that launch also fills in the tables or the places.
+//
 // Workspace: [0] pages handed out, [1] pages copied, then per sequence the end of its demand (inclusive sum) and
 // the page slot it starts at, then the list of copied pages (from, to), then the free pages.
 
@@ -118,54 +121,68 @@ __device__ __host__ inline GrowSpace grow_space(int *ws, int64_t B)
     return {ws, ws + 4, ws + 4 + B, ws + 4 + 2 * B, ws + 4 + 3 * B, ws + 4 + 4 * B};
 }
 
-__global__ __launch_bounds__(kPlan) void k_pages_plan(PagesArgs a)
+constexpr int kTokensHere = 2 * kPlan;  // places filled in by the one workgroup
+
+// First index i in [0, n) with x[i] > v (n: none); x does not fall.
+template <typename P>
+__device__ inline int first_above(P x, int n, int v)
 {
-    __shared__ int lds[kPlanWaves];
-    __shared__ int freed;
-    const GrowSpace ws = grow_space(a.ws, a.B);
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    if (tid == 0)
-        freed = a.P;
-    // what every sequence needs
-    int asked = 0;
-    for (int c = 0; c < a.B; c += kPlan) {
-        const int b = c + tid;
-        int need = 0, slot = -1;
-        if (b < a.B) {
-            const int n = new_tokens(a, b).n, len = length_of(a, b);
-            const int have = pages_for(len, a.page_shift), want = pages_for((int64_t)len + n, a.page_shift);
-            if (n > 0 && want <= a.W) {
-                bool copy = false;
-                if (len & ((1 << a.page_shift) - 1)) {
-                    const int tail = a.table[(int64_t)b * a.W + have - 1];
-                    copy = tail >= 0 && tail < a.P && a.refs[tail] > 1;
-                }
-                need = want - have + copy;
-                slot = have - copy;
-            }
-        }
-        int total;
-        const int before = block_scan(need, lds, total);
-        if (b < a.B) {
-            ws.end[b] = asked + before + need;
-            ws.slot[b] = slot;
-        }
-        asked += total;
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (x[mid] > v)
+            hi = mid;
+        else
+            lo = mid + 1;
     }
-    // the first `asked` free pages
-    constexpr int kPer = 8, kStep = kPlan * kPer;
-    int found = 0, base = asked > 0 ? min(max(*a.first, 0), a.P) : a.P;
-    for (; base < a.P && found < asked; base += kStep) {
-        const int mine = base + wave * 64 * kPer;
+    return lo;
+}
+
+// Need of a sequence: pages, the slot of the first of them (-1: none to be had, or nothing asked), and the page that is
+// copied into it (-1: none).
+struct Need {
+    int pages, slot, from;
+};
+__device__ inline Need need_of(const PagesArgs &a, int b, int n, int len)
+{
+    Need x = {0, -1, -1};
+    const int have = pages_for(len, a.page_shift), want = pages_for((int64_t)len + n, a.page_shift);
+    if (n > 0 && want <= a.W) {
+        if (len & ((1 << a.page_shift) - 1)) {
+            const int tail = a.table[(int64_t)b * a.W + have - 1];
+            if (tail >= 0 && tail < a.P && a.refs[tail] > 1)
+                x.from = tail;
+        }
+        x.pages = want - have + (x.from >= 0);
+        x.slot = have - (x.from >= 0);
+    }
+    return x;
+}
+
+// The first `asked` free pages from `base` on, in order, as put(k, page); how many were found. The first step's counts are
+// given (they were loaded before it was known how many pages are wanted).
+constexpr int kPer = 8, kStep = kPlan * kPer;
+__device__ inline void load_refs(const PagesArgs &a, int base, int (&refs)[kPer])
+{
+    const int mine = base + (int)(threadIdx.x >> 6) * 64 * kPer + (int)(threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        refs[i] = mine + i * 64 < a.P ? a.refs[mine + i * 64] : 1;
+}
+template <typename Put>
+__device__ inline int free_pages(const PagesArgs &a, int base, int asked, int (&refs)[kPer], int *lds, Put put)
+{
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    int found = 0;
+    while (base < a.P && found < asked) {
         uint64_t free[kPer];
         int n = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int page = mine + i * 64 + lane;
-            free[i] = __ballot(page < a.P && a.refs[page] == 0);
+            free[i] = __ballot(refs[i] == 0);
             n += __popcll(free[i]);
         }
-        __syncthreads();
+        __syncthreads();  // lds may still be read from before
         if (lane == 0)
             lds[wave] = n;
         __syncthreads();
@@ -178,10 +195,138 @@ __global__ __launch_bounds__(kPlan) void k_pages_plan(PagesArgs a)
         for (int i = 0; i < kPer; ++i) {
             const int k = at + rank_in(free[i]);
             if ((free[i] >> lane & 1) && k < asked)
-                ws.free[k] = mine + i * 64 + lane;
+                put(k, base + wave * 64 * kPer + i * 64 + lane);
             at += __popcll(free[i]);
         }
+        base += kStep;
+        if (base < a.P && found < asked)
+            load_refs(a, base, refs);
     }
+    return found;
+}
+
+// `first` after `taken` of the pages that were asked for are handed out; freed: the lowest page that may be free now.
+__device__ inline void set_first(const PagesArgs &a, const int *free, int taken, int found, int freed)
+{
+    *a.first = min(taken > 0 ? free[taken - 1] + 1 : found > 0 ? free[0] : a.P, freed);
+}
+
+// The place and number of new token t of sequence b, whose new pages are free[start ..] from slot on.
+struct Token {
+    int row, at;
+};
+__device__ inline Token place_token(const PagesArgs &a, int b, int t, int from, int len, int slot, int start, int end,
+                                    const int *free)
+{
+    const int at = len + t - from;
+    if (slot < 0)
+        return {-1, at};
+    const int p = at >> a.page_shift;
+    // what this call writes to the table is taken from the list
+    const int page = p >= slot && start + p - slot < end ? free[start + p - slot] : a.table[(int64_t)b * a.W + p];
+    return {page < 0 ? -1 : page << a.page_shift | (at & ((1 << a.page_shift) - 1)), at};
+}
+
+__global__ __launch_bounds__(kPlan) void k_pages_plan_small(PagesArgs a)
+{
+    __shared__ int lds[kPlanWaves], s_end[kPlan], s_slot[kPlan], s_from[kPlan + 1], s_len[kPlan];
+    __shared__ int freed;
+    const GrowSpace ws = grow_space(a.ws, a.B);
+    const int b = threadIdx.x;
+    const int base = min(max(*a.first, 0), a.P);
+    int refs[kPer];
+    Need x = {0, -1, -1};
+    Range r = {0, 0};
+    int len = 0;
+    if (b < a.B) {
+        r = new_tokens(a, b);
+        len = length_of(a, b);
+    }
+    load_refs(a, base, refs);
+    if (b < a.B)
+        x = need_of(a, b, r.n, len);
+    if (b == 0)
+        freed = a.P;
+    int asked;
+    const int before = block_scan(x.pages, lds, asked), end = before + x.pages;
+    const int found = free_pages(a, base, asked, refs, lds, [&](int k, int page) { ws.free[k] = page; });
+    const bool fits = x.slot >= 0 && (x.pages == 0 || end <= found);
+    const bool copy = fits && x.from >= 0;
+    s_end[b] = end;
+    s_slot[b] = fits ? x.slot : -1;
+    s_from[b] = b < a.B ? r.from : a.T;
+    s_len[b] = len;
+    if (b == 0)
+        s_from[kPlan] = a.T;
+    int taken, copies;
+    block_scan(fits ? x.pages : 0, lds, taken);
+    const int at = block_scan(copy ? 1 : 0, lds, copies);  // (its barriers: the lists are there for all of the workgroup)
+    if (b < a.B) {
+        a.granted[b] = fits ? r.n : 0;
+        if (fits)
+            a.length[b] = len + r.n;
+    }
+    if (copy) {
+        ws.from[at] = x.from;
+        ws.to[at] = ws.free[before];
+        atomicSub(a.refs + x.from, 1);
+        atomicMin(&freed, x.from);  // perhaps free now
+    }
+    for (int k = b; k < taken; k += kPlan) {
+        const int q = first_above(s_end, a.B, k), page = ws.free[k];
+        a.table[(int64_t)q * a.W + s_slot[q] + k - (q ? s_end[q - 1] : 0)] = page;
+        a.refs[page] = 1;
+    }
+    if (a.T <= kTokensHere) {
+        const int last = a.q_start[a.B];
+        for (int t = b; t < a.T; t += kPlan) {
+            Token k = {-1, -1};
+            const int q = first_above(s_from, a.B, t) - 1;  // the last sequence that starts at or before t
+            if (q >= 0 && t < last)
+                k = place_token(a, q, t, s_from[q], s_len[q], s_slot[q], q ? s_end[q - 1] : 0, s_end[q], ws.free);
+            a.rows[t] = k.row;
+            a.positions[t] = k.at;
+        }
+    } else if (b < a.B) {
+        ws.end[b] = s_end[b];
+        ws.slot[b] = s_slot[b];
+    }
+    __syncthreads();
+    if (b == 0) {
+        ws.counts[0] = taken;
+        ws.counts[1] = copies;
+        if (asked > 0)
+            set_first(a, ws.free, taken, found, freed);
+    }
+}
+
+__global__ __launch_bounds__(kPlan) void k_pages_plan(PagesArgs a)
+{
+    __shared__ int lds[kPlanWaves];
+    __shared__ int freed;
+    const GrowSpace ws = grow_space(a.ws, a.B);
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        freed = a.P;
+    // what every sequence needs
+    int asked = 0;
+    for (int c = 0; c < a.B; c += kPlan) {
+        const int b = c + tid;
+        Need x = {0, -1, -1};
+        if (b < a.B)
+            x = need_of(a, b, new_tokens(a, b).n, length_of(a, b));
+        int total;
+        const int before = block_scan(x.pages, lds, total);
+        if (b < a.B) {
+            ws.end[b] = asked + before + x.pages;
+            ws.slot[b] = x.slot;
+        }
+        asked += total;
+    }
+    const int base = asked > 0 ? min(max(*a.first, 0), a.P) : a.P;
+    int refs[kPer];
+    load_refs(a, base, refs);
+    const int found = free_pages(a, base, asked, refs, lds, [&](int k, int page) { ws.free[k] = page; });
     __syncthreads();  // the lists, for all of the workgroup
     // who gets them: those whose demand ends within what was found
     int taken = 0, copies = 0;
@@ -199,8 +344,8 @@ __global__ __launch_bounds__(kPlan) void k_pages_plan(PagesArgs a)
                 if (copy) {
                     from = a.table[(int64_t)b * a.W + slot];
                     to = ws.free[end - need];
-                    if (atomicSub(a.refs + from, 1) == 1)
-                        atomicMin(&freed, from);
+                    atomicSub(a.refs + from, 1);
+                    atomicMin(&freed, from);
                 }
                 a.length[b] = len + n;
             } else {
@@ -222,78 +367,117 @@ __global__ __launch_bounds__(kPlan) void k_pages_plan(PagesArgs a)
     if (tid == 0) {
         ws.counts[0] = taken;
         ws.counts[1] = copies;
-        if (asked > 0) {
-            const int next = taken > 0 ? ws.free[taken - 1] + 1 : found > 0 ? ws.free[0] : a.P;
-            *a.first = min(next, freed);
-        }
+        if (asked > 0)
+            set_first(a, ws.free, taken, found, freed);
     }
 }
 
-// First index i in [0, n) with x[i] > v (n: none); x does not fall.
-__device__ inline int first_above(const int *x, int n, int v)
+// tables, tokens: whether the tables and the places are left to this launch
+__global__ __launch_bounds__(256) void k_pages_grow(PagesArgs a, int tables, int tokens)
 {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (x[mid] > v)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    return lo;
-}
-
-__global__ __launch_bounds__(256) void k_pages_grow(PagesArgs a)
-{
+    __shared__ int s_end[kPlan];
     const GrowSpace ws = grow_space(a.ws, a.B);
-    const int taken = ws.counts[0], copies = ws.counts[1];
-    const int id = blockIdx.x * 256 + threadIdx.x, step = gridDim.x * 256;
-    for (int k = id; k < taken; k += step) {
-        const int b = first_above(ws.end, a.B, k);
-        if (b >= a.B)
-            continue;
-        const int start = b ? ws.end[b - 1] : 0, page = ws.free[k];
-        a.table[(int64_t)b * a.W + ws.slot[b] + k - start] = page;
-        a.refs[page] = 1;
-    }
-    const int mask = (1 << a.page_shift) - 1;
-    for (int t = id; t < a.T; t += step) {
-        const int b = first_above(a.q_start + 1, a.B, t);
-        int row = -1, at = -1;
-        if (b < a.B) {
-            const Range r = new_tokens(a, b);
-            if (t >= r.from && t < r.from + r.n) {
-                at = length_of(a, b) - a.granted[b] + t - r.from;
-                const int slot = ws.slot[b];
-                if (slot >= 0) {
-                    const int p = at >> a.page_shift, start = b ? ws.end[b - 1] : 0;
-                    // what this launch writes to the table is taken from the list
-                    const int page = p >= slot && start + p - slot < ws.end[b] ? ws.free[start + p - slot]
-                                                                              : a.table[(int64_t)b * a.W + p];
-                    row = page < 0 ? -1 : page << a.page_shift | (at & mask);
-                }
-            }
-        }
-        a.rows[t] = row;
-        a.positions[t] = at;
-    }
+    const int copies = ws.counts[1];
     copy_pages(a, copies, [&](int64_t i, int64_t &src, int64_t &dst) {
         src = ws.from[i];
         dst = ws.to[i];
         return true;
     });
+    const int id = blockIdx.x * 256 + threadIdx.x, step = gridDim.x * 256;
+    if (tables)
+        for (int k = id; k < ws.counts[0]; k += step) {
+            const int b = first_above(ws.end, a.B, k);
+            if (b >= a.B)
+                continue;
+            const int start = b ? ws.end[b - 1] : 0, page = ws.free[k];
+            a.table[(int64_t)b * a.W + ws.slot[b] + k - start] = page;
+            a.refs[page] = 1;
+        }
+    if (tokens) {
+        // the sequences' ends nearby where they fit
+        const bool near = a.B <= kPlan;
+        if (near) {
+            for (int i = threadIdx.x; i < a.B; i += 256)
+                s_end[i] = a.q_start[i + 1];
+            __syncthreads();
+        }
+        for (int t = id; t < a.T; t += step) {
+            const int b = near ? first_above(s_end, a.B, t) : first_above(a.q_start + 1, a.B, t);
+            Token k = {-1, -1};
+            if (b < a.B) {
+                const Range r = new_tokens(a, b);
+                if (t >= r.from && t < r.from + r.n)
+                    k = place_token(a, b, t, r.from, length_of(a, b) - a.granted[b], ws.slot[b], b ? ws.end[b - 1] : 0,
+                                    ws.end[b], ws.free);
+            }
+            a.rows[t] = k.row;
+            a.positions[t] = k.at;
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------------- fork
 //
-// One workgroup per sequence. First launch: the rows as they will be, from the parents' rows as they are, and the
-// counts up. Second: the counts of what a sequence held down, and its new row.
-// Workspace: the new lengths, the new rows.
+// Counts go up first, for all pages that are taken, and down only then, for all that are given up. Small tables (kCells
+// entries) in one launch of one workgroup, with a barrier between the two; larger ones in two launches of one
+// workgroup per sequence, the first of which also keeps the rows as they will be in the workspace (the new lengths, the
+// new rows). 8 sequences of 11 pages: XXX.
+
+constexpr int kCells = 8 * kPlan;
 
 __device__ inline bool fork_source(const PagesArgs &a, int b, int &p)
 {
     p = a.parent[b];
     return p >= 0 && p < a.B;
+}
+
+__global__ __launch_bounds__(kPlan) void k_fork_small(PagesArgs a)
+{
+    constexpr int U = kCells / kPlan;
+    const uint32_t cells = (uint32_t)a.B * a.W;
+    int page[U], old[U], now[U];  // what the cell will hold; pages of its sequence before and after (0, 0: it stays)
+    int len = -1;                 // of sequence threadIdx.x
+    if ((int)threadIdx.x < a.B) {
+        int p;
+        const bool from = fork_source(a, threadIdx.x, p);
+        if (!(from && p == (int)threadIdx.x))
+            len = from ? length_of(a, p) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t c = u * kPlan + threadIdx.x;
+        page[u] = -1;
+        old[u] = now[u] = 0;
+        if (c < cells) {
+            const int b = (int)(c / (uint32_t)a.W), i = (int)(c - (uint32_t)b * (uint32_t)a.W);
+            int p;
+            const bool from = fork_source(a, b, p);
+            if (!(from && p == b)) {
+                old[u] = pages_for(length_of(a, b), a.page_shift) - i;
+                now[u] = (from ? pages_for(length_of(a, p), a.page_shift) : 0) - i;
+                if (now[u] > 0) {
+                    page[u] = a.table[(int64_t)p * a.W + i];
+                    if (page[u] >= 0 && page[u] < a.P)
+                        atomicAdd(a.refs + page[u], 1);
+                }
+            }
+        }
+    }
+    __threadfence();
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t c = u * kPlan + threadIdx.x;
+        if (old[u] > 0) {
+            const int was = a.table[c];
+            if (was >= 0 && was < a.P && atomicSub(a.refs + was, 1) == 1)
+                atomicMin(a.first, was);
+        }
+        if (old[u] > 0 || now[u] > 0)
+            a.table[c] = page[u];
+    }
+    if (len >= 0)
+        a.length[threadIdx.x] = len;
 }
 
 __global__ __launch_bounds__(256) void k_fork_take(PagesArgs a)
@@ -372,15 +556,25 @@ __global__ __launch_bounds__(kPlan) void k_compact_count(PagesArgs a)
         compact_space(a.ws, a.P).segment[blockIdx.x] = total;
 }
 
-__global__ __launch_bounds__(kPlan) void k_compact_list(PagesArgs a)
+// counted: whether a launch before counted the segments; otherwise (few of them) every workgroup goes over all counts
+__global__ __launch_bounds__(kPlan) void k_compact_list(PagesArgs a, int counted)
 {
     __shared__ int lds[kPlanWaves];
     const CompactSpace ws = compact_space(a.ws, a.P);
     const int segments = (a.P + kSegment - 1) / kSegment, base = blockIdx.x * kSegment;
     int live = 0, rank = 0, total;
-    for (int i = threadIdx.x; i < segments; i += kPlan) {
-        live += ws.segment[i];
-        rank += i < (int)blockIdx.x ? ws.segment[i] : 0;
+    if (counted) {
+        for (int i = threadIdx.x; i < segments; i += kPlan) {
+            live += ws.segment[i];
+            rank += i < (int)blockIdx.x ? ws.segment[i] : 0;
+        }
+    } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < a.P; i += kPlan) {
+            const int used = a.refs[i] > 0;
+            live += used;
+            rank += i < base ? used : 0;
+        }
     }
     block_scan(live, lds, total);
     live = total;
@@ -459,17 +653,25 @@ size_t pages_workspace_bytes(int64_t B, int64_t W, int64_t P)
 
 hipError_t launch_pages_grow(const PagesArgs &a, hipStream_t s)
 {
-    k_pages_plan<<<1, kPlan, 0, s>>>(a);
+    const bool small = a.B <= kPlan, tokens = !small || a.T > kTokensHere;
+    if (small)
+        k_pages_plan_small<<<1, kPlan, 0, s>>>(a);
+    else
+        k_pages_plan<<<1, kPlan, 0, s>>>(a);
     if (hipError_t e = hipGetLastError())
         return e;
-    const int64_t tokens = ((int64_t)a.T + 255) / 256;
-    const unsigned copies = copy_grid(a, a.B), all = tokens > 4096 ? 4096u : (unsigned)(tokens < 1 ? 1 : tokens);
-    k_pages_grow<<<copies > all ? copies : all, 256, 0, s>>>(a);
+    const int64_t places = tokens ? ((int64_t)a.T + 255) / 256 : 1;
+    const unsigned copies = copy_grid(a, a.B), all = places > 4096 ? 4096u : (unsigned)(places < 1 ? 1 : places);
+    k_pages_grow<<<copies > all ? copies : all, 256, 0, s>>>(a, !small, tokens);
     return hipGetLastError();
 }
 
 hipError_t launch_pages_fork(const PagesArgs &a, hipStream_t s)
 {
+    if (a.B <= kPlan && (int64_t)a.B * a.W <= kCells) {
+        k_fork_small<<<1, kPlan, 0, s>>>(a);
+        return hipGetLastError();
+    }
     k_fork_take<<<(unsigned)a.B, 256, 0, s>>>(a);
     if (hipError_t e = hipGetLastError())
         return e;
@@ -480,10 +682,13 @@ hipError_t launch_pages_fork(const PagesArgs &a, hipStream_t s)
 hipError_t launch_pages_compact(const PagesArgs &a, hipStream_t s)
 {
     const unsigned segments = (unsigned)((a.P + kSegment - 1) / kSegment);
-    k_compact_count<<<segments, kPlan, 0, s>>>(a);
-    if (hipError_t e = hipGetLastError())
-        return e;
-    k_compact_list<<<segments, kPlan, 0, s>>>(a);
+    const bool counted = segments > 8;
+    if (counted) {
+        k_compact_count<<<segments, kPlan, 0, s>>>(a);
+        if (hipError_t e = hipGetLastError())
+            return e;
+    }
+    k_compact_list<<<segments, kPlan, 0, s>>>(a, counted);
     if (hipError_t e = hipGetLastError())
         return e;
     const int64_t cells = ((int64_t)a.B * a.W + 255) / 256;
