@@ -29,7 +29,7 @@ using V8 = bf16x8;
 // -------------------------------------------------------------------------- work items
 //
 // Items are those of csrc/attention_items.h. Where up to four sequences fall to a lane, their lengths are loaded
-// side by side and kept, instead of one wave's worth after the other, twice (300 decoding sequences: XXX).
+// side by side and kept, instead of one wave's worth after the other, twice (300 decoding sequences: 68.0 us, side by side 66.7).
 // The tile's number among all sequences' goes with the item: its first slice notes for the joining where the tile's
 // results lie, and the first item of all how many tiles there are.
 
@@ -1081,10 +1081,11 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
     const bool fills = tiles128 * Hkv >= 512, cached = most_keys > 2 * T;
     p.bm = few ? kFewRows : rows <= kSmallRows * seqs || !(fills || cached) ? kSmallRows : kTileRows;
     p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
-    // Keys are cut into slices where the tiles alone leave CUs idle: so that about four workgroups of few rows or two
-    // of many share a CU. 64 tokens over slabs of up to 8192 keys, 2B heads: 104 us uncut, 55 cut; 300 tokens over 300 to
-    // 1200 keys, eight key heads: 66 uncut, 76 cut.
-    const int64_t target = ((few ? 1024 : 512) + Hkv - 1) / Hkv;
+    // Keys are cut into slices where the tiles alone leave CUs idle (64 tokens over slabs of up to 8192 keys, five key
+    // heads: 104 us uncut, 55 cut; 300 tokens over 300 to 1200 keys, eight key heads: 66 uncut, 76 cut): into about four
+    // workgroups of few rows a CU, or a little under the two of many that a CU holds, since the tiles' last slices come on
+    // top (256 tokens over 8192 keys, five key heads: 65 us aiming at 512, 49 at 480, 55 at 384).
+    const int64_t target = ((few ? 1024 : 480) + Hkv - 1) / Hkv;
     const bool cut = few ? p.tiles * Hkv < 768 : p.bm == kSmallRows ? cached : !fills;
     p.target = cut && most_keys > 512 ? target : 0;
     p.min_units = few ? 2 : 4;
