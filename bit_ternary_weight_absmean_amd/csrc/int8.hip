@@ -27,11 +27,15 @@ __global__ __launch_bounds__(256) void k_int8_pack(const int8_t *W, int64_t ld, 
     const int64_t block = id >> 6;
     const int lane = (int)(id & 63);
     const int64_t n = block / KC * 16 + (lane & 15), k = block % KC * 64 + 16 * (lane >> 4);
-    __attribute__((aligned(16))) int8_t x[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        x[e] = n < N && k + e < K ? W[n * ld + k + e] : (int8_t)0;
-    *reinterpret_cast<uint4 *>(Wp + id * 16) = *reinterpret_cast<const uint4 *>(x);
+    v4i x = {0, 0, 0, 0};
+    if (n < N && k + 16 <= K) {
+        typedef int unaligned __attribute__((ext_vector_type(4), aligned(1)));
+        x = *reinterpret_cast<const unaligned *>(W + n * ld + k);
+    } else if (n < N) {
+        for (int e = 0; e < 16 && k + e < K; ++e)
+            x[e / 4] |= (int)((uint32_t)(uint8_t)W[n * ld + k + e] << 8 * (e % 4));
+    }
+    *reinterpret_cast<v4i *>(Wp + id * 16) = x;
 }
 
 struct Int8Args {
@@ -108,9 +112,11 @@ __device__ inline int piece_place(int row) { return (row >> 1 & 2) ^ (row >> 3 &
 //
 // k_int8_few: 16 RT weight rows against 16 MT tokens by W waves, which take every W-th 64-k block each (side by side, so
 // that the workgroup streams whole rows of blocks) and are joined through LDS. Weights go from memory straight into
-// registers, RING blocks ahead. So do tokens where weights are what there is to read (RING == 2, DIRECT: more
+// registers, RING blocks ahead. So do tokens where weights are what there is to read (DIRECT; with RING == 2 more
 // workgroups fit a CU); in few workgroups they take a direct way into a piece of LDS of the wave's own, since a lane's
 // 16 bytes of 16 rows cost the load path more than 64 bytes side by side do.
+// Bound by the weights' bytes: 1 x 32000 x 2560 in 14 us (5.8 TB/s, more than from memory alone: part of the 82 MB is still
+// in the last cache from the call before), 40 x 28672 x 8192 50.6 us (4.7 TB/s; a large copy 5.2).
 
 template <typename TY, int RT, int MT, int RING, int W, bool DIRECT>
 __global__ __launch_bounds__(64 * W) void k_int8_few(Int8Args a)
@@ -267,6 +273,9 @@ __global__ __launch_bounds__(64 * W) void k_int8_few(Int8Args a)
 // A step is two halves of the wave's tokens. While the first one's MFMAs run, the second's operands are read; then one
 // barrier publishes the next stage and frees this one for the load four steps ahead; while the second half's MFMAs run,
 // the next step's weights and first tokens are read.
+// Bound by the matrix cores at the clock that the power leaves them: 4096 x 28672 x 8192 in 620 to 720 us (2.7 to 3.1 POP/s
+// where the library's product has 2.2), at 1.6 to 1.9 GHz. Steps of 128 k, matrix instructions of 32 x 32 x 32, four
+// waves of 128 x 128 or a ring of eight stages: slower or no gain.
 
 
 // The same for all waves of the workgroup.
@@ -503,14 +512,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
 template <typename TY>
 __global__ __launch_bounds__(256) void k_int8_zero(Int8Args a)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= a.M * a.N)
-        return;
-    const float y = a.bias ? a.bias[id % a.N] : 0.f;
-    if (a.acc)
-        a.acc[id] = 0;
-    if (a.Y)
-        static_cast<TY *>(a.Y)[id] = (TY)y;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < a.M * a.N; id += (int64_t)gridDim.x * 256) {
+        const float y = a.bias ? a.bias[id % a.N] : 0.f;
+        if (a.acc)
+            a.acc[id] = 0;
+        if (a.Y)
+            static_cast<TY *>(a.Y)[id] = (TY)y;
+    }
 }
 
 template <typename TY, int RT, int MT, int RING, int W, bool DIRECT>
@@ -531,7 +539,9 @@ hipError_t run_tile(Int8Args a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Few workgroups, tokens through LDS: the smallest tile of which no more than one a CU is needed.
+// Few workgroups, tokens through LDS: the smallest tile of which no more than one a CU is needed (RT x MT; 128 x 2560 x 2560
+// in us: 2 x 3 7.4, 4 x 2 8.8, 2 x 2 10.6, 1 x 4 11.4, 128 x 128 in LDS 14.5; 256 x 4096 x 11008: 4 x 4 35, 4 x 2 50, 128 x 128 59; 300
+// rows, which need more workgroups than CUs: 61, 73, 46). 0: there is none.
 int few_tile(int64_t M, int64_t NB)
 {
     constexpr int order[] = {12, 13, 14, 22, 23, 24, 42, 43, 44};  // 10 RT + MT
@@ -549,18 +559,29 @@ template <typename TY>
 hipError_t run_int8(const Int8Args &a, hipStream_t s)
 {
     if (a.KC == 0) {
-        k_int8_zero<TY><<<(unsigned)((a.M * a.N + 255) / 256), 256, 0, s>>>(a);
+        const int64_t blocks = (a.M * a.N + 255) / 256;
+        k_int8_zero<TY><<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(a);
         return hipGetLastError();
     }
+    // Up to 16 tokens: 16 weight rows a workgroup and loads four blocks ahead where that is no more than one a CU (1 x 4096 x
+    // 4096: 5.5 us, two ahead 6.1), else 32 rows, two ahead (in us for 1 and 16 tokens, x 6912 x 2560: 5.6 and 6.3, 16 rows and
+    // four ahead 6.4 and 8.0; x 32000 x 2560: 14.7 and 17.4; 16 rows, two ahead, 14.9 and 21.9, since the tokens are read
+    // twice as often).
     if (a.M <= 16)
-        return a.NB >= 1600  ? run_few<TY, 4, 1, 2, 8, true>(a, s)
-               : a.NB >= 512 ? run_few<TY, 2, 1, 2, 8, true>(a, s)
-                             : run_few<TY, 1, 1, 4, 8, true>(a, s);
-    if (a.M <= 64 && a.NB >= 800)
-        return a.M <= 32   ? run_few<TY, 4, 2, 2, 8, true>(a, s)
-               : a.M <= 48 ? (a.NB >= 1200 ? run_few<TY, 4, 3, 2, 4, true>(a, s) : run_few<TY, 4, 3, 2, 8, true>(a, s))
-               : a.NB >= 1200 ? run_few<TY, 4, 4, 2, 4, true>(a, s)
-                              : run_few<TY, 4, 4, 2, 8, true>(a, s);
+        return a.NB <= 256 ? run_few<TY, 1, 1, 4, 8, true>(a, s) : run_few<TY, 2, 1, 2, 8, true>(a, s);
+    // Up to 64, where 32 weight rows would be more than one workgroup a CU: 64 rows and tokens straight into registers (40 x
+    // 13824 x 2560: 11.6 us, through LDS 12.8; 40 x 8192 x 4096, the other way's 32 rows: 14.4, 11.6), by four waves where
+    // even those are more than one a CU, so that more fit (40 x 18000 x 4096: 23.9 us, by eight 27.4; 16384 rows: 20.1,
+    // 17.6).
+    if (a.M <= 64 && a.NB > 512) {
+        if (a.NB <= 1024)
+            return a.M <= 32   ? run_few<TY, 4, 2, 2, 8, true>(a, s)
+                   : a.M <= 48 ? run_few<TY, 4, 3, 2, 8, true>(a, s)
+                               : run_few<TY, 4, 4, 2, 8, true>(a, s);
+        return a.M <= 32   ? run_few<TY, 4, 2, 2, 4, true>(a, s)
+               : a.M <= 48 ? run_few<TY, 4, 3, 2, 4, true>(a, s)
+                           : run_few<TY, 4, 4, 2, 4, true>(a, s);
+    }
     switch (few_tile(a.M, a.NB)) {
     case 12: return run_few<TY, 1, 2, 4, 8, false>(a, s);
     case 13: return run_few<TY, 1, 3, 4, 8, false>(a, s);
@@ -573,8 +594,9 @@ hipError_t run_int8(const Int8Args &a, hipStream_t s)
     case 44: return run_few<TY, 4, 4, 4, 8, false>(a, s);
     default: break;
     }
-    // one workgroup of large tiles fills a CU: from three quarters of the CUs on they win
-    if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= 192)
+    // one workgroup of large tiles fills a CU, two of small ones do: from 160 large ones on they win (2048 x 5120 x 4096, 160:
+    // 46.6 us, small ones 51.2; 1024 x 8192 x 4096, 128: 46.6 and 42.0; 512 x 22016 x 4096, 172: 53.8 and 67.5)
+    if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= 160)
         return run_tile<TY, 256, 256, 2, 4>(a, s);
     return run_tile<TY, 128, 128, 2, 2>(a, s);
 }
