@@ -9,7 +9,9 @@
 //
 // Types. A code with its scale is exactly a bf16, one conversion for two of them, so both products run on bf16
 // operands: K is exact, a bf16 query is exact, an fp16 query is two bf16 (its 11 bits are 8 and 3) and two products.
-// Probabilities are carried as a bf16 and its rest (16 bits), and a second rest for fp32 outputs (24 bits).
+// Probabilities are carried as a bf16 and its rest (16 bits), and a second rest for fp32 outputs (24 bits); for bf16
+// outputs of tiles as one bf16, an error of the order of the outputs' own rounding (7B prompts behind cached keys: 0.0020 of
+// the outputs' size against 64 bits, where rounding alone gives 0.0016), for half of the second product's work.
 //
 // Order of the values. A product's order of summation is free as long as both operands have it. Lane (r, g) of an S^T
 // operand takes a key's group g, 16 bytes and one scale in one load each, as its part of the four steps of
@@ -28,10 +30,10 @@ using V8 = bf16x8;
 
 // -------------------------------------------------------------------------- work items
 //
-// Items are those of csrc/attention_items.h. Where up to four sequences fall to a lane, their lengths are loaded
-// side by side and kept, instead of one wave's worth after the other, twice (300 decoding sequences: 68.0 us, side by side 66.7).
-// The tile's number among all sequences' goes with the item: its first slice notes for the joining where the tile's
-// results lie, and the first item of all how many tiles there are.
+// Items are those of csrc/attention_items.h. Where up to sixteen sequences fall to a lane, their lengths are loaded side by
+// side and kept, instead of one wave's worth after the other, twice (300 decoding sequences over 300 to 1200 keys: 68.0 us,
+// side by side 66.7). The tile's number among all sequences' goes with the item: its first slice notes for the joining
+// where the tile's results lie, and the first item of all how many tiles there are.
 
 struct Item4 : Item {
     int number;  // of the tile
@@ -291,6 +293,12 @@ __device__ inline uint32_t first_bits(int n) { return n >= 16 ? 0xFFFFu : n <= 0
 //
 // HALVES == 2, for calls whose tiles of 128 rows would not fill the CUs: 64 rows, and the waves of a pair take the two
 // halves of every block's keys and are joined at the end.
+//
+// Bound by the matrix cores and the vector phase in turn, two waves a SIMD: a prompt of 8192 tokens of 32 heads of 128, bf16,
+// 646 us (0.85 PFLOP/s; a matrix product of 8192^3 reaches 1.39 on this card), fp16, with twice the products, 1015; 512 and
+// 300 tokens of 32 heads over 4608 and 300 keys 66 us and 8 for the joining (0.52 PFLOP/s); 256 tokens of 20 heads of five
+// groups over 8192 keys 45 together. Codes are converted once for 128 rows instead of once for 16, and a block is two
+// barriers: with each wave converting the codes for its own rows the conversion took longer than both products.
 
 constexpr int kTileRows = 128, kSmallRows = 64, kTileKeys = 64;
 
@@ -422,7 +430,8 @@ __device__ __forceinline__ void attn4_tile(const Attn4Args &a, int block, char *
                 sc[b][i] = 0.f;
 #pragma unroll
             for (int st = 0; st < NS; ++st) {
-                const V8 k = __builtin_bit_cast(V8, *reinterpret_cast<const u32x4 *>(kb + (kbase ^ (st << 5)) + b * 32 * DP * 2));
+                const char *at = kb + (kbase ^ (st << 5)) + b * 32 * DP * 2;
+                const V8 k = __builtin_bit_cast(V8, *reinterpret_cast<const u32x4 *>(at));
                 sc[b] = Elem<bf16_t>::mma32(k, qf[st], sc[b]);
                 if constexpr (kSplitQuery<E>)
                     sc[b] = Elem<bf16_t>::mma32(k, ql[st], sc[b]);
@@ -439,7 +448,8 @@ __device__ __forceinline__ void attn4_tile(const Attn4Args &a, int block, char *
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (key + 32 * (part0 + b) + 8 * (i / 4) + 4 * h + i % 4 >= limit || (part0 ? gone[2 + i / 8] : gone[2 * b + i / 8]))
+                    if (key + 32 * (part0 + b) + 8 * (i / 4) + 4 * h + i % 4 >= limit ||
+                        (part0 ? gone[2 + i / 8] : gone[2 * b + i / 8]))
                         sc[b][i] = -INFINITY;
         }
         float mx = sc[0][0];
@@ -644,6 +654,11 @@ __device__ __forceinline__ void attn4_tile(const Attn4Args &a, int block, char *
 // the cache's bytes. Each of four waves takes every fourth block of 32 keys on its own. K's codes become S^T operands
 // in their registers; V's go as bf16 through a private piece of LDS for the transposing read. The next block's
 // loads are issued before this block is used; the four partial results are joined at the end.
+//
+// 64 tokens of 20 heads of 128 in five groups over 253 thousand keys (172 MB): 51 us, 3.4 TB/s; with the loads alone 47, so
+// that it is the loads' latency with two blocks a wave on their way. Three blocks, blocks of 64 keys, loads past the
+// caches or more waves a CU: no gain. One token over 777 keys: 6.3 us, of which finding the item and the page are
+// about three, and 3.7 for the joining.
 
 constexpr int kFewRows = 16, kFewKeys = 32, kFewWaves = 4;
 
@@ -762,7 +777,8 @@ __device__ __forceinline__ void attn4_few(const Attn4Args &a, int block, char *b
                 for (int w = 0; w < Codes::W; ++w) {
                     const int c = Codes::W * (g + 4 * n) + w;
                     const V8 y = cache_values(none ? 0u : x.t[b].v[n][w], f);
-                    *reinterpret_cast<u32x4 *>(vb + r * (DP * 2) + ((c ^ swizzle<DP>(r)) << 4)) = __builtin_bit_cast(u32x4, y);
+                    *reinterpret_cast<u32x4 *>(vb + r * (DP * 2) + ((c ^ swizzle<DP>(r)) << 4)) =
+                        __builtin_bit_cast(u32x4, y);
                 }
             }
         }
@@ -919,7 +935,9 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void k_attn4_tile(Attn4Args 
 // ------------------------------------------------------------------------------- joining
 //
 // k_attn4_join: a row's slices joined by their lse, out = sum_i w_i out_i / sum_i w_i with w_i = exp(lse_i - max), as
-// k_attn_combine of csrc/attention.hip does, from the notes that the items left.
+// k_attn_combine of csrc/attention.hip does, from the notes that the items left. Up to eight rows of a tile to a workgroup;
+// fewer share its groups of lanes, four slices of each on their way at once. 3.7 us for one token's slices, 4.8 for those
+// of 64 tokens, 8.5 for 812 tokens of 32 heads.
 
 constexpr int kJoinGroups = 8;  // and the largest number of rows of a workgroup
 
@@ -1081,12 +1099,13 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
     const bool fills = tiles128 * Hkv >= 512, cached = most_keys > 2 * T;
     p.bm = few ? kFewRows : rows <= kSmallRows * seqs || !(fills || cached) ? kSmallRows : kTileRows;
     p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
-    // Keys are cut into slices where the tiles alone leave CUs idle (64 tokens over slabs of up to 8192 keys, five key
-    // heads: 104 us uncut, 55 cut; 300 tokens over 300 to 1200 keys, eight key heads: 66 uncut, 76 cut): into about four
-    // workgroups of few rows a CU, or a little under the two of many that a CU holds, since the tiles' last slices come on
-    // top (256 tokens over 8192 keys, five key heads: 65 us aiming at 512, 49 at 480, 55 at 384).
+    // Keys are cut into slices where the tiles alone leave CUs idle: into about four workgroups of few rows a CU, or a
+    // little under the two of many that a CU holds, since the tiles' last slices come on top (256 tokens over 8192 keys, five
+    // key heads: 65 us aiming at 512, 49 at 480, 55 at 384). Few rows: 64 tokens over slabs of up to 8192 keys, five key
+    // heads, 104 us uncut, 55 cut; 300 tokens over 300 to 1200 keys, eight key heads, 66 and 76. Tiles of 64: 48 drafts of 8
+    // over 2000 keys, five key heads, 62 and 46; 64 of them 70 and 76; 100 of them 79 and 129.
     const int64_t target = ((few ? 1024 : 480) + Hkv - 1) / Hkv;
-    const bool cut = few ? p.tiles * Hkv < 768 : p.bm == kSmallRows ? cached : !fills;
+    const bool cut = few ? p.tiles * Hkv < 768 : p.bm == kSmallRows ? cached && p.tiles * Hkv < 448 : !fills;
     p.target = cut && most_keys > 512 ? target : 0;
     p.min_units = few ? 2 : 4;
     const int64_t most = ((most_keys + kUnit - 1) / kUnit + p.min_units - 1) / p.min_units;
