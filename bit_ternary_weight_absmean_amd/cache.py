@@ -168,7 +168,7 @@ def attention4(q: torch.Tensor, cache: Cache4, table: torch.Tensor, k_len: torch
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     qs, os, base = q.stride(), out.stride(), cache._layer(layer)
-    shape = _ATTENTION4_SHAPE.pack(T, B, W, max(table.stride(0), W), cache.pages, cache.page_tokens, heads,
+    shape = _ATTENTION4_SHAPE.pack(T, B, W, table.stride(0) if B > 1 else W, cache.pages, cache.page_tokens, heads,
                                    cache.kv_heads, D, kind, _TYPES[ot], causal, D ** -0.5 if scale is None else scale,
                                    qs[0], qs[1], os[0], os[1])
     _call(dev, api.lib().bt_attention4, shape, q.data_ptr(), base, table.data_ptr(),
