@@ -474,7 +474,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
                         y[3] = y[3] + bias.w;
                     }
                     const int byte = (16 * i + 4 * g) * (int)sizeof(TY), row = 16 * j + r;
-                    store4(reinterpret_cast<TY *>(mine + row * ROW + ((byte >> 4 ^ (row & (PIECES - 1))) << 4) + (byte & 15)), y);
+                    char *at = mine + row * ROW + ((byte >> 4 ^ (row & (PIECES - 1))) << 4) + (byte & 15);
+                    store4(reinterpret_cast<TY *>(at), y);
                 }
             }
             // LDS operations of a wave complete in order: only the compiler has to keep them so
@@ -482,7 +483,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_int8_tile(Int8Args a)
 #pragma unroll
             for (int q = 0; q < TOKENS * PIECES / 64; ++q) {
                 const int row = (q * 64 + lane) / PIECES, piece = lane % PIECES;
-                const uint4 y = *reinterpret_cast<const uint4 *>(mine + row * ROW + ((piece ^ (row & (PIECES - 1))) << 4));
+                const char *at = mine + row * ROW + ((piece ^ (row & (PIECES - 1))) << 4);
+                const uint4 y = *reinterpret_cast<const uint4 *>(at);
                 const int64_t m = mw + 16 * j0 + row, n = nw + piece * (16 / (int)sizeof(TY));
                 if (m < a.M && n < a.N)
                     *reinterpret_cast<uint4 *>(static_cast<TY *>(a.Y) + m * a.N + n) = y;
@@ -539,9 +541,9 @@ hipError_t run_tile(Int8Args a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Few workgroups, tokens through LDS: the smallest tile of which no more than one a CU is needed (RT x MT; 128 x 2560 x 2560
-// in us: 2 x 3 7.4, 4 x 2 8.8, 2 x 2 10.6, 1 x 4 11.4, 128 x 128 in LDS 14.5; 256 x 4096 x 11008: 4 x 4 35, 4 x 2 50, 128 x 128 59; 300
-// rows, which need more workgroups than CUs: 61, 73, 46). 0: there is none.
+// Few workgroups, tokens through LDS: the smallest tile of which no more than one a CU is needed. In us by RT x MT: 128 x
+// 2560 x 2560 in 2 x 3 7.4, 4 x 2 8.8, 2 x 2 10.6, 1 x 4 11.4, in k_int8_tile 14.5; 256 x 4096 x 11008 in 4 x 4 35, 4 x 2
+// 50, k_int8_tile 59; 300 x 4096 x 11008, for which each would be more than one a CU, 61, 73 and 46. 0: there is none.
 int few_tile(int64_t M, int64_t NB)
 {
     constexpr int order[] = {12, 13, 14, 22, 23, 24, 42, 43, 44};  // 10 RT + MT
@@ -563,16 +565,16 @@ hipError_t run_int8(const Int8Args &a, hipStream_t s)
         k_int8_zero<TY><<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(a);
         return hipGetLastError();
     }
-    // Up to 16 tokens: 16 weight rows a workgroup and loads four blocks ahead where that is no more than one a CU (1 x 4096 x
-    // 4096: 5.5 us, two ahead 6.1), else 32 rows, two ahead (in us for 1 and 16 tokens, x 6912 x 2560: 5.6 and 6.3, 16 rows and
-    // four ahead 6.4 and 8.0; x 32000 x 2560: 14.7 and 17.4; 16 rows, two ahead, 14.9 and 21.9, since the tokens are read
-    // twice as often).
+    // Up to 16 tokens: 16 weight rows a workgroup and loads four blocks ahead where that is no more than one a CU (1 x
+    // 4096 x 4096: 5.5 us, two ahead 6.1), else 32 rows, two ahead (in us for 1 and 16 tokens, x 6912 x 2560: 5.6 and 6.3,
+    // 16 rows and four ahead 6.4 and 8.0; x 32000 x 2560: 14.7 and 17.4, 16 rows and two ahead 14.9 and 21.9, since
+    // the tokens are read twice as often).
     if (a.M <= 16)
         return a.NB <= 256 ? run_few<TY, 1, 1, 4, 8, true>(a, s) : run_few<TY, 2, 1, 2, 8, true>(a, s);
-    // Up to 64, where 32 weight rows would be more than one workgroup a CU: 64 rows and tokens straight into registers (40 x
-    // 13824 x 2560: 11.6 us, through LDS 12.8; 40 x 8192 x 4096, the other way's 32 rows: 14.4, 11.6), by four waves where
-    // even those are more than one a CU, so that more fit (40 x 18000 x 4096: 23.9 us, by eight 27.4; 16384 rows: 20.1,
-    // 17.6).
+    // Up to 64, where 32 weight rows would be more than one workgroup a CU: 64 rows and tokens straight into registers
+    // (40 x 13824 x 2560: 11.6 us, through LDS 12.8; 40 x 8192 x 4096: 14.4, 32 rows through LDS 11.6), by four waves where
+    // even those are more than one a CU, so that more fit (40 x 18000 x 4096: 23.9 us, by eight 27.4; 16384 rows: 20.1
+    // and 17.6).
     if (a.M <= 64 && a.NB > 512) {
         if (a.NB <= 1024)
             return a.M <= 32   ? run_few<TY, 4, 2, 2, 8, true>(a, s)
@@ -594,8 +596,8 @@ hipError_t run_int8(const Int8Args &a, hipStream_t s)
     case 44: return run_few<TY, 4, 4, 4, 8, false>(a, s);
     default: break;
     }
-    // one workgroup of large tiles fills a CU, two of small ones do: from 160 large ones on they win (2048 x 5120 x 4096, 160:
-    // 46.6 us, small ones 51.2; 1024 x 8192 x 4096, 128: 46.6 and 42.0; 512 x 22016 x 4096, 172: 53.8 and 67.5)
+    // one workgroup of large tiles fills a CU, two of small ones do: from 160 large ones on they win (2048 x 5120 x 4096,
+    // 160: 46.6 us, small ones 51.2; 1024 x 8192 x 4096, 128: 46.6 and 42.0; 512 x 22016 x 4096, 172: 53.8 and 67.5)
     if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= 160)
         return run_tile<TY, 256, 256, 2, 4>(a, s);
     return run_tile<TY, 128, 128, 2, 2>(a, s);

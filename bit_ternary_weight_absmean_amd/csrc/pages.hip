@@ -420,16 +420,77 @@ __global__ __launch_bounds__(256) void k_pages_grow(PagesArgs a, int tables, int
 
 // ---------------------------------------------------------------------------------- fork
 //
-// Counts go up first, for all pages that are taken, and down only in a second launch, for all that are given up. One
-// workgroup for each sequence; the first launch also keeps the rows as they will be in the workspace (the new lengths,
-// the new rows), since a row may be parent and child. Bound by the chain parent, length, entry, count: 8 sequences of up to
-// 9 pages 3.1 and 3.4 us, 256 of up to 64 pages 2.0 and 3.4. (One launch of one workgroup for small tables took 6.1 us for
-// the former, and the step around it no less.)
+// Counts go up first, for all pages that are taken, and down only then, for all that are given up. Tables of up to kCells
+// entries in one launch of one workgroup, with a barrier between the two; larger ones in two launches of one workgroup
+// per sequence, the first of which also keeps the rows as they will be in the workspace (the new lengths, the new rows).
+// Bound by the chain parent, length, entry, count: 8 sequences of up to 9 pages 6.1 us (two launches: 3.1 and 3.4, and a beam
+// step called from the host 21.3 us instead of 18), 256 of up to 64 pages 2.0 and 3.4.
+
+constexpr int kCells = 8 * kPlan;
 
 __device__ inline bool fork_source(const PagesArgs &a, int b, int &p)
 {
     p = a.parent[b];
     return p >= 0 && p < a.B;
+}
+
+// `first` to the lowest of the workgroup's pages, by one lane of each wave.
+__device__ inline void lower_first(const PagesArgs &a, uint32_t lowest)
+{
+    lowest = wave_reduce_bits(lowest, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+    if ((threadIdx.x & 63) == 0 && lowest != UINT32_MAX)
+        atomicMin(a.first, (int)lowest);
+}
+
+__global__ __launch_bounds__(kPlan) void k_fork_small(PagesArgs a)
+{
+    constexpr int U = kCells / kPlan;
+    const uint32_t cells = (uint32_t)a.B * a.W;
+    int page[U], old[U], now[U];  // what the cell will hold; pages of its sequence before and after (0, 0: it stays)
+    int len = -1;                 // of sequence threadIdx.x
+    if ((int)threadIdx.x < a.B) {
+        int p;
+        const bool from = fork_source(a, threadIdx.x, p);
+        if (!(from && p == (int)threadIdx.x))
+            len = from ? length_of(a, p) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t c = u * kPlan + threadIdx.x;
+        page[u] = -1;
+        old[u] = now[u] = 0;
+        if (c < cells) {
+            const int b = (int)(c / (uint32_t)a.W), i = (int)(c - (uint32_t)b * (uint32_t)a.W);
+            int p;
+            const bool from = fork_source(a, b, p);
+            if (!(from && p == b)) {
+                old[u] = pages_for(length_of(a, b), a.page_shift) - i;
+                now[u] = (from ? pages_for(length_of(a, p), a.page_shift) : 0) - i;
+                if (now[u] > 0) {
+                    page[u] = a.table[(int64_t)p * a.W + i];
+                    if (page[u] >= 0 && page[u] < a.P)
+                        atomicAdd(a.refs + page[u], 1);
+                }
+            }
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    uint32_t lowest = UINT32_MAX;  // of the pages that nothing holds any more
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t c = u * kPlan + threadIdx.x;
+        if (old[u] > 0) {
+            const int was = a.table[c];
+            if (was >= 0 && was < a.P && atomicSub(a.refs + was, 1) == 1)
+                lowest = min(lowest, (uint32_t)was);
+        }
+        if (old[u] > 0 || now[u] > 0)
+            a.table[c] = page[u];
+    }
+    lower_first(a, lowest);
+    if (len >= 0)
+        a.length[threadIdx.x] = len;
 }
 
 __global__ __launch_bounds__(256) void k_fork_take(PagesArgs a)
@@ -469,9 +530,7 @@ __global__ __launch_bounds__(256) void k_fork_give(PagesArgs a)
         }
         table[i] = i < n ? rows[i] : -1;
     }
-    lowest = wave_reduce_bits(lowest, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
-    if ((threadIdx.x & 63) == 0 && lowest != UINT32_MAX)
-        atomicMin(a.first, (int)lowest);
+    lower_first(a, lowest);
     __syncthreads();  // all have read the length
     if (threadIdx.x == 0)
         a.length[b] = len;
@@ -624,6 +683,10 @@ hipError_t launch_pages_grow(const PagesArgs &a, hipStream_t s)
 
 hipError_t launch_pages_fork(const PagesArgs &a, hipStream_t s)
 {
+    if (a.B <= kPlan && (int64_t)a.B * a.W <= kCells) {
+        k_fork_small<<<1, kPlan, 0, s>>>(a);
+        return hipGetLastError();
+    }
     k_fork_take<<<(unsigned)a.B, 256, 0, s>>>(a);
     if (hipError_t e = hipGetLastError())
         return e;
