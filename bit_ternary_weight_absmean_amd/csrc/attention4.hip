@@ -128,14 +128,23 @@ __device__ inline bool take_item(const Attn4Args &a, int bm, int id, int head, I
     if (a.target && head == 0 && threadIdx.x < 64) {
         if (id == 0) {
             int tiles = 0;
-            for (int b = threadIdx.x; b < a.B; b += 64)
-                tiles += row_tiles(a, load_seq(a, b), bm);
+            float items = 0.f;
+            for (int b = threadIdx.x; b < a.B; b += 64) {
+                const Seq s = load_seq(a, b);
+                const int n = row_tiles(a, s, bm);
+                tiles += n;
+                items += (float)n * (float)pieces_of(s, it.unit);
+            }
             tiles = wave_sum_i32(tiles);
+            items = __uint_as_float(wave_reduce_bits(__float_as_uint(items), [](uint32_t x, uint32_t y) {
+                return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+            }));
+            // (sequences that overlap may have more items than were launched: then some notes are not written, and nothing
+            // is joined)
             if (threadIdx.x == 0)
-                notes[0].pieces = tiles;
+                notes[0].pieces = items <= (float)a.items && tiles <= a.tiles ? tiles : 0;
         }
-        // (sequences that overlap may have more tiles than there is room for: those are not joined)
-        if (found && it.piece == 0 && it.number < a.tiles && threadIdx.x == 0)
+        if (found && it.piece == 0 && (uint32_t)it.number < (uint32_t)a.tiles && threadIdx.x == 0)
             notes[1 + it.number] = TileNote{first_item(a, it, bm), it.pieces, it.tile, it.s.q0, it.s.nq, {0, 0, 0}};
     }
     return found;
@@ -953,8 +962,8 @@ __global__ __launch_bounds__(32 * kJoinGroups) void k_attn4_join(Attn4Args a, in
         return;
     const TileNote tile = notes[1 + id];
     const int pieces = tile.pieces, slot = tile.slot;
-    if (pieces == 1 || slot + pieces > a.items)
-        return;  // written by its one item; or tiles of sequences that overlap, without room
+    if (pieces == 1)
+        return;  // written by its one item
     const int rows = tile.nq * a.G;
     const int r0 = blockIdx.y * kJoinGroups;
     const int here = min(min(bm - r0, kJoinGroups), rows - tile.tile * bm - r0);  // rows of this workgroup

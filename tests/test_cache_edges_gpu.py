@@ -67,6 +67,27 @@ def test_offsets_that_leave_the_arrays():
     assert torch.equal(got, want)
 
 
+def test_sequences_that_overlap():
+    """A caller's mistake: more rows than tokens. What the rows hold is open; nothing beside them is touched."""
+    note("attention4 sequences that overlap")
+    c = Case([30], [900], 64, 8, 64, "bf16", page=32)
+    T, B = 30, 200
+    table, k_len = i32(c.table * B).view(B, c.W), i32([900] * B)
+    room = torch.full((3 * T, 64, 64), 7.0, device=DEV)
+    lse = torch.full((3 * T, 64), 7.0, device=DEV)
+    need = bt.attention4_workspace_bytes(T, B, 64, 8, 64, c.W, 32)
+    ws = torch.full((need + 8192,), 129, dtype=torch.uint8, device=DEV)  # notes of before: negative numbers
+    before = c.cache.data.clone()
+    for offsets in ([0, T] * (B // 2) + [0], [0, T, 0, 10] * (B // 4) + [T]):
+        bt.attention4(c.q, c.cache, table, k_len, i32(offsets), out=room[T: 2 * T], lse=lse[T: 2 * T], workspace=ws[:need])
+        torch.cuda.synchronize()
+        for x in (room, lse):
+            assert bool((x[:T] == 7).all()) and bool((x[2 * T:] == 7).all())
+        assert bool((ws[need:] == 129).all()) and torch.equal(c.cache.data, before)
+    bt.attention4(c.q, c.cache, table[:1], k_len[:1], i32([0, T]), out=room[T: 2 * T], lse=lse[T: 2 * T])
+    c.check(room[T: 2 * T], lse[T: 2 * T])
+
+
 def test_workspace_of_two_graphs():
     """Two captured calls that share a workspace, replayed one behind the other with other work in it in between."""
     note("attention4 one workspace")
