@@ -9,9 +9,10 @@
 //
 // Types. A code with its scale is exactly a bf16, one conversion for two of them, so both products run on bf16
 // operands: K is exact, a bf16 query is exact, an fp16 query is two bf16 (its 11 bits are 8 and 3) and two products.
-// Probabilities are carried as a bf16 and its rest (16 bits), and a second rest for fp32 outputs (24 bits); for bf16
-// outputs of tiles as one bf16, an error of the order of the outputs' own rounding (7B prompts behind cached keys: 0.0020 of
-// the outputs' size against 64 bits, where rounding alone gives 0.0016), for half of the second product's work.
+// Probabilities are carried as a bf16 and its rest (16 bits), and a second rest for fp32 outputs (24 bits), in every form,
+// so that a sequence's precision does not depend on what it is batched with. (One bf16 alone would save tiles with bf16
+// outputs half of the second product, 14% of a long prompt, and add as much error as the outputs' own rounding: 7B
+// prompts behind cached keys 0.0020 of the outputs' size against 64 bits, where rounding alone gives 0.0016, as two do.)
 //
 // Order of the values. A product's order of summation is free as long as both operands have it. Lane (r, g) of an S^T
 // operand takes a key's group g, 16 bytes and one scale in one load each, as its part of the four steps of
@@ -304,9 +305,10 @@ __device__ inline uint32_t first_bits(int n) { return n >= 16 ? 0xFFFFu : n <= 0
 // halves of every block's keys and are joined at the end.
 //
 // Bound by the matrix cores and the vector phase in turn, two waves a SIMD: a prompt of 8192 tokens of 32 heads of 128, bf16,
-// 646 us (0.85 PFLOP/s; a matrix product of 8192^3 reaches 1.39 on this card), fp16, with twice the products, 1015; 512 and
-// 300 tokens of 32 heads over 4608 and 300 keys 66 us and 8 for the joining (0.52 PFLOP/s); 256 tokens of 20 heads of five
-// groups over 8192 keys 45 together. Codes are converted once for 128 rows instead of once for 16, and a block is two
+// 754 us (0.73 PFLOP/s of the formula's operations, 1.09 of the matrix cores', whose second product runs twice; a matrix
+// product of 8192^3 reaches 1.39 on this card), fp16, where the first does too, 999; 512 and 300 tokens of 32 heads over
+// 4608 and 300 keys 76 us and 8 for the joining; 256 tokens of 20 heads of five groups over 8192 keys 43 and
+// 8. Codes are converted once for 128 rows instead of once for 16, and a block is two
 // barriers: with each wave converting the codes for its own rows the conversion took longer than both products.
 
 constexpr int kTileRows = 128, kSmallRows = 64, kTileKeys = 64;
@@ -325,7 +327,7 @@ __device__ __forceinline__ void attn4_tile(const Attn4Args &a, int block, char *
 {
     constexpr int ROWS = kTileRows / HALVES, KB = 2 / HALVES;  // rows of the tile, 32-key parts per wave
     constexpr int NS = DP / 16, ND = DP / 32;                  // MFMA steps over D, 32-wide tiles of D
-    constexpr int PARTS = WIDE ? 3 : kSplitQuery<E> ? 2 : 1;   // of a probability
+    constexpr int PARTS = WIDE ? 3 : 2;                        // of a probability
     using Codes = Codes4<DP>;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 31, h = lane >> 5, r16 = lane & 15, g = lane >> 4;
@@ -1098,11 +1100,11 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
 {
     Attn4Plan plan{};
     AttnPart &p = plan.main;
-    const int64_t rows = T * (Hq / Hkv), seqs = B < T ? B : T;  // the sequences that have rows
-    // Rows of a tile, by the mean rows of a sequence: up to 16, one small tile each; up to 64, one of 64. Longer ones take
-    // tiles of 128, or of 64 where those would not fill the CUs and there are no long caches to cut instead (capacity of
-    // twice the call's tokens or more; 7B prompts of 813 tokens behind 4096 keys: 79 us cut, 118 uncut with 64 rows; packed
-    // 2B prompts of 2048 tokens 45 and 36).
+    const int64_t rows = T * (Hq / Hkv), seqs = B < T ? B : T;  // no more than these have rows
+    // Rows of a tile, by the mean rows of such a sequence (idle ones of the table count, too): up to 16, one small tile
+    // each; up to 64, one of 64. Longer ones take tiles of 128, or of 64 where those would not fill the CUs and there are no
+    // long caches to cut instead (capacity of twice the call's tokens or more; 7B prompts of 813 tokens behind 4096 keys:
+    // 86 us cut, 137 uncut with 64 rows; packed 2B prompts of 2048 tokens 49 and 39).
     const bool few = rows <= kFewRows * seqs;
     const int64_t tiles128 = rows / kTileRows + seqs;
     const bool fills = tiles128 * Hkv >= 512, cached = most_keys > 2 * T;
@@ -1110,9 +1112,9 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
     p.tiles = seqs == 1 ? (rows + p.bm - 1) / p.bm : rows / p.bm + seqs;  // at least sum of ceil(rows_b / bm)
     // Keys are cut into slices where the tiles alone leave CUs idle: into about four workgroups of few rows a CU, or a
     // little under the two of many that a CU holds, since the tiles' last slices come on top (256 tokens over 8192 keys, five
-    // key heads: 65 us aiming at 512, 49 at 480, 55 at 384). Few rows: 64 tokens over slabs of up to 8192 keys, five key
+    // key heads: 72 us aiming at 512, 55 at 480, 62 at 384). Few rows: 64 tokens over slabs of up to 8192 keys, five key
     // heads, 104 us uncut, 55 cut; 300 tokens over 300 to 1200 keys, eight key heads, 66 and 76. Tiles of 64: 48 drafts of 8
-    // over 2000 keys, five key heads, 62 and 46; 64 of them 70 and 76; 100 of them 79 and 129.
+    // over 2000 keys, five key heads, 60 and 47; 64 of them 65 and 78; 100 of them 75 and 73.
     const int64_t target = ((few ? 1024 : 480) + Hkv - 1) / Hkv;
     const bool cut = few ? p.tiles * Hkv < 768 : p.bm == kSmallRows ? cached && p.tiles * Hkv < 448 : !fills;
     p.target = cut && most_keys > 512 ? target : 0;

@@ -553,11 +553,9 @@ bt_status bt_cache4_read(const bt_cache4_rows *shape, const void *cache, const i
  *   table     [seqs, max_pages] int32 on the device, rows table_row elements apart. Entries behind a sequence's last
  *             key are not read. The keys of an entry outside [0, pages) count as not seen.
  * type: BT_BF16 or BT_F16, of q; out_type: the same or BT_F32. Keys and values are exact in the products, scores,
- * statistics and sums fp32; probabilities are carried in 16 bits, for fp32 outputs in 24, and for bf16 outputs in 8 (as a
- * bf16) where the call has more than 16 rows of a sequence and key head, on average over its sequences with any. Results
- * do not depend on timing. What a query does not see
- * does not reach it, NaNs included; a NaN group of V that it sees is NaN in its output's values of that group, one of K
- * makes the whole row NaN.
+ * statistics and sums fp32; probabilities are carried in 16 bits, for fp32 outputs in 24. Results do not depend on timing.
+ * What a query does not see does not reach it, NaNs included; a NaN group of V that it sees is NaN in its output's values
+ * of that group, one of K makes the whole row NaN.
  * q: 16-byte aligned with strides multiples of 8; out: aligned to four elements. tokens <= BT_MAX_DIM; tokens *
  * heads and max_pages * page_tokens at most BT_ATTENTION_MAX_KEYS; scale finite and positive.
  *   workspace bt_attention4_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim, max_pages, page_tokens) bytes of
