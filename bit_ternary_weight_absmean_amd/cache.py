@@ -184,7 +184,8 @@ class Pages:
     """Which of ``seqs`` sequences holds which of ``pages`` pages of ``page_tokens`` tokens (a power of two up to
     1024), all of it on the device: ``table`` [seqs, max_pages] (-1 behind a sequence's pages), ``length`` [seqs] in
     tokens, ``refs`` [pages] (how many entries hold a page; 0: free) and ``first`` [1] (no page below it is free), int32
-    views of one array ``state`` in this order, which can be copied to keep or go back to a state. Starts empty."""
+    views of one array ``state`` in this order, which can be copied to keep or go back to a state. Starts empty. A deep,
+    pickled or saved copy is a second table with arrays of its own."""
 
     seqs: int
     max_pages: int
@@ -201,18 +202,33 @@ class Pages:
         cells = self.seqs * self.max_pages
         state = torch.zeros(cells + self.seqs + self.pages + 1, dtype=torch.int32, device=self.device)
         state[:cells] = -1
+        self._hold(state)
+
+    def _hold(self, state):
+        """Makes ``state`` this object's, with views of it and a workspace."""
+        cells = self.seqs * self.max_pages
         parts = state.split([cells, self.seqs, self.pages, 1])
+        need = _workspace_bytes("bt_pages_workspace_bytes", self.seqs, self.max_pages, self.pages)
         for name, value in (("state", state), ("table", parts[0].view(self.seqs, self.max_pages)),
                             ("length", parts[1]), ("refs", parts[2]), ("first", parts[3]), ("device", state.device),
-                            ("_need", need), ("_workspace", torch.empty(need, dtype=torch.uint8, device=self.device)),
-                            ("_at", state.data_ptr()), ("_offsets", (4 * cells, 4 * (cells + self.seqs),
-                                                                     4 * (cells + self.seqs + self.pages)))):
+                            ("_need", need), ("_workspace", torch.empty(need, dtype=torch.uint8, device=state.device)),
+                            ("_offsets", (4 * cells, 4 * (cells + self.seqs), 4 * (cells + self.seqs + self.pages)))):
             object.__setattr__(self, name, value)
 
+    # A copy, by copy.deepcopy, pickle or torch.save, has its own state, and views and a workspace of it; copy.copy shares
+    # the state.
+    def __getstate__(self):
+        return {name: getattr(self, name) for name in ("seqs", "max_pages", "pages", "page_tokens", "state")}
+
+    def __setstate__(self, kept):
+        for name, value in kept.items():
+            object.__setattr__(self, name, value)
+        self._hold(self.state)
+
     def _arrays(self):
-        """The addresses of table, length, refs and first."""
-        length, refs, first = self._offsets
-        return self._at, self._at + length, self._at + refs, self._at + first
+        """The addresses of table, length, refs and first, asked for at every call: a copy's are its own."""
+        at, (length, refs, first) = self.state.data_ptr(), self._offsets
+        return at, at + length, at + refs, at + first
 
     def _shape(self, pool=None, tokens: int = 0):
         layers = stride = size = 0
