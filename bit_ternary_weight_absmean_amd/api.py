@@ -495,6 +495,9 @@ class LoraAdapters:
                             ("_K", self.A.shape[2]), ("_type", _TYPES[self.B.dtype])):
             object.__setattr__(self, name, value)
 
+    def __setstate__(self, kept):  # perhaps loaded onto another device than it was saved from
+        self.__dict__.update(kept, _dev=kept["B"].device)
+
     @property
     def K(self) -> int:
         return self.A.shape[2]

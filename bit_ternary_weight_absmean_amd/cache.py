@@ -51,6 +51,9 @@ class Cache4:
         object.__setattr__(self, "device", self.data.device)
         object.__setattr__(self, "_layer_bytes", self.pages * size)
 
+    def __setstate__(self, kept):  # perhaps loaded onto another device than it was saved from
+        self.__dict__.update(kept, device=kept["data"].device)
+
     def _layer(self, layer: int) -> int:
         """The address of a layer's pages."""
         if not 0 <= layer < self.layers:
