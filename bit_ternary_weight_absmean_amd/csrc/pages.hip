@@ -229,7 +229,7 @@ __device__ inline Token place_token(const PagesArgs &a, int b, int t, int from, 
     const int p = at >> a.page_shift;
     // what this call writes to the table is taken from the list
     const int page = p >= slot && start + p - slot < end ? free[start + p - slot] : a.table[(int64_t)b * a.W + p];
-    return {page < 0 ? -1 : page << a.page_shift | (at & ((1 << a.page_shift) - 1)), at};
+    return {page < 0 || page >= a.P ? -1 : page << a.page_shift | (at & ((1 << a.page_shift) - 1)), at};
 }
 
 __global__ __launch_bounds__(kPlan) void k_pages_plan_small(PagesArgs a)

@@ -605,7 +605,8 @@ size_t bt_pages_workspace_bytes(int64_t seqs, int64_t max_pages, int64_t pages);
  * pages are not there any more, or that max_pages has no room for, is refused: it stays as it is. The pages asked for
  * by a refused sequence stay free, but those behind it that need pages are refused with it.
  *   rows      [tokens] int32 out: the place of each new token (page * page_tokens + place in the page) for the writes
- *             of its keys and values; -1 in a refused sequence, and for tokens of none.
+ *             of its keys and values; -1 in a refused sequence, for tokens of none, and where the table's entry is no
+ *             page of the pool.
  *   positions [tokens] int32 out: the token's number in its sequence, from 0 (-1 for tokens of none).
  *   granted   [seqs] int32 out: n, or 0.
  */
