@@ -251,10 +251,12 @@ def _check_pages(pages):
         raise TypeError(f"pages must be a Pages, got {type(pages).__name__}")
 
 
-def _pool(pool, pages: int, dev):
-    """((layers, bytes between layers, bytes of a page), address) of a pool: a Cache4, or a tensor [layers, pages,
-    ...] of whole 16 bytes a page."""
+def _pool(pool, pages: int, dev, page_tokens: int | None = None):
+    """((layers, bytes between layers, bytes of a page), address) of a pool: a Cache4 (of ``page_tokens``, where given),
+    or a tensor [layers, pages, ...] of whole 16 bytes a page."""
     if isinstance(pool, Cache4):
+        if page_tokens is not None and pool.page_tokens != page_tokens:
+            raise ValueError(f"the pool is a Cache4 with pages of {pool.page_tokens} tokens, the table's have {page_tokens}")
         pool = pool.data
     if not isinstance(pool, torch.Tensor) or pool.dim() < 3:
         raise ValueError("pool must be a Cache4 or a tensor [layers, pages, ...]")
@@ -274,10 +276,10 @@ def pages_grow(pages: Pages, q_start: torch.Tensor, pool, out=None, tokens: int 
                workspace: torch.Tensor | None = None):
     """bt_pages_grow: room for q_start[b + 1] - q_start[b] new tokens of every sequence b (``q_start`` [seqs + 1]
     int32 on the device, as attention4 takes it). A partly filled last page that others hold too is copied in ``pool``
-    (a Cache4, or a tensor [layers, pages, ...]). Returns (rows, positions, granted): the place of each new token (-1:
-    refused), its number in its sequence, and the tokens each sequence got (all it asked for, or 0). ``tokens``, the
-    rows of the first two, is q_start's last entry where the host knows it; or pass ``out`` = (rows, positions,
-    granted)."""
+    (a Cache4 of the same page_tokens, or a tensor [layers, pages, ...]). Returns (rows, positions, granted): the place of
+    each new token (-1: refused), its number in its sequence, and the tokens each sequence got (all it asked for, or
+    0). ``tokens``, the rows of the first two, is q_start's last entry where the host knows it; or pass ``out`` = (rows,
+    positions, granted)."""
     _check_pages(pages)
     dev, i32, at = pages.device, torch.int32, pages.state.get_device()
     if not _is(q_start, i32, (pages.seqs + 1,), at):
@@ -296,7 +298,7 @@ def pages_grow(pages: Pages, q_start: torch.Tensor, pool, out=None, tokens: int 
         _need(rows, "rows", i32, (T,), dev)
         _need(positions, "positions", i32, (T,), dev)
         _need(granted, "granted", i32, (pages.seqs,), dev)
-    over, base = _pool(pool, pages.pages, dev)
+    over, base = _pool(pool, pages.pages, dev, pages.page_tokens)
     table, length, refs, first = pages._arrays()
     scratch = pages._scratch(workspace)
     _call(dev, api.lib().bt_pages_grow, pages._shape(over, T), table, length, refs, first, q_start.data_ptr(), base,
@@ -318,7 +320,7 @@ def pages_compact(pages: Pages, pool, workspace: torch.Tensor | None = None) -> 
     """bt_pages_compact: the pages in use, L of them, to places 0 .. L - 1 of ``pool`` (as in pages_grow), tables
     and counts with them. ``pages.first`` then holds L."""
     _check_pages(pages)
-    over, base = _pool(pool, pages.pages, pages.device)
+    over, base = _pool(pool, pages.pages, pages.device, pages.page_tokens)
     table, _, refs, first = pages._arrays()
     scratch = pages._scratch(workspace)
     _call(pages.device, api.lib().bt_pages_compact, pages._shape(over), table, refs, first, base, scratch)
