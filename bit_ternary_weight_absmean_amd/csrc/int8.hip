@@ -21,21 +21,21 @@ typedef __attribute__((address_space(1))) const void global_void;
 __global__ __launch_bounds__(256) void k_int8_pack(const int8_t *W, int64_t ld, int64_t N, int64_t K, int64_t pieces,
                                                    int64_t KC, char *Wp)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 16 bytes of Wp
-    if (id >= pieces)
-        return;
-    const int64_t block = id >> 6;
-    const int lane = (int)(id & 63);
-    const int64_t n = block / KC * 16 + (lane & 15), k = block % KC * 64 + 16 * (lane >> 4);
-    v4i x = {0, 0, 0, 0};
-    if (n < N && k + 16 <= K) {
-        typedef int unaligned __attribute__((ext_vector_type(4), aligned(1)));
-        x = *reinterpret_cast<const unaligned *>(W + n * ld + k);
-    } else if (n < N) {
-        for (int e = 0; e < 16 && k + e < K; ++e)
-            x[e / 4] |= (int)((uint32_t)(uint8_t)W[n * ld + k + e] << 8 * (e % 4));
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < pieces; id += step) {  // 16 bytes of Wp
+        const int64_t block = id >> 6;
+        const int lane = (int)(id & 63);
+        const int64_t n = block / KC * 16 + (lane & 15), k = block % KC * 64 + 16 * (lane >> 4);
+        v4i x = {0, 0, 0, 0};
+        if (n < N && k + 16 <= K) {
+            typedef int unaligned __attribute__((ext_vector_type(4), aligned(1)));
+            x = *reinterpret_cast<const unaligned *>(W + n * ld + k);
+        } else if (n < N) {
+            for (int e = 0; e < 16 && k + e < K; ++e)
+                x[e / 4] |= (int)((uint32_t)(uint8_t)W[n * ld + k + e] << 8 * (e % 4));
+        }
+        *reinterpret_cast<v4i *>(Wp + id * 16) = x;
     }
-    *reinterpret_cast<v4i *>(Wp + id * 16) = x;
 }
 
 struct Int8Args {
@@ -610,8 +610,10 @@ size_t int8_weight_bytes(int64_t N, int64_t K) { return (size_t)(round_up(N, 16)
 hipError_t launch_int8_pack(const int8_t *W, int64_t ld, int64_t N, int64_t K, void *Wp, hipStream_t s)
 {
     const int64_t pieces = (int64_t)int8_weight_bytes(N, K) / 16;
-    k_int8_pack<<<(unsigned)((pieces + 255) / 256), 256, 0, s>>>(W, ld, N, K, pieces, (K + 63) / 64,
-                                                                 static_cast<char *>(Wp));
+    // a launch holds less than 2^32 work-items, and the largest weights have that many pieces: 2^28 at a time
+    const int64_t blocks = (pieces + 255) / 256, most = 1 << 20;
+    k_int8_pack<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(W, ld, N, K, pieces, (K + 63) / 64,
+                                                                         static_cast<char *>(Wp));
     return hipGetLastError();
 }
 
