@@ -66,6 +66,7 @@ from .cache import (
     Cache4,
     Pages,
     attention4,
+    attention4_plan,
     attention4_workspace,
     attention4_workspace_bytes,
     cache4_page_bytes,
@@ -94,7 +95,7 @@ __all__ = [
     "ternary_gemv", "unpack_weights", "kernel_plan", "CALL_LINEAR", "CALL_GEMV", "CALL_GEMM", "CALL_GEMM_WS", "CALL_QUANT", "linear_static", "STATIC_SCRATCH_BYTES",
     "LORA_MAX_RANK", "LoraAdapters", "lora_apply", "lora_workspace", "lora_workspace_bytes", "qk_norm_rope",
     "rope_frequencies", "attention", "attention_workspace", "attention_workspace_bytes",
-    "Cache4", "cache4_page_bytes", "cache4_read", "cache4_write", "attention4", "attention4_workspace",
+    "Cache4", "cache4_page_bytes", "cache4_read", "cache4_write", "attention4", "attention4_plan", "attention4_workspace",
     "attention4_workspace_bytes", "Pages", "pages_compact", "pages_copy", "pages_fork", "pages_grow",
     "Int8Weight", "int8_gemm", "int8_linear", "int8_weight_bytes", "int8_workspace", "int8_workspace_bytes",
     "pack_int8", "pack_weights_int8",

@@ -48,6 +48,7 @@ SIGNATURES = {
     "bt_cache4_read": (_i32, [_vp] * 6),
     "bt_attention4_workspace_bytes": (_sz, [_i64] * 7),
     "bt_attention4": (_i32, [_vp] * 10),
+    "bt_attention4_plan": (_i32, [_vp, ctypes.c_char_p, _sz]),
     "bt_pages_workspace_bytes": (_sz, [_i64] * 3),
     "bt_pages_grow": (_i32, [_vp] * 12),
     "bt_pages_fork": (_i32, [_vp] * 8),

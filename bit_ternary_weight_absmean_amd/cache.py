@@ -7,6 +7,7 @@ shares prompts and drops what has ended; ``pages_compact`` brings the pages in u
 """
 from __future__ import annotations
 
+import ctypes
 import struct
 from dataclasses import dataclass, field
 
@@ -125,6 +126,16 @@ def attention4_workspace(q: torch.Tensor, cache: Cache4, table: torch.Tensor) ->
     n = attention4_workspace_bytes(q.shape[0], table.shape[0], q.shape[1], cache.kv_heads, cache.head_dim,
                                    table.shape[1], cache.page_tokens)
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def attention4_plan(tokens: int, seqs: int, heads: int, kv_heads: int, head_dim: int, max_pages: int, page_tokens: int,
+                    dtype: torch.dtype = torch.bfloat16, out_dtype: torch.dtype | None = None) -> str:
+    """bt_attention4_plan: the kernel instances that such an attention4 call would launch (host-only query)."""
+    shape = _ATTENTION4_SHAPE.pack(tokens, seqs, max_pages, max_pages, 0, page_tokens, heads, kv_heads, head_dim,
+                                   _TYPES[dtype], _TYPES[out_dtype or dtype], True, 1.0, 0, 0, 0, 0)
+    buf = ctypes.create_string_buffer(128)
+    api.check(api.lib().bt_attention4_plan(shape, buf, len(buf)))
+    return buf.value.decode()
 
 
 def attention4(q: torch.Tensor, cache: Cache4, table: torch.Tensor, k_len: torch.Tensor, q_start: torch.Tensor,

@@ -226,6 +226,23 @@ bt_status check_attention4(int64_t tokens, int64_t seqs, int64_t heads, int64_t 
     return BT_OK;
 }
 
+// What bt_attention4 and its plan query check of a shape.
+bt_status check_attention4_shape(const bt_attention4_shape *shape, bt::Attn4Plan &plan, int &shift)
+{
+    if (!shape)
+        return fail(BT_ERR_NULL, "shape is NULL");
+    const bt_attention4_shape &s = *shape;
+    if (bt_status e = check_attention4(s.tokens, s.seqs, s.heads, s.kv_heads, s.head_dim, s.max_pages, s.page_tokens, plan))
+        return e;
+    if (bt_status e = check_cache4(s.pages, s.page_tokens, s.kv_heads, s.head_dim, shift))
+        return e;
+    if (!(s.scale > 0.0f) || !(s.scale < 1.0e30f))
+        return fail(BT_ERR_SHAPE, "scale must be finite and positive");
+    if ((s.type != BT_BF16 && s.type != BT_F16) || (s.out_type != s.type && s.out_type != BT_F32))
+        return fail(BT_ERR_UNSUPPORTED, "type %d with out_type %d", s.type, s.out_type);
+    return BT_OK;
+}
+
 // The shape of a table of pages and, where `pool` counts, of what it lies over.
 bt_status check_pages(const bt_pages_shape *shape, bool pooled, bt::PagesArgs &a)
 {
@@ -1034,19 +1051,11 @@ bt_status bt_attention4(const bt_attention4_shape *shape, const void *q, const v
                         const int32_t *q_start, const int32_t *k_len, void *out, float *lse, void *workspace,
                         void *stream)
 {
-    if (!shape)
-        return fail(BT_ERR_NULL, "shape is NULL");
-    const bt_attention4_shape &s = *shape;
     bt::Attn4Plan plan;
     bt::Attn4Args a{};
-    if (bt_status e = check_attention4(s.tokens, s.seqs, s.heads, s.kv_heads, s.head_dim, s.max_pages, s.page_tokens, plan))
+    if (bt_status e = check_attention4_shape(shape, plan, a.page_shift))
         return e;
-    if (bt_status e = check_cache4(s.pages, s.page_tokens, s.kv_heads, s.head_dim, a.page_shift))
-        return e;
-    if (!(s.scale > 0.0f) || !(s.scale < 1.0e30f))
-        return fail(BT_ERR_SHAPE, "scale must be finite and positive");
-    if ((s.type != BT_BF16 && s.type != BT_F16) || (s.out_type != s.type && s.out_type != BT_F32))
-        return fail(BT_ERR_UNSUPPORTED, "type %d with out_type %d", s.type, s.out_type);
+    const bt_attention4_shape &s = *shape;
     if (s.tokens == 0 || s.seqs == 0)
         return ok();
     const bool keys = s.pages > 0 && s.max_pages > 0;
@@ -1093,6 +1102,20 @@ bt_status bt_attention4(const bt_attention4_shape *shape, const void *q, const v
     a.groups = bt::cache_groups(s.head_dim);
     return hip_status(bt::launch_attention4(a, plan, s.type, s.out_type, static_cast<hipStream_t>(stream)),
                       "bt_attention4 launch");
+}
+
+bt_status bt_attention4_plan(const bt_attention4_shape *shape, char *buf, size_t len)
+{
+    if (!buf || len == 0)
+        return fail(BT_ERR_NULL, "buf is NULL or len is 0");
+    buf[0] = '\0';
+    bt::Attn4Plan plan;
+    int shift;
+    if (bt_status e = check_attention4_shape(shape, plan, shift))
+        return e;
+    if (shape->tokens > 0 && shape->seqs > 0)
+        bt::attention4_plan_text(plan, (int)shape->head_dim, shape->type, shape->out_type, buf, len);
+    return ok();
 }
 
 size_t bt_pages_workspace_bytes(int64_t seqs, int64_t max_pages, int64_t pages)

@@ -64,5 +64,6 @@ struct Attn4Plan {
 
 Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t most_keys);
 hipError_t launch_attention4(const Attn4Args &args, const Attn4Plan &p, int type, int out_type, hipStream_t s);
+void attention4_plan_text(const Attn4Plan &p, int D, int type, int out_type, char *buf, size_t len);
 
 }  // namespace bt

@@ -21,6 +21,8 @@
 // NaN. A group of K that holds a NaN makes the scores of its key NaN, which counts in rows that see it only (unseen
 // scores are replaced). A group of V that holds one goes into the product as zeros, and rows that see its key get NaN
 // in the group's values directly. Finite groups are finite in bf16, so there are no infinities to meet.
+#include <stdio.h>
+
 #include "attention_items.h"
 #include "cache4.h"
 
@@ -1128,6 +1130,20 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
     plan.notes_off = p.l_off + round_up(slots * 4, 256);
     plan.bytes = (size_t)(plan.notes_off + (p.target ? round_up((1 + p.tiles) * kNoteBytes, 256) : 0));
     return plan;
+}
+
+// The kernels of launch_attention4, in order (bt_attention4_plan).
+void attention4_plan_text(const Attn4Plan &p, int D, int type, int out_type, char *buf, size_t len)
+{
+    auto name = [](int t) { return t == kF32 ? "fp32" : t == kBF16 ? "bf16" : "fp16"; };
+    const int dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+    char tile[32] = "", join[64] = "";
+    if (p.main.bm != kFewRows)
+        snprintf(tile, sizeof(tile), ",%d", p.main.bm);
+    if (p.main.target)
+        snprintf(join, sizeof(join), " + k_attn4_join<%s>", name(out_type));
+    snprintf(buf, len, "k_attn4_%s<%s,%d,%s%s>%s", p.main.bm == kFewRows ? "few" : "tile", name(type), dp, name(out_type),
+             tile, join);
 }
 
 hipError_t launch_attention4(const Attn4Args &args, const Attn4Plan &p, int type, int out_type, hipStream_t s)

@@ -574,6 +574,12 @@ size_t bt_attention4_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads
 bt_status bt_attention4(const bt_attention4_shape *shape, const void *q, const void *cache, const int32_t *table,
                         const int32_t *q_start, const int32_t *k_len, void *out, float *lse, void *workspace,
                         void *stream);
+/*
+ * bt_attention4_plan -- the kernel instances that a call of this shape would launch, as text in `buf` of `len` bytes (as
+ * bt_kernel_plan; a host-only query): k_attn4_few<type,head dim,out_type> or k_attn4_tile<type,head dim,out_type,rows>,
+ * the head dim rounded up to 64, 128 or 256, and " + k_attn4_join<out_type>" where the keys are cut into slices.
+ */
+bt_status bt_attention4_plan(const bt_attention4_shape *shape, char *buf, size_t len);
 
 /*
  * The pages of a cache: which sequence holds which, all of it on the device.
