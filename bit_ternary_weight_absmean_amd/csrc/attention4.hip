@@ -307,10 +307,10 @@ __device__ inline uint32_t first_bits(int n) { return n >= 16 ? 0xFFFFu : n <= 0
 // halves of every block's keys and are joined at the end.
 //
 // Bound by the matrix cores and the vector phase in turn, two waves a SIMD: a prompt of 8192 tokens of 32 heads of 128, bf16,
-// 754 us (0.73 PFLOP/s of the formula's operations, 1.09 of the matrix cores', whose second product runs twice; a matrix
-// product of 8192^3 reaches 1.39 on this card), fp16, where the first does too, 999; 512 and 300 tokens of 32 heads over
-// 4608 and 300 keys 76 us and 8 for the joining; 256 tokens of 20 heads of five groups over 8192 keys 43 and
-// 8. Codes are converted once for 128 rows instead of once for 16, and a block is two
+// 754 to 787 us (0.70 to 0.73 PFLOP/s of the formula's operations, 1.05 to 1.09 of the matrix cores', whose second product
+// runs twice; a matrix product of 8192^3 reaches 1.39 on this card), fp16, where the first does too, 999 to 1029; 512 and
+// 300 tokens of 32 heads over 4608 and 300 keys 76 to 78 us and 8 for the joining; 256 tokens of 20 heads of five groups
+// over 8192 keys 43 to 48 and 8. Codes are converted once for 128 rows instead of once for 16, and a block is two
 // barriers: with each wave converting the codes for its own rows the conversion took longer than both products.
 
 constexpr int kTileRows = 128, kSmallRows = 64, kTileKeys = 64;
@@ -668,10 +668,11 @@ __device__ __forceinline__ void attn4_tile(const Attn4Args &a, int block, char *
 // in their registers; V's go as bf16 through a private piece of LDS for the transposing read. The next block's
 // loads are issued before this block is used; the four partial results are joined at the end.
 //
-// 64 tokens of 20 heads of 128 in five groups over 253 thousand keys (172 MB): 51 us, 3.4 TB/s; with the loads alone 47, so
-// that it is the loads' latency with two blocks a wave on their way. Three blocks, blocks of 64 keys, loads past the
-// caches or more waves a CU: no gain. One token over 777 keys: 6.3 us, of which finding the item and the page are
-// about three, and 3.7 for the joining.
+// 64 tokens of 20 heads of 128 in five groups over 253 thousand keys (172 MB): 51 us, 3.4 TB/s, with nothing but its loads
+// 47; pages of 16 tokens, whose numbers a wave has to read four times as often, take no longer (49). Part of it is the end,
+// where not all CUs have work: 1140 workgroups of one length where 768 fit at once. Three blocks on their way, blocks of
+// 64 keys, loads past the caches or more waves a CU: no gain. One token over 777 keys: 6.2 us, of which finding
+// the item and the page are about three, and 3.7 for the joining.
 
 constexpr int kFewRows = 16, kFewKeys = 32, kFewWaves = 4;
 
@@ -1106,7 +1107,9 @@ Attn4Plan attn4_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
     // Rows of a tile, by the mean rows of such a sequence (idle ones of the table count, too): up to 16, one small tile
     // each; up to 64, one of 64. Longer ones take tiles of 128, or of 64 where those would not fill the CUs and there are no
     // long caches to cut instead (capacity of twice the call's tokens or more; 7B prompts of 813 tokens behind 4096 keys:
-    // 86 us cut, 137 uncut with 64 rows; packed 2B prompts of 2048 tokens 49 and 39).
+    // 86 us cut, 137 uncut with 64 rows; packed 2B prompts of 2048 tokens 49 and 39). Lengths are on the device, so that the
+    // capacity, what a row of the table can hold, is what there is to go by: new prompts in a wide table count as cached
+    // (those packed ones in a table of 128 pages of 64: 52 us; one prompt of 2048 82 where a table cut to size takes 66).
     const bool few = rows <= kFewRows * seqs;
     const int64_t tiles128 = rows / kTileRows + seqs;
     const bool fills = tiles128 * Hkv >= 512, cached = most_keys > 2 * T;

@@ -115,8 +115,8 @@ __device__ inline int piece_place(int row) { return (row >> 1 & 2) ^ (row >> 3 &
 // registers, RING blocks ahead. So do tokens where weights are what there is to read (DIRECT; with RING == 2 more
 // workgroups fit a CU); in few workgroups they take a direct way into a piece of LDS of the wave's own, since a lane's
 // 16 bytes of 16 rows cost the load path more than 64 bytes side by side do.
-// Bound by the weights' bytes: 1 x 32000 x 2560 in 14 us (5.8 TB/s, more than from memory alone: part of the 82 MB is still
-// in the last cache from the call before), 40 x 28672 x 8192 50.6 us (4.7 TB/s; a large copy 5.2).
+// Bound by the weights' bytes: 1 x 32000 x 2560 in 12.1 us (6.8 TB/s, more than from memory alone: part of the 82 MB is
+// still in the last cache from the call before), 40 x 28672 x 8192 48.2 us (4.9 TB/s; a large copy 5.2).
 
 template <typename TY, int RT, int MT, int RING, int W, bool DIRECT>
 __global__ __launch_bounds__(64 * W) void k_int8_few(Int8Args a)
@@ -273,9 +273,10 @@ __global__ __launch_bounds__(64 * W) void k_int8_few(Int8Args a)
 // A step is two halves of the wave's tokens. While the first one's MFMAs run, the second's operands are read; then one
 // barrier publishes the next stage and frees this one for the load four steps ahead; while the second half's MFMAs run,
 // the next step's weights and first tokens are read.
-// Bound by the matrix cores at the clock that the power leaves them: 4096 x 28672 x 8192 in 620 to 720 us (2.7 to 3.1 POP/s
-// where the library's product has 2.2), at 1.6 to 1.9 GHz. Steps of 128 k, matrix instructions of 32 x 32 x 32, four
-// waves of 128 x 128 or a ring of eight stages: slower or no gain.
+// Bound by the matrix cores at the clock that the power leaves them: 4096 x 28672 x 8192 in 727 us (2.65 POP/s where the
+// library's product has 2.17; median of 40 under the tracer 765, least 730; in bursts of five, which the power limit
+// hardly reaches, 622), at 1.6 to 1.9 GHz. Steps of 128 k, matrix instructions of 32 x 32 x 32, four waves of
+// 128 x 128 or a ring of eight stages: slower or no gain.
 
 
 // The same for all waves of the workgroup.

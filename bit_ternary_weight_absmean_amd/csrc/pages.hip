@@ -67,7 +67,7 @@ __device__ inline int block_scan(int v, int *lds, int &total)
 }
 
 // Copies one piece of page src to page dst: four pieces of 16 bytes for each of 256 threads, all read before the first is
-// written (through LDS, where the compiler put an array of them: 62 us for a compaction that takes 49).
+// written. (Not an array: the compiler put one into LDS, and a compaction took a quarter longer.)
 __device__ inline void copy_piece(const PagesArgs &a, int64_t src, int64_t dst, int layer, int piece)
 {
     const char *from = a.pool + layer * a.layer_stride + src * a.page_bytes;
@@ -113,7 +113,11 @@ unsigned copy_grid(const PagesArgs &a, int64_t count)
 // (each reading of memory behind another costs about 0.7 us here: first lengths, then the last pages' numbers and the
 // counts from `first` on, then the last pages' counts); the second launch copies pages. For more sequences, or more
 // than 2048 tokens, that launch also fills in the tables or the places. 8 sequences and 256 with a token each and 300 new
-// ones: 6.8 us and 2 to 3 for the copies. (The way for more sequences costs 1.5 us more for 8, 3 for 256.)
+// ones: 7.0 and 7.6 us, and 2.3 and 4.3 for the copies. (The way for more sequences costs 1.5 us more for 8, 3 for 256.)
+//
+// Who needs a copy of a shared last page is told by the counts before the call, for all sequences at once: each of its
+// holders that grows gets one, also where none stays, and the page is free after the call. To leave it to one of them, the
+// holders of every page would have to be put in order behind those that are refused: a chain more, to save one copy.
 //
 // Workspace: [0] pages handed out, [1] pages copied, then per sequence the end of its demand (inclusive sum) and
 // the page slot it starts at, then the list of copied pages (from, to), then the free pages.
@@ -424,8 +428,8 @@ __global__ __launch_bounds__(256) void k_pages_grow(PagesArgs a, int tables, int
 // Counts go up first, for all pages that are taken, and down only then, for all that are given up. Tables of up to kCells
 // entries in one launch of one workgroup, with a barrier between the two; larger ones in two launches of one workgroup
 // per sequence, the first of which also keeps the rows as they will be in the workspace (the new lengths, the new rows).
-// Bound by the chain parent, length, entry, count: 8 sequences of up to 9 pages 6.1 us (two launches: 3.1 and 3.4, and a beam
-// step called from the host 21.3 us instead of 18), 256 of up to 64 pages 2.0 and 3.4.
+// Bound by the chain parent, length, entry, count: 8 sequences of up to 9 pages 5.9 us (two launches: 3.1 and 3.4, and a beam
+// step called from the host 21.3 us instead of 18), 256 of up to 64 pages 2.1 and 3.8.
 
 constexpr int kCells = 8 * kPlan;
 
@@ -542,8 +546,9 @@ __global__ __launch_bounds__(256) void k_fork_give(PagesArgs a)
 // With L pages in use, the k-th one at or past L goes to the k-th free one below L. A page in use has a rank (how
 // many are in use before it), a free page i has i - rank free ones before it: segments of pages need no more than
 // the counts of those before them. The pages that move are those with the last ranks. Up to eight segments are listed in one
-// launch, every workgroup going over all counts (4096 pages: 6.3 us; with a launch that counts 2 to 3 more); bound by the
-// copies: 64 sequences of up to 40 pages in four layers of 43520 bytes 39 us (237 MB read and written, 5.6 TB/s).
+// launch, every workgroup going over all counts (4096 pages: 6.1 us; with a launch that counts 2 to 3 more); bound by the
+// copies: 64 sequences of up to 40 pages in four layers of 43520 bytes 39 us (237 MB read and written; 6.0 TB/s, more
+// than a large copy's 5.2 since part of the pool is in the last cache from the call before).
 // Workspace: [0] L, [1] moves, then counts of the segments, then for each free page below L (in order) its index, for
 // each rank its page (those that move), for each page its rank (those that move; -1).
 

@@ -606,7 +606,8 @@ size_t bt_pages_workspace_bytes(int64_t seqs, int64_t max_pages, int64_t pages);
 /*
  * bt_pages_grow -- room for new tokens: sequence b gains n = q_start[b+1] - q_start[b] of them (q_start [seqs + 1]
  * int32, not falling, inside [0, tokens]). It needs pages for length + n tokens, and one more where its last page is
- * partly filled and held more than once: it then gets a copy of that page of its own (in all layers).
+ * partly filled and was held more than once before the call: it then gets a copy of that page of its own (in all layers), as
+ * does every other one of its holders that grows; where all do, the page itself is free afterwards.
  * Free pages go, lowest index first, to the sequences in order; within one, its copy comes first. A sequence whose
  * pages are not there any more, or that max_pages has no room for, is refused: it stays as it is. The pages asked for
  * by a refused sequence stay free, but those behind it that need pages are refused with it.
@@ -653,7 +654,8 @@ bt_status bt_pages_copy(const bt_pages_shape *shape, void *pool, const int32_t *
  *   Y         [M, N] of y_type (BT_F32, BT_BF16 or BT_F16), acc [M, N] int32; either may be NULL, not both. Aligned to
  *             their element.
  *   workspace bt_int8_workspace_bytes(M, N, K) bytes of device scratch, 256-byte aligned, or NULL when that is 0;
- *             contents on entry are ignored. Calls sharing one must not overlap.
+ *             contents on entry are ignored. Calls sharing one must not overlap. (No present kernel needs any: it is 0 for
+ *             all sizes.)
  * Codes may be -128 to 127; acc is exact while K * max|X| * max|W| < 2^31 (always, with one side in +-127). K == 0
  * gives acc 0.
  */
