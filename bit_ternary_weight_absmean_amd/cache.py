@@ -131,6 +131,9 @@ def attention4_workspace(q: torch.Tensor, cache: Cache4, table: torch.Tensor) ->
 def attention4_plan(tokens: int, seqs: int, heads: int, kv_heads: int, head_dim: int, max_pages: int, page_tokens: int,
                     dtype: torch.dtype = torch.bfloat16, out_dtype: torch.dtype | None = None) -> str:
     """bt_attention4_plan: the kernel instances that such an attention4 call would launch (host-only query)."""
+    for t in (dtype, out_dtype or dtype):
+        if t not in _TYPES:
+            raise TypeError(f"dtype and out_dtype must be of {[str(a) for a in _TYPES]}, got {t}")
     shape = _ATTENTION4_SHAPE.pack(tokens, seqs, max_pages, max_pages, 0, page_tokens, heads, kv_heads, head_dim,
                                    _TYPES[dtype], _TYPES[out_dtype or dtype], True, 1.0, 0, 0, 0, 0)
     buf = ctypes.create_string_buffer(128)

@@ -45,6 +45,9 @@ def test_plan_query():
         bt.attention4_plan(1, 1, 4, 2, 64, 10, 16, torch.float32)
     with pytest.raises(bt.BTError):
         bt.attention4_plan(1, 1, 4, 2, 64, 10, 16, torch.float16, torch.bfloat16)
+    for bad in ((torch.float64,), (torch.bfloat16, torch.int8)):
+        with pytest.raises(TypeError, match="out_dtype must be"):
+            bt.attention4_plan(1, 1, 4, 2, 64, 10, 16, *bad)
     # agrees with the workspace: joined where there is one
     for shape in ((1, 1, 4, 2, 64, 32, 16), (1, 1, 4, 2, 64, 1000, 16), (300, 300, 4, 2, 64, 40, 64), (2048, 1, 20, 5, 128, 512, 64)):
         assert ("join" in bt.attention4_plan(*shape)) == (bt.attention4_workspace_bytes(*shape) > 0)
