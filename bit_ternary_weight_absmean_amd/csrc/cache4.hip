@@ -10,7 +10,7 @@
 // each token's row. 16384 tokens of eight key heads of 128, bf16 (85 MB): 19.2 us written, 24.3 read (4.4 and 3.5 TB/s; a
 // large copy on this card: 5.2); in random places, where each group's 16 bytes and one are lines of their own, 30.8 and
 // 31.4. With four lanes to a group and 64-bit index arithmetic 28.6 and 35.7 in random places. Below a few thousand tokens
-// the launch is what counts (37 tokens: 3.4 us under the tracer).
+// the launch is what counts (37 tokens: 3.5 us under the tracer).
 #include "bt_internal.h"
 #include "cache4.h"
 #include "wave.h"
